@@ -9,7 +9,7 @@ cmp_ratio 4, K2 = 512 top-k indices, fp8 e4m3 KV with per-64 fp32 scales,
 128-token pages). Metric: query tokens per second.
 
   python bench.py [--gpus N --steps K --warmup W] [--impl qsfm|reference]
-                  [--workload I] [--kv-format fp8_fp32_scales|packed640|bf16]
+                  [--workload I] [--kv-format fp8_fp32_scales|packed640|packed384|bf16]
                   [--n1 64|128] [--quick]
 
 --kv-format and --n1 time the same workload with another KV row format or
@@ -49,7 +49,7 @@ UNIT = "query-tokens/s"
 FLUSH_BYTES = 512 << 20  # > 129 MB L2
 # bytes one KV row takes in each row format: 512 fp8 + 8 fp32 scales; a
 # packed 640-byte row; 512 bf16
-KV_ROW_BYTES = {"fp8_fp32_scales": 512 + 8 * 4, "packed640": 640, "bf16": 1024}
+KV_ROW_BYTES = {"fp8_fp32_scales": 512 + 8 * 4, "packed640": 640, "packed384": 384, "bf16": 1024}
 FLOPS_PER_ROW_HEAD = 4 * 512  # QK^T + PV per attended (token, row) and head
 KERNEL_SRCS = [os.path.join(ROOT, "compressed_mla_attention_gb300", "csrc", f)
                for f in ("qsfm_attention.cu", "qsfm_device.cuh")]

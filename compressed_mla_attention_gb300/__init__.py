@@ -11,6 +11,7 @@ is missing, importing the op functions raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -29,7 +30,10 @@ LAYOUT_TND = 1
 KV_FP8_FP32_SCALES = 0
 KV_PACKED640 = 1
 KV_BF16 = 2
+KV_PACKED384 = 3
 PACKED_ROW_BYTES = 640
+PACKED384_ROW_BYTES = 384
+ELEM_TYPE = {"torch.bfloat16": 0, "torch.float16": 1, "torch.float32": 2}
 
 STATUS = {
     0: "QSFM_OK",
@@ -48,9 +52,13 @@ FAULT_METADATA = 0x10
 FAULT_TIMEOUT = 0x20
 FAULT_RANGE = 0x40
 FAULT_KV_ROW = 0x80
+FAULT_BLOCK_POOL = 0x100
+FAULT_SLOT = 0x200
+FAULT_POSITION = 0x400
 LAYOUT_KV = {"PA_BBND": 0, "BSND": 1, "TND": 2}
 
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _ptr = ctypes.c_void_p
 
 
@@ -93,6 +101,30 @@ class IndexerParams(ctypes.Structure):
     ]
 
 
+class NormRopeParams(ctypes.Structure):
+    """Mirror of ``qsfm_norm_rope_params`` (include/qsfm.h); field order must match."""
+
+    _fields_ = [
+        ("tokens", _i32), ("heads", _i32), ("dim", _i32), ("in_type", _i32), ("weights_bf16", _i32),
+        ("norm_q", _i32), ("norm_kv", _i32), ("rope_dim", _i32), ("rope_offset", _i32), ("interleaved", _i32),
+        ("max_positions", _i32), ("kv_layout", _i32), ("num_blocks", _i32), ("eps", ctypes.c_float),
+        ("q_token_stride", _i64), ("q_head_stride", _i64), ("kv_token_stride", _i64),
+        ("q", _ptr), ("kv", _ptr), ("q_weight", _ptr), ("kv_weight", _ptr), ("cos_sin", _ptr), ("positions", _ptr),
+        ("slot_map", _ptr), ("q_out", _ptr), ("kv_cache", _ptr), ("kv_scale", _ptr), ("kv_out", _ptr),
+    ]
+
+
+class BlockTableParams(ctypes.Structure):
+    """Mirror of ``qsfm_block_table_params`` (include/qsfm.h); field order must match."""
+
+    _fields_ = [
+        ("batch", _i32), ("max_blocks", _i32), ("num_blocks", _i32), ("free_capacity", _i32), ("max_rows", _i32),
+        ("cmp_ratio", _i32), ("block_size", _i32),
+        ("block_table", _ptr), ("prev_lens", _ptr), ("lens", _ptr), ("free_list", _ptr), ("free_count", _ptr),
+        ("free_count_out", _ptr), ("slot_map", _ptr), ("positions", _ptr), ("cu_rows", _ptr), ("residual", _ptr),
+    ]
+
+
 class QsfmError(RuntimeError):
     def __init__(self, fn: str, code: int, cuda_error: str = ""):
         detail = f" ({cuda_error})" if cuda_error else ""
@@ -121,6 +153,10 @@ EXPORTS = {
     "qsfm_lightning_indexer_workspace_size": (_i32, [ctypes.POINTER(IndexerParams),
                                                      ctypes.POINTER(ctypes.c_size_t)]),
     "qsfm_lightning_indexer": (_i32, [ctypes.POINTER(IndexerParams), _ptr, ctypes.c_size_t, _ptr]),
+    "qsfm_norm_rope_params_init": (None, [ctypes.POINTER(NormRopeParams)]),
+    "qsfm_norm_rope_store": (_i32, [ctypes.POINTER(NormRopeParams), _ptr]),
+    "qsfm_block_table_params_init": (None, [ctypes.POINTER(BlockTableParams)]),
+    "qsfm_update_block_tables": (_i32, [ctypes.POINTER(BlockTableParams), _ptr]),
 }
 
 
@@ -167,6 +203,14 @@ def _stream_ptr(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _row_format(kv) -> int:
+    """The qsfm_kv_layout of a KV tensor, from its type and row width."""
+    if str(kv.dtype) == "torch.bfloat16":
+        return KV_BF16
+    return {PACKED_ROW_BYTES: KV_PACKED640, PACKED384_ROW_BYTES: KV_PACKED384}.get(int(kv.shape[-1]),
+                                                                                  KV_FP8_FP32_SCALES)
+
+
 def make_params(
     *,
     q,
@@ -208,8 +252,10 @@ def make_params(
     q / attn_out: BSND [B, S1, N1, 512] or TND [T1, N1, 512] bf16, N1 = 64 or 128.
     Paged KV (layout_kv "PA_BBND"): [blocks, 128, 1, 512] uint8 (fp8 e4m3fn
     bytes) with fp32 scales [blocks, 128, 1, 8], or packed [blocks, 128, 1,
-    640] uint8 rows (bf16 rope, e4m3fn nope, e8m0 scales; scales None), or
-    bf16 rows [blocks, 128, 1, 512] (scales None); block tables int32 [B,
+    640] uint8 rows (bf16 rope, e4m3fn nope, e8m0 scales; scales None), 4-bit
+    [blocks, 128, 1, 384] uint8 rows (bf16 rope, e2m1 nope, e4m3fn scales, an
+    e8m0 row exponent; scales None), or bf16 rows [blocks, 128, 1, 512]
+    (scales None); block tables int32 [B,
     width]. Non-paged KV: layout_kv "BSND" ([B, S, 1, row], q BSND) or "TND"
     ([T, 1, row], q TND, cu_seqlens_ori_kv / cu_seqlens_cmp_kv int32 [B+1]),
     no block tables. ori_sparse_indices int32 [T, 1, K1] (or BSND
@@ -239,12 +285,7 @@ def make_params(
     # bf16 rows, packed 640-byte rows (bf16 rope, e4m3 nope, e8m0 scales) or fp8 rows + fp32 scales
     if cmp_kv is not None and (cmp_kv.dtype != ori_kv.dtype or cmp_kv.shape[-1] != ori_kv.shape[-1]):
         raise ValueError("ori_kv and cmp_kv must have the same row format")
-    if str(ori_kv.dtype) == "torch.bfloat16":
-        p.kv_layout = KV_BF16
-    elif int(ori_kv.shape[-1]) == PACKED_ROW_BYTES:
-        p.kv_layout = KV_PACKED640
-    else:
-        p.kv_layout = KV_FP8_FP32_SCALES
+    p.kv_layout = _row_format(ori_kv)
     if layout_kv not in LAYOUT_KV:
         raise ValueError(layout_kv)
     p.layout_kv = LAYOUT_KV[layout_kv]
@@ -580,3 +621,246 @@ def lightning_indexer(
     _check("qsfm_lightning_indexer", lib().qsfm_lightning_indexer(
         ctypes.byref(p), _dptr(workspace), workspace.numel() * workspace.element_size(), _stream_ptr(stream)))
     return out, (values if return_value else None)
+
+
+def _one_device(tensors: dict):
+    """The CUDA device all given tensors are on (None entries are absent)."""
+    given = {k: t for k, t in tensors.items() if t is not None}
+    dev = next(iter(given.values())).device
+    for k, t in given.items():
+        if t.device.type != "cuda" or t.device != dev:
+            raise ValueError(f"{k} is on {t.device}: every tensor must be on one CUDA device")
+    return dev
+
+
+def _expect(name: str, t, dtypes, shape=None):
+    """Type, shape and contiguity of an argument (a None in shape: any length)."""
+    if t is None:
+        return
+    if str(t.dtype) not in dtypes:
+        raise ValueError(f"{name} has type {t.dtype}; expected {' or '.join(dtypes)}")
+    if shape is not None and (t.dim() != len(shape) or
+                              any(n is not None and int(m) != int(n) for m, n in zip(t.shape, shape))):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _on(stream, device):
+    """Context in which torch allocates and fills for `stream`."""
+    import torch
+
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+class _Launch:
+    """A parameter block with its device: calls run on that device, and the
+    tensors it points to live as long as it does."""
+
+    def __init__(self, params, device, tensors):
+        self.params, self.device, self.tensors = params, device, tensors
+        self.ref = ctypes.byref(params)
+
+    def call(self, fn: str, stream):
+        import torch
+
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        at = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        if self.device.index == torch.cuda.current_device():
+            _check(fn, getattr(lib(), fn)(self.ref, at))
+        else:
+            with torch.cuda.device(self.device):
+                _check(fn, getattr(lib(), fn)(self.ref, at))
+
+
+_I32 = ("torch.int32",)
+_F32 = ("torch.float32",)
+_BF16 = ("torch.bfloat16",)
+
+
+def make_norm_rope_params(
+    *,
+    q=None,
+    q_out=None,
+    kv=None,
+    kv_cache=None,
+    kv_scale=None,
+    kv_out=None,
+    slot_map=None,
+    positions=None,
+    cos_sin=None,
+    q_weight=None,
+    kv_weight=None,
+    eps: float = 1e-6,
+    rope_offset: int = 0,
+    interleaved: bool = True,
+    norm_q: bool = True,
+    norm_kv: bool = True,
+) -> _Launch:
+    """A parameter block for norm_rope() (arguments as norm_rope_store()), to
+    be made once for fixed buffers and launched every step."""
+    tensors = dict(q=q, q_out=q_out, kv=kv, kv_cache=kv_cache, kv_scale=kv_scale, kv_out=kv_out, slot_map=slot_map,
+                   positions=positions, cos_sin=cos_sin, q_weight=q_weight, kv_weight=kv_weight)
+    if q is None and kv is None:
+        raise ValueError("norm_rope needs q or kv")
+    x = q if q is not None else kv
+    T = int(x.shape[0])
+    if str(x.dtype) not in ELEM_TYPE or (q is not None and kv is not None and q.dtype != kv.dtype):
+        raise ValueError("q and kv must have one type: bfloat16, float16 or float32")
+    if q is not None and (q.dim() != 3 or int(q.shape[2]) != HEAD_DIM or q.stride(2) != 1):
+        raise ValueError(f"q must be [T, N, {HEAD_DIM}] with contiguous rows")
+    if kv is not None:
+        if kv.dim() == 3 and int(kv.shape[1]) == 1:
+            kv = kv[:, 0]
+        if kv.dim() != 2 or tuple(kv.shape) != (T, HEAD_DIM) or kv.stride(1) != 1:
+            raise ValueError(f"kv must be [T, {HEAD_DIM}] (or [T, 1, {HEAD_DIM}]) with contiguous rows")
+    if q is not None:
+        _expect("q_out", q_out, _BF16, tuple(q.shape))
+    _expect("kv_out", kv_out, _BF16, (T, HEAD_DIM))
+    _expect("positions", positions, _I32, (T,))
+    _expect("slot_map", slot_map, _I32, (T,))
+    _expect("cos_sin", cos_sin, _F32, (None, None))
+    weights = [w for w in (q_weight, kv_weight) if w is not None]
+    for name, w in (("q_weight", q_weight), ("kv_weight", kv_weight)):
+        _expect(name, w, _F32 + _BF16, (HEAD_DIM,))
+    if len({w.dtype for w in weights}) > 1:
+        raise ValueError("q_weight and kv_weight must have one type")
+    dev = _one_device(tensors)
+    p = NormRopeParams()
+    lib().qsfm_norm_rope_params_init(ctypes.byref(p))
+    p.tokens, p.heads = T, int(q.shape[1]) if q is not None else 0
+    p.in_type, p.weights_bf16 = ELEM_TYPE[str(x.dtype)], int(bool(weights) and str(weights[0].dtype) in _BF16)
+    p.norm_q, p.norm_kv, p.eps = int(bool(norm_q)), int(bool(norm_kv)), float(eps)
+    p.rope_offset, p.interleaved = int(rope_offset), int(bool(interleaved))
+    if cos_sin is not None:
+        p.max_positions, p.rope_dim = int(cos_sin.shape[0]), int(cos_sin.shape[1])
+    if kv_cache is not None:
+        p.kv_layout = _row_format(kv_cache)
+        width = {KV_FP8_FP32_SCALES: HEAD_DIM, KV_PACKED640: PACKED_ROW_BYTES, KV_BF16: HEAD_DIM,
+                 KV_PACKED384: PACKED384_ROW_BYTES}[p.kv_layout]
+        types = ("torch.bfloat16",) if p.kv_layout == KV_BF16 else ("torch.uint8", "torch.float8_e4m3fn")
+        _expect("kv_cache", kv_cache, types, (None, BLOCK_SIZE, 1, width))
+        p.num_blocks = int(kv_cache.shape[0])
+        _expect("kv_scale", kv_scale, _F32, (p.num_blocks, BLOCK_SIZE, 1, HEAD_DIM // 64))
+    if q is not None:
+        p.q, p.q_out = q.data_ptr(), _dptr(q_out)
+        p.q_token_stride, p.q_head_stride = q.stride(0), q.stride(1)
+    if kv is not None:
+        p.kv, p.kv_token_stride = kv.data_ptr(), kv.stride(0)
+    p.q_weight, p.kv_weight, p.cos_sin = _dptr(q_weight), _dptr(kv_weight), _dptr(cos_sin)
+    p.positions, p.slot_map = _dptr(positions), _dptr(slot_map)
+    p.kv_cache, p.kv_scale, p.kv_out = _dptr(kv_cache), _dptr(kv_scale), _dptr(kv_out)
+    return _Launch(p, dev, tensors)
+
+
+def norm_rope(launch: _Launch, stream=None) -> None:
+    """qsfm_norm_rope_store() with a block of make_norm_rope_params()."""
+    launch.call("qsfm_norm_rope_store", stream)
+
+
+def norm_rope_store(q=None, kv=None, *, stream=None, **kwargs):
+    """Norm of the query rows and the latent key row of each token with the
+    position rotation in the same pass, and the store of the key row into the
+    paged cache (qsfm_norm_rope_store).
+
+    q [T, N, 512] and kv [T, 512] bf16, fp16 or fp32, each optional, with any
+    strides of tokens and heads that keep rows 16-byte aligned (slices of one
+    projection's output, for instance). q_out bf16 [T, N, 512] is allocated
+    when not given (q itself for an update in place). kv_cache in any row
+    format of quant_sparse_flash_mla (with kv_scale for fp8 rows) takes the
+    key rows at slot_map int32 [T] (-1: not stored); kv_out bf16 [T, 512]
+    takes the values of the stored rows. positions int32 [T] (-1: a padded
+    token, left alone) index cos_sin fp32 [P, rope_dim] (cosines, then sines);
+    q_weight / kv_weight [512] fp32 or bf16; interleaved rotates elements
+    (2i, 2i + 1) from rope_offset on, else (i, i + rope_dim / 2). norm_q /
+    norm_kv False leave the norm out. Returns q_out (None without q).
+    """
+    import torch
+
+    if q is not None and kwargs.get("q_out") is None:
+        # the rows of padded tokens are left as they are: zeros in a new tensor
+        with _on(stream, q.device):
+            kwargs["q_out"] = torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+    norm_rope(make_norm_rope_params(q=q, kv=kv, **kwargs), stream)
+    return kwargs.get("q_out")
+
+
+def make_block_table_params(
+    *,
+    block_table,
+    prev_lens,
+    lens,
+    free_list,
+    free_count,
+    slot_map,
+    free_count_out=None,
+    positions=None,
+    cu_rows=None,
+    residual=None,
+    cmp_ratio: int = 1,
+    num_blocks: Optional[int] = None,
+) -> _Launch:
+    """A parameter block for block_tables() (arguments as
+    update_block_tables()), to be made once for fixed buffers."""
+    tensors = dict(block_table=block_table, prev_lens=prev_lens, lens=lens, free_list=free_list,
+                   free_count=free_count, slot_map=slot_map, free_count_out=free_count_out, positions=positions,
+                   cu_rows=cu_rows, residual=residual)
+    B = int(lens.shape[0])
+    _expect("block_table", block_table, _I32, (B, None))
+    for name in ("prev_lens", "lens", "residual"):
+        _expect(name, tensors[name], _I32, (B,))
+    _expect("free_list", free_list, _I32, (None,))
+    _expect("free_count", free_count, _I32, (1,))
+    _expect("free_count_out", free_count_out, _I32, (1,))
+    _expect("slot_map", slot_map, _I32, (None,))
+    _expect("positions", positions, _I32, tuple(slot_map.shape))
+    _expect("cu_rows", cu_rows, _I32, (B + 1,))
+    dev = _one_device(tensors)
+    p = BlockTableParams()
+    lib().qsfm_block_table_params_init(ctypes.byref(p))
+    p.batch, p.max_blocks = B, int(block_table.shape[1])
+    p.free_capacity, p.max_rows, p.cmp_ratio = int(free_list.shape[0]), int(slot_map.shape[0]), int(cmp_ratio)
+    p.num_blocks = int(free_list.shape[0]) if num_blocks is None else int(num_blocks)
+    for name, t in tensors.items():
+        setattr(p, name, _dptr(t))
+    return _Launch(p, dev, tensors)
+
+
+def block_tables(launch: _Launch, stream=None) -> None:
+    """qsfm_update_block_tables() with a block of make_block_table_params()."""
+    launch.call("qsfm_update_block_tables", stream)
+
+
+def update_block_tables(block_table, prev_lens, lens, free_list, free_count, *, max_rows: Optional[int] = None,
+                        slot_map=None, stream=None, **kwargs):
+    """Block tables, slots and positions of a step's new cache rows from the
+    requests' lengths, on the GPU (qsfm_update_block_tables).
+
+    block_table int32 [B, W], free_list int32 [P] (block ids, a stack of which
+    the first free_count int32 [1] entries are free) are updated in place:
+    requests that shrink from prev_lens[b] to lens[b] tokens (0: ended) give
+    blocks back, then requests that grow take them, in order. With cmp_ratio
+    r, floor(len / r) rows count (compressed rows). free_count_out: the new
+    count goes there instead. slot_map int32 [max_rows] (allocated when not
+    given, with positions) gets the pool row of every new row and positions
+    its token position, -1 behind the last; cu_rows int32 [B + 1] the rows'
+    prefix sums; residual int32 [B] the tokens behind the last row. num_blocks
+    bounds the block ids (default: P). Returns (slot_map, positions).
+    """
+    import torch
+
+    if slot_map is None:
+        if max_rows is None:
+            raise ValueError("update_block_tables needs slot_map or max_rows")
+        with _on(stream, lens.device):
+            slot_map = torch.empty(int(max_rows), dtype=torch.int32, device=lens.device)
+            if kwargs.get("positions") is None:
+                kwargs["positions"] = torch.empty_like(slot_map)
+    block_tables(make_block_table_params(block_table=block_table, prev_lens=prev_lens, lens=lens, free_list=free_list,
+                                         free_count=free_count, slot_map=slot_map, **kwargs), stream)
+    return slot_map, kwargs.get("positions")

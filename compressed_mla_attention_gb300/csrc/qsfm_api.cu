@@ -105,7 +105,7 @@ qsfm_status validate(const qsfm_params* pp, bool need_outputs) {
   if (p.k2 < 0) return QSFM_ERR_INVALID_ARG;
   if (p.k2 > kMaxK2) return QSFM_ERR_UNSUPPORTED;
   if (p.kv_layout != QSFM_KV_FP8_FP32_SCALES && p.kv_layout != QSFM_KV_PACKED640 &&
-      p.kv_layout != QSFM_KV_BF16)
+      p.kv_layout != QSFM_KV_BF16 && p.kv_layout != QSFM_KV_PACKED384)
     return QSFM_ERR_INVALID_ARG;
   const bool no_scales = p.kv_layout != QSFM_KV_FP8_FP32_SCALES;
   // packed rows carry their scales and bf16 rows need none: a separate scale
@@ -279,6 +279,124 @@ qsfm_status check_indexer(const qsfm_indexer_params* pp, long long* T) {
   return QSFM_OK;
 }
 
+// Whether two ranges of device memory have a byte in common.
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+  if (a == nullptr || b == nullptr || na <= 0 || nb <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + uintptr_t(nb) && y < x + uintptr_t(na);
+}
+
+constexpr long long kMaxNormRows = 1ll << 30;
+
+// Checks of qsfm_norm_rope_store().
+qsfm_status check_norm_rope(const qsfm_norm_rope_params* pp) {
+  if (pp == nullptr) return QSFM_ERR_INVALID_ARG;
+  const qsfm_norm_rope_params& p = *pp;
+  if (p.tokens < 0 || p.heads < 0 || p.dim <= 0) return QSFM_ERR_INVALID_ARG;
+  if (p.dim != QSFM_HEAD_DIM) return QSFM_ERR_UNSUPPORTED;
+  if (p.in_type != QSFM_BF16 && p.in_type != QSFM_F16 && p.in_type != QSFM_F32) return QSFM_ERR_INVALID_ARG;
+  if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return QSFM_ERR_INVALID_ARG;
+  if ((long long)p.tokens * (p.heads + 1ll) > kMaxNormRows) return QSFM_ERR_UNSUPPORTED;
+  if (p.q == nullptr && p.kv == nullptr) return QSFM_ERR_INVALID_ARG;
+  if ((p.q != nullptr) != (p.heads > 0) || (p.q != nullptr) != (p.q_out != nullptr)) return QSFM_ERR_INVALID_ARG;
+  if (p.q == nullptr && p.q_weight != nullptr) return QSFM_ERR_INVALID_ARG;
+  if (p.kv == nullptr && (p.kv_cache != nullptr || p.kv_out != nullptr || p.kv_weight != nullptr))
+    return QSFM_ERR_INVALID_ARG;
+  if (p.kv != nullptr && p.kv_cache == nullptr && p.kv_out == nullptr) return QSFM_ERR_INVALID_ARG;
+  // the rotation
+  if (p.rope_dim < 0 || p.rope_offset < 0 || p.rope_dim + (long long)p.rope_offset > QSFM_HEAD_DIM)
+    return QSFM_ERR_INVALID_ARG;
+  if (p.rope_dim != 0) {
+    if (p.rope_dim != 32 && p.rope_dim != 64 && p.rope_dim != 128 && p.rope_dim != 256) return QSFM_ERR_UNSUPPORTED;
+    if (p.rope_offset % p.rope_dim != 0) return QSFM_ERR_UNSUPPORTED;
+    if (p.cos_sin == nullptr || p.positions == nullptr || p.max_positions < 1) return QSFM_ERR_INVALID_ARG;
+  } else if (p.cos_sin != nullptr) {
+    return QSFM_ERR_INVALID_ARG;
+  }
+  // the cache
+  if (p.kv_cache != nullptr) {
+    if (p.kv_layout != QSFM_KV_FP8_FP32_SCALES && p.kv_layout != QSFM_KV_PACKED640 && p.kv_layout != QSFM_KV_BF16 &&
+        p.kv_layout != QSFM_KV_PACKED384)
+      return QSFM_ERR_INVALID_ARG;
+    if (p.slot_map == nullptr || p.num_blocks < 1) return QSFM_ERR_INVALID_ARG;
+    if ((p.kv_layout == QSFM_KV_FP8_FP32_SCALES) != (p.kv_scale != nullptr)) return QSFM_ERR_INVALID_ARG;
+    if ((long long)p.num_blocks * QSFM_BLOCK_SIZE > kMaxPoolRows) return QSFM_ERR_UNSUPPORTED;
+  } else if (p.slot_map != nullptr || p.kv_scale != nullptr) {
+    return QSFM_ERR_INVALID_ARG;
+  }
+  // 16-byte vector accesses to the rows, the weights and the table
+  const long long size = p.in_type == QSFM_F32 ? 4 : 2;
+  if (p.q != nullptr && ((p.q_token_stride * size) % 16 != 0 || (p.q_head_stride * size) % 16 != 0 ||
+                         p.q_token_stride < 0 || p.q_head_stride < 0))
+    return QSFM_ERR_INVALID_ARG;
+  if (p.kv != nullptr && ((p.kv_token_stride * size) % 16 != 0 || p.kv_token_stride < 0)) return QSFM_ERR_INVALID_ARG;
+  const void* vectors[] = {p.q, p.kv, p.q_out, p.kv_cache, p.kv_out, p.q_weight, p.kv_weight, p.cos_sin};
+  for (const void* v : vectors)
+    if (!aligned(v, 16)) return QSFM_ERR_INVALID_ARG;
+  if (!aligned(p.positions, 4) || !aligned(p.slot_map, 4) || !aligned(p.kv_scale, 4)) return QSFM_ERR_INVALID_ARG;
+  if (p.tokens == 0) return QSFM_OK;
+  // rows are written while others are still read: no output overlaps an input
+  const long long T = p.tokens;
+  const long long q_bytes = ((T - 1) * p.q_token_stride + (p.heads - 1ll) * p.q_head_stride + QSFM_HEAD_DIM) * size;
+  const long long kv_bytes = ((T - 1) * p.kv_token_stride + QSFM_HEAD_DIM) * size;
+  const long long q_out_bytes = T * p.heads * QSFM_HEAD_DIM * 2, kv_out_bytes = T * QSFM_HEAD_DIM * 2;
+  const bool in_place = p.q == p.q_out && p.in_type == QSFM_BF16 && (p.heads <= 1 || p.q_head_stride == QSFM_HEAD_DIM) &&
+                        (T == 1 || p.q_token_stride == (long long)p.heads * QSFM_HEAD_DIM);
+  const int row = p.kv_layout == QSFM_KV_PACKED640   ? QSFM_PACKED_ROW_BYTES
+                  : p.kv_layout == QSFM_KV_BF16      ? QSFM_BF16_ROW_BYTES
+                  : p.kv_layout == QSFM_KV_PACKED384 ? QSFM_PACKED384_ROW_BYTES
+                                                     : QSFM_HEAD_DIM;
+  struct Span { const void* at; long long bytes; };
+  const long long cache_rows = p.kv_cache != nullptr ? (long long)p.num_blocks * QSFM_BLOCK_SIZE : 0;
+  const Span outs[] = {{p.q_out, q_out_bytes}, {p.kv_out, kv_out_bytes}, {p.kv_cache, cache_rows * row},
+                       {p.kv_scale, cache_rows * QSFM_SCALES_PER_ROW * 4}};
+  const long long wsize = p.weights_bf16 ? 2 : 4;
+  const Span ins[] = {{p.q, q_bytes}, {p.kv, kv_bytes}, {p.positions, T * 4}, {p.slot_map, T * 4},
+                      {p.cos_sin, (long long)p.max_positions * p.rope_dim * 4}, {p.q_weight, QSFM_HEAD_DIM * wsize},
+                      {p.kv_weight, QSFM_HEAD_DIM * wsize}};
+  for (int o = 0; o < 4; ++o) {
+    for (int i = 0; i < 7; ++i)
+      if (!(o == 0 && i == 0 && in_place) && overlap(outs[o].at, outs[o].bytes, ins[i].at, ins[i].bytes))
+        return QSFM_ERR_INVALID_ARG;
+    for (int k = 0; k < o; ++k)
+      if (overlap(outs[o].at, outs[o].bytes, outs[k].at, outs[k].bytes)) return QSFM_ERR_INVALID_ARG;
+  }
+  return QSFM_OK;
+}
+
+constexpr int kMaxTableRequests = 8192;
+
+// Checks of qsfm_update_block_tables().
+qsfm_status check_block_tables(const qsfm_block_table_params* pp) {
+  if (pp == nullptr) return QSFM_ERR_INVALID_ARG;
+  const qsfm_block_table_params& p = *pp;
+  if (p.batch < 0 || p.max_blocks < 1 || p.num_blocks < 1 || p.free_capacity < 0 || p.max_rows < 0)
+    return QSFM_ERR_INVALID_ARG;
+  if (p.cmp_ratio < 1 || p.cmp_ratio > 128) return QSFM_ERR_INVALID_ARG;
+  if (p.block_size < 1 || p.block_size > 1024) return QSFM_ERR_INVALID_ARG;
+  if (p.block_size != QSFM_BLOCK_SIZE) return QSFM_ERR_UNSUPPORTED;
+  if (p.batch > kMaxTableRequests) return QSFM_ERR_UNSUPPORTED;
+  if ((long long)p.num_blocks * p.block_size > kMaxPoolRows) return QSFM_ERR_UNSUPPORTED;
+  if ((long long)p.max_blocks * p.block_size > 1 << 30) return QSFM_ERR_UNSUPPORTED;
+  if (p.max_rows > 1 << 30 || (long long)p.batch * p.max_blocks > 1 << 30) return QSFM_ERR_UNSUPPORTED;
+  if (p.free_count == nullptr || (p.free_capacity > 0 && p.free_list == nullptr)) return QSFM_ERR_INVALID_ARG;
+  if (p.batch > 0 && (p.block_table == nullptr || p.prev_lens == nullptr || p.lens == nullptr))
+    return QSFM_ERR_INVALID_ARG;
+  if (p.max_rows > 0 && p.slot_map == nullptr) return QSFM_ERR_INVALID_ARG;
+  struct Span { const void* at; long long words; };
+  const Span all[] = {{p.block_table, (long long)p.batch * p.max_blocks}, {p.free_list, p.free_capacity},
+                      {p.free_count, 1}, {p.free_count_out, 1}, {p.slot_map, p.max_rows}, {p.positions, p.max_rows},
+                      {p.cu_rows, p.batch + 1ll}, {p.residual, p.batch}, {p.prev_lens, p.batch}, {p.lens, p.batch}};
+  for (int i = 0; i < 10; ++i) {
+    if (!aligned(all[i].at, 4)) return QSFM_ERR_INVALID_ARG;
+    for (int k = 0; k < i && i < 10; ++k)  // prev_lens and lens, which are only read, may be one tensor
+      if (!(i == 9 && k == 8) && !(i == 3 && k == 2 && all[i].at == all[k].at) &&
+          overlap(all[i].at, 4 * all[i].words, all[k].at, 4 * all[k].words))
+        return QSFM_ERR_INVALID_ARG;
+  }
+  return QSFM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -444,6 +562,40 @@ qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* pp, void* workspac
   if (fault == nullptr) return QSFM_ERR_CUDA;
   const NvtxRange range("qsfm_lightning_indexer");
   return cuda_status(qsfm::launch_indexer(p, int(T), workspace, fault, static_cast<cudaStream_t>(stream)));
+}
+
+void qsfm_norm_rope_params_init(qsfm_norm_rope_params* p) {
+  if (p == nullptr) return;
+  std::memset(p, 0, sizeof(*p));
+  p->dim = QSFM_HEAD_DIM;
+  p->norm_q = p->norm_kv = 1;
+  p->eps = 1e-6f;
+}
+
+qsfm_status qsfm_norm_rope_store(const qsfm_norm_rope_params* p, void* stream) {
+  const qsfm_status st = check_norm_rope(p);
+  if (st != QSFM_OK) return st;
+  if (p->tokens == 0) return QSFM_OK;
+  int* fault = fault_ptr();
+  if (fault == nullptr) return QSFM_ERR_CUDA;
+  const NvtxRange range("qsfm_norm_rope_store");
+  return cuda_status(qsfm::launch_norm_rope(*p, fault, static_cast<cudaStream_t>(stream)));
+}
+
+void qsfm_block_table_params_init(qsfm_block_table_params* p) {
+  if (p == nullptr) return;
+  std::memset(p, 0, sizeof(*p));
+  p->cmp_ratio = 1;
+  p->block_size = QSFM_BLOCK_SIZE;
+}
+
+qsfm_status qsfm_update_block_tables(const qsfm_block_table_params* p, void* stream) {
+  const qsfm_status st = check_block_tables(p);
+  if (st != QSFM_OK) return st;
+  int* fault = fault_ptr();
+  if (fault == nullptr) return QSFM_ERR_CUDA;
+  const NvtxRange range("qsfm_update_block_tables");
+  return cuda_status(qsfm::launch_block_tables(*p, fault, static_cast<cudaStream_t>(stream)));
 }
 
 qsfm_status qsfm_get_device_status(int32_t* fault_word) {

@@ -447,6 +447,11 @@ __device__ void mma_role(const qsfm_params& p, const Smem& sm, Range rg, int T, 
 //                nope bytes 64 + 128 c + 16 j .. + 15 (the same d as fp8
 //                rows, e8m0 scale 2 c - 1 + j / 4); lane j = 4 of each row
 //                loads the seven scale bytes (576 .. 583);
+//   4-bit rows   chunk 0: bf16 rope bytes 16 j .. + 15 and, for j < 4, the 16
+//                codes of nope bytes 128 + 8 j .. + 7 (d 64 + 16 j .., scale
+//                j); chunk c >= 1: the 16 codes of bytes 96 + 64 c + 8 j ..
+//                + 7 (d 128 c + 16 j .., scale 8 c - 4 + j); lane j holds
+//                word j of the row's 28 scales and exponent;
 //   bf16 rows    bytes 256 c + 16 j and 256 c + 128 + 16 j: unit j of
 //                d-blocks 2 c and 2 c + 1, copied as they are (chunks 2 and
 //                3 are loaded into the registers of chunks 0 and 1 once
@@ -509,6 +514,8 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
         scl[u].x = ldg_pred_u32(spool + size_t(v ? prr[u] : 0) * kScales + j, v);
       } else if constexpr (kFmt == QSFM_KV_PACKED640) {
         scl[u] = (v && j == 4) ? ldg_stream_v2(row + 576) : make_uint2(0, 0);
+      } else if constexpr (kFmt == QSFM_KV_PACKED384) {
+        scl[u].x = ldg_pred_u32(row + 352 + 4 * j, v);
       }
     }
     if constexpr (kFmt == QSFM_KV_FP8_FP32_SCALES) {
@@ -516,6 +523,16 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
     } else if constexpr (kFmt == QSFM_KV_BF16) {
       R[2 * (c & 1)][u] = v ? ldg_stream_v4(row + 256 * c + 16 * j) : z;
       R[2 * (c & 1) + 1][u] = v ? ldg_stream_v4(row + 256 * c + 128 + 16 * j) : z;
+    } else if constexpr (kFmt == QSFM_KV_PACKED384) {
+      uint2 codes = make_uint2(0, 0);
+      if (c == 0) {
+        RR[u] = v ? ldg_stream_v4(row + 16 * j) : z;
+        if (v && j < 4) codes = ldg_stream_v2(row + 128 + 8 * j);
+      } else if (v) {
+        codes = ldg_stream_v2(row + 96 + 64 * c + 8 * j);
+      }
+      R[c][u].x = codes.x;
+      R[c][u].y = codes.y;
     } else {
       if (c == 0) {
         RR[u] = v ? ldg_stream_v4(row + 16 * j) : z;
@@ -548,6 +565,24 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
         const float s = fminf(__shfl_sync(0xffffffffu, __uint_as_float(sc[u].x), grp | (2 * c + odd)) * rsc[u],
                               65504.f / 448.f);
         dequant16_f16(R[c][u], pack_f16(s, s), lo, hi);
+      } else if constexpr (kFmt == QSFM_KV_PACKED384) {
+        const uint32_t w7 = __shfl_sync(0xffffffffu, sc[u].x, grp | 7);  // the row's exponent
+        const int word = c == 0 ? 0 : 2 * c - 1 + odd;
+        const uint32_t ws = __shfl_sync(0xffffffffu, sc[u].x, grp | word);
+        const float s = scale_e4m3(ws, j & 3, e8m0_value(w7 & 0xFFu));
+        const uint2 a = dequant4_e2m1(R[c][u].x, s), b = dequant4_e2m1(R[c][u].x >> 16, s);
+        const uint2 d = dequant4_e2m1(R[c][u].y, s), e = dequant4_e2m1(R[c][u].y >> 16, s);
+        lo = make_uint4(a.x, a.y, b.x, b.y);
+        hi = make_uint4(d.x, d.y, e.x, e.y);
+        if (c == 0) {
+          sts_v4(tile + rr * 128 + ((uint32_t(j) ^ sw) << 4), RR[u]);  // rope: d-block 0
+          if (j < 4) {
+            const uint32_t rowb = tile + kSlabBytes + rr * 128;  // nope d 64..127: d-block 1
+            sts_v4(rowb + ((uint32_t(2 * j) ^ sw) << 4), lo);
+            sts_v4(rowb + ((uint32_t(2 * j + 1) ^ sw) << 4), hi);
+          }
+          continue;
+        }
       } else {
         const uint32_t w0 = __shfl_sync(0xffffffffu, sc[u].x, grp | 4);  // scale bytes 0..3
         const uint32_t w1 = __shfl_sync(0xffffffffu, sc[u].y, grp | 4);  // scale bytes 4..6
@@ -1079,6 +1114,7 @@ cudaError_t launch_attention(const qsfm_params& p, int num_tokens, int num_ctas,
   // one instantiation per KV row format, so none pays for the others
   auto* kernel = p.kv_layout == QSFM_KV_PACKED640 ? attention_kernel<QSFM_KV_PACKED640>
                  : p.kv_layout == QSFM_KV_BF16    ? attention_kernel<QSFM_KV_BF16>
+                 : p.kv_layout == QSFM_KV_PACKED384 ? attention_kernel<QSFM_KV_PACKED384>
                                                   : attention_kernel<QSFM_KV_FP8_FP32_SCALES>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;

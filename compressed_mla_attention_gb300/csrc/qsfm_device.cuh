@@ -253,7 +253,10 @@ __device__ __forceinline__ void resolve_tile_rows(const qsfm_params& p, const To
 
 // Bytes of one KV row in the pool of each row format.
 __host__ __device__ constexpr int kv_row_bytes(int fmt) {
-  return fmt == QSFM_KV_PACKED640 ? QSFM_PACKED_ROW_BYTES : fmt == QSFM_KV_BF16 ? QSFM_BF16_ROW_BYTES : kDim;
+  return fmt == QSFM_KV_PACKED640   ? QSFM_PACKED_ROW_BYTES
+         : fmt == QSFM_KV_BF16      ? QSFM_BF16_ROW_BYTES
+         : fmt == QSFM_KV_PACKED384 ? QSFM_PACKED384_ROW_BYTES
+                                    : kDim;
 }
 
 // ------------------------------------------------------------ PTX wrappers
@@ -677,6 +680,28 @@ __device__ __forceinline__ void dequant16(const uint4& in, float scale, uint4& l
   hi.y = dequant2(uint16_t(in.z >> 16), scale);
   hi.z = dequant2(uint16_t(in.w & 0xFFFF), scale);
   hi.w = dequant2(uint16_t(in.w >> 16), scale);
+}
+
+// The four e4m3 scales of a word, each times the row's power of two, in fp32.
+__device__ __forceinline__ float scale_e4m3(uint32_t word, int byte, float power) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(uint8_t(word >> (8 * byte)), __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half*>(&h)) * power;
+}
+
+// 4 e2m1 codes (the low 16 bits of `four`, low nibble first) times `scale`,
+// as bf16 pairs: code and scale have 2 and 4 significant bits, so the product
+// is exact.
+__device__ __forceinline__ uint2 dequant4_e2m1(uint32_t four, float scale) {
+  uint32_t a, b;
+  asm("{\n .reg .b8 x, y, z, w;\n mov.b32 {x, y, z, w}, %2;\n"
+      " cvt.rn.f16x2.e2m1x2 %0, x;\n cvt.rn.f16x2.e2m1x2 %1, y;\n}"
+      : "=r"(a), "=r"(b)
+      : "r"(four));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
+  const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(f.x * scale, f.y * scale);
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(g.x * scale, g.y * scale);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 __device__ __forceinline__ uint4 ldg_nc_v4(const void* ptr) {

@@ -54,6 +54,8 @@ cudaError_t launch_combine(const qsfm_params& p, int num_tokens, int num_ctas,
 size_t indexer_workspace_bytes(const qsfm_indexer_params& p, int num_tokens);
 cudaError_t launch_indexer(const qsfm_indexer_params& p, int num_tokens, void* workspace, int* fault,
                            cudaStream_t s);
+cudaError_t launch_norm_rope(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s);
+cudaError_t launch_block_tables(const qsfm_block_table_params& p, int* fault, cudaStream_t s);
 cudaError_t launch_bounded_wait(uint64_t timeout_ns, unsigned long long* elapsed, int* fault,
                                 cudaStream_t s);
 cudaError_t launch_debug_gather(const qsfm_params& p, const int32_t* tokens, int n,

@@ -104,6 +104,7 @@ extern "C" {
 #define QSFM_MAX_CTAS 256
 #define QSFM_PACKED_ROW_BYTES 640
 #define QSFM_BF16_ROW_BYTES 1024
+#define QSFM_PACKED384_ROW_BYTES 384
 
 /* KV row formats (qsfm_params.kv_layout). */
 typedef enum {
@@ -118,7 +119,16 @@ typedef enum {
   QSFM_KV_PACKED640 = 1,
   /* bf16 rows [blocks, 128, 1, 512] without quantisation (the KV of
    * SparseCompressedFlashAttention); ori_scale and cmp_scale must be NULL. */
-  QSFM_KV_BF16 = 2
+  QSFM_KV_BF16 = 2,
+  /* 4-bit rows [blocks, 128, 1, 384], an addition of this library: bf16
+   * rope (64 elements, bytes 0..127), e2m1 nope (448 codes, bytes 128..351,
+   * the lower element in the low nibble), e4m3fn scales (28, one per 16
+   * nope elements, bytes 352..379), one e8m0 exponent for the row's scales
+   * (byte 380), zero padding to 384. The 512 elements of a row are rope then
+   * nope; nope element i is code_i * scale_(i / 16) * 2^(exponent - 127),
+   * which has at most six significant bits. ori_scale and cmp_scale must be
+   * NULL. qsfm_norm_rope_store() writes such rows. */
+  QSFM_KV_PACKED384 = 3
 } qsfm_kv_layout;
 
 typedef enum {
@@ -153,6 +163,12 @@ typedef enum {
                                           2^22: its values were clamped    */
 #define QSFM_FAULT_KV_ROW         0x80 /* a non-paged KV row past the end of
                                           its tensor (skipped)             */
+#define QSFM_FAULT_BLOCK_POOL     0x100 /* qsfm_update_block_tables(): no free
+                                          block was left, or the free list
+                                          would have overflowed            */
+#define QSFM_FAULT_SLOT           0x200 /* a slot past the end of the cache, or
+                                          more new rows than slot_map holds */
+#define QSFM_FAULT_POSITION       0x400 /* a position past the cos_sin table */
 
 /*
  * All inputs, attributes and outputs of one forward call. Pointers are
@@ -301,7 +317,8 @@ qsfm_status qsfm_forward_noalloc(const qsfm_params* p, void* stream);
  * max_rows of them:
  *   rows_out    uint8 [n, max_rows, R]    the bytes of the resolved row in
  *                                         the pool's own format, R = 512
- *                                         (fp8), 640 (packed) or 1024 (bf16)
+ *                                         (fp8), 640 or 384 (packed) or 1024
+ *                                         (bf16)
  *   scales_out  fp32  [n, max_rows, 8]    its dequant scales (fp8 only)
  *   row_ids_out int32 [n, max_rows]       (source << 30) | logical row, with
  *                                         source 0 = ori, 1 = cmp; -1 for a
@@ -434,6 +451,154 @@ qsfm_status qsfm_lightning_indexer_workspace_size(const qsfm_indexer_params* p, 
  * (workspace NULL, misaligned or too small). */
 qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* p, void* workspace, size_t workspace_bytes,
                                    void* stream);
+
+/*
+ * Norm of the queries and keys of each head with the position rotation in
+ * the same pass, and the store of the key rows into the cache that the
+ * attention reads. An addition of this library: the step that makes what
+ * qsfm_forward() takes. For each query token t, each head row x of q (and
+ * the token's one latent row of kv), of dim = 512 elements:
+ *   y = x / sqrt(mean(x^2) + eps) * weight          (norm_q / norm_kv set;
+ *                                                    else y = x)
+ *   the rope_dim elements from rope_offset on are rotated by the angles of
+ *   positions[t]: (a, b) -> (a cos - b sin, b cos + a sin) with the pairs
+ *   (2i, 2i + 1) when interleaved is set, (i, i + rope_dim / 2) otherwise,
+ *   cos = cos_sin[pos][i], sin = cos_sin[pos][rope_dim / 2 + i]
+ * in fp32 throughout, rounded once: q_out[t] in bf16; the kv row in the row
+ * format kv_layout at row slot_map[t] of the cache (kv_cache is
+ * [num_blocks, 128, 1, row], row s its s-th row).
+ *   packed384  exponent byte 127 + E, E = floor(log2 max|y|) - 10 over the
+ *              whole row (clipped to -100 .. 100), scale = e4m3(max|y| of the
+ *              16 / 6 / 2^E), code = e2m1(y / (scale 2^E)), to nearest even,
+ *              saturating
+ *   packed640  exponent of each 64 nope elements the smallest with max|y| <=
+ *              448 2^(e - 127) (e clipped to 27 .. 227), code = e4m3(y / 2^(e - 127))
+ *   fp8        scale = max|y| of each 64 / 448 (at least 1e-12 / 448), code =
+ *              e4m3(y / scale)
+ *   A scale group with an element that is not finite stores a scale of NaN
+ *   (packed formats); the other groups are as without it.
+ * A token whose position is negative is padding: nothing of it is read or
+ * written. A slot that is negative stores no row (q_out and kv_out are
+ * written); each slot is named by at most one token (of two, the row's bytes
+ * are a mixture). A position past the table skips the token
+ * (QSFM_FAULT_POSITION), a slot past the cache the store (QSFM_FAULT_SLOT).
+ *
+ *   q          [T, heads, 512] bf16, fp16 or fp32 (in_type), element strides
+ *              q_token_stride and q_head_stride, or NULL (heads = 0)
+ *   kv         [T, 512] of the same type, kv_token_stride, or NULL
+ *   q_out      bf16 [T, heads, 512] contiguous; may be q itself where q is
+ *              bf16 and contiguous
+ *   kv_cache   NULL: no row is stored; kv_scale fp32 [num_blocks, 128, 1, 8]
+ *              for fp8 rows, else NULL
+ *   kv_out     bf16 [T, 512] or NULL: the values of the stored rows (rounded
+ *              to bf16 for fp8 rows, exact otherwise; without kv_cache the
+ *              rows of format bf16)
+ *   q_weight, kv_weight  [512] fp32, or bf16 (weights_bf16), or NULL (ones)
+ *   positions  int32 [T]; cos_sin fp32 [max_positions, rope_dim], both NULL
+ *              with rope_dim 0 (positions may be given all the same)
+ *   slot_map   int32 [T], required with kv_cache
+ * rope_dim is 0 or 32, 64, 128 or 256 and rope_offset a multiple of it.
+ * Pointers and strides: q, kv, q_out, kv_cache, kv_out, the weights and
+ * cos_sin 16-byte aligned, strides multiples of 16 bytes; the rest 4-byte.
+ * Outputs overlap no input (QSFM_ERR_INVALID_ARG) but for q_out = q.
+ */
+typedef enum { QSFM_BF16 = 0, QSFM_F16 = 1, QSFM_F32 = 2 } qsfm_elem_type;
+
+typedef struct qsfm_norm_rope_params {
+  int32_t tokens;          /* T                                             */
+  int32_t heads;           /* head rows of a token in q; 0 without q        */
+  int32_t dim;             /* must be 512                                   */
+  int32_t in_type;         /* qsfm_elem_type of q and kv                    */
+  int32_t weights_bf16;    /* non-zero: q_weight and kv_weight are bf16     */
+  int32_t norm_q;          /* non-zero (default): normalise the query rows  */
+  int32_t norm_kv;         /* non-zero (default): normalise the kv rows     */
+  int32_t rope_dim;
+  int32_t rope_offset;
+  int32_t interleaved;
+  int32_t max_positions;   /* rows of cos_sin                               */
+  int32_t kv_layout;       /* qsfm_kv_layout of kv_cache                    */
+  int32_t num_blocks;      /* blocks of 128 rows in kv_cache                */
+  float eps;
+  int64_t q_token_stride, q_head_stride, kv_token_stride; /* in elements    */
+  const void* q;
+  const void* kv;
+  const void* q_weight;
+  const void* kv_weight;
+  const float* cos_sin;
+  const int32_t* positions;
+  const int32_t* slot_map;
+  void* q_out;
+  void* kv_cache;
+  float* kv_scale;
+  void* kv_out;
+} qsfm_norm_rope_params;
+
+/* Defaults: dim 512, both norms, eps 1e-6, kv_layout fp8, pointers NULL. */
+void qsfm_norm_rope_params_init(qsfm_norm_rope_params* p);
+
+/* One launch on `stream`; no workspace, nothing read back. Errors:
+ * QSFM_ERR_INVALID_ARG, QSFM_ERR_UNSUPPORTED (dim other than 512, rope_dim
+ * not built, T (heads + 1) above 2^30, a cache of 2^31 rows or more). */
+qsfm_status qsfm_norm_rope_store(const qsfm_norm_rope_params* p, void* stream);
+
+/*
+ * Block tables and slots from request lengths, on the GPU. An addition of
+ * this library: the bookkeeping of the paged cache between two steps. With
+ * rows(n) = floor(n / cmp_ratio), held_b = ceil(rows(prev_lens[b]) / 128) and
+ * need_b = ceil(rows(lens[b]) / 128), for the B requests in order:
+ *   a request that shrinks gives the blocks of its table columns need_b ..
+ *   held_b - 1 back to the end of the free list (a request that has ended has
+ *   lens[b] = 0), then a request that grows takes the blocks of columns
+ *   held_b .. need_b - 1 from the end of the list, in the order (request,
+ *   column). So a block given back in a call may be taken in the same call.
+ * The table columns behind need_b are left as they were.
+ * The new rows rows(prev_lens[b]) .. rows(lens[b]) - 1 of all requests, end to
+ * end, are described by
+ *   slot_map   int32 [max_rows]  row of the pool: table[b][row / 128] * 128 +
+ *              row % 128; -1 where no block was left and behind the last row
+ *   positions  int32 [max_rows] or NULL: row * cmp_ratio; -1 behind the last
+ *   cu_rows    int32 [B + 1] or NULL: the rows' prefix sums (with cmp_ratio 1
+ *              the cu_seqlens_q of the step)
+ *   residual   int32 [B] or NULL: lens[b] - rows(lens[b]) * cmp_ratio
+ *              (cmp_residual_kv)
+ * block_table int32 [B, max_blocks], free_list int32 [free_capacity] and
+ * free_count int32 [1] are the state, updated in place; free_count_out, when
+ * not NULL, takes the new count instead of free_count (the call can then be
+ * repeated on the same inputs). Bad data is reported in the fault word and
+ * skipped: no free block left (QSFM_FAULT_BLOCK_POOL: -1 in the table), a
+ * block id outside [0, num_blocks) (QSFM_FAULT_ORI_BLOCK_ID: slots -1), more
+ * than max_blocks blocks in a request (QSFM_FAULT_ORI_TABLE_COL), more new
+ * rows than max_rows (QSFM_FAULT_SLOT). Negative lengths count as 0. The
+ * buffers do not overlap.
+ */
+typedef struct qsfm_block_table_params {
+  int32_t batch;           /* B, at most 8192                               */
+  int32_t max_blocks;      /* block_table row width                         */
+  int32_t num_blocks;      /* blocks in the pool                            */
+  int32_t free_capacity;   /* entries of free_list                          */
+  int32_t max_rows;        /* entries of slot_map and positions             */
+  int32_t cmp_ratio;       /* 1 .. 128                                      */
+  int32_t block_size;      /* must be 128                                   */
+  int32_t* block_table;
+  const int32_t* prev_lens;
+  const int32_t* lens;
+  int32_t* free_list;
+  int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* slot_map;
+  int32_t* positions;
+  int32_t* cu_rows;
+  int32_t* residual;
+} qsfm_block_table_params;
+
+/* Defaults: cmp_ratio 1, block size 128, all pointers NULL. */
+void qsfm_block_table_params_init(qsfm_block_table_params* p);
+
+/* One launch on `stream`; no workspace, nothing read back. Errors:
+ * QSFM_ERR_INVALID_ARG, QSFM_ERR_UNSUPPORTED (more than 8192 requests, a
+ * block size other than 128, a pool of 2^31 rows or more, max_blocks * 128 or
+ * max_rows or B * max_blocks above 2^30). */
+qsfm_status qsfm_update_block_tables(const qsfm_block_table_params* p, void* stream);
 
 /* Synchronously read and clear the device fault word of the current
  * device (QSFM_FAULT_* bits). Returns QSFM_ERR_DEVICE_FAULT when non-zero. */

@@ -122,6 +122,42 @@ def dequant_packed_rows(rows: np.ndarray) -> np.ndarray:
     return np.concatenate([rope, nope * np.repeat(scales, TILE, axis=1)], axis=1).reshape(n, HEAD_DIM)
 
 
+# --------------------------------------------------------------------------
+# 4-bit rows (an addition of this library). e2m1: 1 sign bit, 2 exponent bits
+# with bias 1, 1 mantissa bit; exponent 0 is subnormal (m/2); no infinity and
+# no NaN.
+# --------------------------------------------------------------------------
+def decode_e2m1_code(code: int) -> float:
+    """Value of one e2m1 code (0..15), from the bit fields."""
+    sign = -1.0 if (code >> 3) & 1 else 1.0
+    exp = (code >> 1) & 0x3
+    man = code & 0x1
+    return sign * (man / 2.0 if exp == 0 else (1.0 + man / 2.0) * 2.0 ** (exp - 1))
+
+
+E2M1_TABLE = np.array([decode_e2m1_code(c) for c in range(16)], dtype=np.float64)
+PACKED384_ROW = 384
+
+
+def dequant_packed384_rows(rows: np.ndarray) -> np.ndarray:
+    """K~ of 4-bit rows [n, 384] -> fp64 [n, 512], exactly.
+
+    A row is rope (64 bf16, bytes 0..127), nope (448 e2m1 codes, bytes
+    128..351, the lower element in the low nibble), scales (28 e4m3fn, bytes
+    352..379, one per 16 nope elements) and one e8m0 exponent (byte 380) that
+    multiplies all of them. The 512 elements are rope then nope.
+    """
+    rows = np.ascontiguousarray(rows)
+    n = rows.shape[0]
+    bits = rows[:, :2 * ROPE_DIM].copy().view("<u2").astype(np.uint32) << 16
+    rope = bits.view(np.float32).astype(np.float64)
+    two = rows[:, 128:352].astype(np.int64)
+    nope = np.empty((n, HEAD_DIM - ROPE_DIM))
+    nope[:, 0::2], nope[:, 1::2] = E2M1_TABLE[two & 0xF], E2M1_TABLE[two >> 4]
+    scales = E4M3FN_TABLE[rows[:, 352:380].astype(np.int64)] * E8M0_TABLE[rows[:, 380:381].astype(np.int64)]
+    return np.concatenate([rope, nope * np.repeat(scales, 16, axis=1)], axis=1).reshape(n, HEAD_DIM)
+
+
 BF16_ROW = 2 * HEAD_DIM
 
 
@@ -279,11 +315,13 @@ def gather_paged(kv_pool, scale_pool, table_row, rows):
 
 
 def decode_rows(kv_bytes: np.ndarray, scales) -> np.ndarray:
-    """K~ of gathered rows: packed 640-byte rows carry their scales, bf16
-    rows (1024 bytes) need none; 512-byte fp8 rows come with a separate fp32
+    """K~ of gathered rows: packed 640-byte and 4-bit 384-byte rows carry their
+    scales, bf16 rows (1024 bytes) need none; 512-byte fp8 rows come with a separate fp32
     scale row."""
     if kv_bytes.shape[-1] == PACKED_ROW:
         return dequant_packed_rows(kv_bytes)
+    if kv_bytes.shape[-1] == PACKED384_ROW:
+        return dequant_packed384_rows(kv_bytes)
     if kv_bytes.shape[-1] == BF16_ROW:
         return decode_bf16_rows(kv_bytes)
     return dequant_rows(kv_bytes, scales)

@@ -67,7 +67,7 @@ class Workload:
     q_lens: np.ndarray  # int64 [B]: query tokens per batch
     cu_seqlens_q: Optional[torch.Tensor]  # int32 [B+1] (TND)
     q: torch.Tensor  # bf16 [T, N1, 512], N1 = 64 or 128 (BSND memory is identical)
-    ori_kv: torch.Tensor  # paged pool [nb, 128, 1, row] (uint8 512 fp8 / 640 packed, or bf16 512); see layout_kv
+    ori_kv: torch.Tensor  # paged pool [nb, 128, 1, row] (uint8 512 fp8 / 640 or 384 packed, or bf16 512); see layout_kv
     ori_scale: Optional[torch.Tensor]  # fp32 [nb, 128, 1, 8]; None for packed and bf16 rows
     ori_block_table: Optional[torch.Tensor]  # int32 [B, wo]; None for non-paged KV
     seqused_ori_kv: Optional[torch.Tensor]  # int32 [B]; None for TND KV (and optionally BSND KV)
@@ -163,6 +163,44 @@ def _quantize_packed_rows(x: torch.Tensor):
     return out
 
 
+PACKED384_ROW = 384  # bf16 rope 64 (128 B) + e2m1 nope 448 + e4m3fn scales 28 + e8m0 exponent + pad
+
+
+def _quantize_packed384_rows(x: torch.Tensor):
+    """fp32 rows [n, 512] as 4-bit rows: the first 64 elements in bf16, the
+    other 448 as e2m1 codes with an e4m3fn scale (amax / 6) per 16 elements,
+    all scales relative to a power of two that puts the largest near the top
+    of the e4m3fn range."""
+    n = x.shape[0]
+    amax = x.abs().amax(dim=1)
+    e = torch.where(amax > 0, torch.frexp(amax).exponent - 11, -100).clamp(-100, 100)
+    t = x[:, ROPE_DIM:].reshape(n, 28, 16)
+    power = torch.ldexp(torch.ones(n), e)[:, None]
+    s8 = (t.abs().amax(dim=-1) / 6.0 / power).to(torch.float8_e4m3fn)
+    scale = (s8.to(torch.float32) * power).unsqueeze(-1)
+    r = torch.where(scale > 0, t / scale, torch.zeros(())).clamp(-6.0, 6.0)
+    # nearest e2m1 value, ties to the even mantissa: a step of 0.5 below 2, of
+    # 1 below 4, of 2 above (torch.round rounds halves to even)
+    step = torch.where(r.abs() < 2, 0.5, torch.where(r.abs() < 4, 1.0, 2.0))
+    v = (torch.round(r / step) * step).abs()
+    code = torch.where(v < 2, 2 * v, torch.where(v < 4, v + 2, v / 2 + 4)).to(torch.int32)
+    code = (code + 8 * (r < 0)).reshape(n, 224, 2)
+    out = torch.zeros(n, PACKED384_ROW, dtype=torch.uint8)
+    out[:, :128] = x[:, :ROPE_DIM].to(torch.bfloat16).view(torch.uint8).view(n, 128)
+    out[:, 128:352] = (code[:, :, 0] + 16 * code[:, :, 1]).to(torch.uint8)
+    out[:, 352:380] = s8.view(torch.uint8)
+    out[:, 380] = (e + 127).to(torch.uint8)
+    return out
+
+
+def _random_packed384_rows(n: int, gen: torch.Generator, chunk: int = 1 << 16):
+    rows = torch.empty(n, PACKED384_ROW, dtype=torch.uint8)
+    for lo in range(0, n, chunk):
+        hi = min(n, lo + chunk)
+        rows[lo:hi] = _quantize_packed384_rows(torch.randn(hi - lo, HEAD_DIM, generator=gen, dtype=torch.float32))
+    return rows
+
+
 def _random_packed_rows(n: int, gen: torch.Generator, chunk: int = 1 << 16):
     rows = torch.empty(n, PACKED_ROW, dtype=torch.uint8)
     for lo in range(0, n, chunk):
@@ -195,8 +233,8 @@ def _random_rows(n: int, gen: torch.Generator, chunk: int = 1 << 16):
 def _paged_pool(lengths: np.ndarray, gen: torch.Generator, min_width: int = 0,
                 block: int = BLOCK, fmt: str = "fp8_fp32_scales"):
     """Pool + shuffled block table holding lengths[b] rows for each batch
-    (fmt packed640: 640-byte rows, bf16: bf16 rows; neither has a scale
-    tensor)."""
+    (fmt packed640: 640-byte rows, packed384: 4-bit rows, bf16: bf16 rows;
+    none of them has a scale tensor)."""
     nblk = [(int(l) + block - 1) // block for l in lengths]
     total = sum(nblk)
     width = max([min_width] + nblk + [1])
@@ -207,8 +245,10 @@ def _paged_pool(lengths: np.ndarray, gen: torch.Generator, min_width: int = 0,
         table[b, :k] = perm[off:off + k]
         off += k
     nrows = max(total, 1) * block
-    if fmt in ("packed640", "bf16"):
-        make, width_b = (_random_packed_rows, PACKED_ROW) if fmt == "packed640" else (_random_bf16_rows, HEAD_DIM)
+    if fmt in ("packed640", "packed384", "bf16"):
+        make, width_b = {"packed640": (_random_packed_rows, PACKED_ROW),
+                         "packed384": (_random_packed384_rows, PACKED384_ROW),
+                         "bf16": (_random_bf16_rows, HEAD_DIM)}[fmt]
         if nrows <= BANK_ROWS:
             rows = make(nrows, gen)
         else:
@@ -228,9 +268,11 @@ def _paged_pool(lengths: np.ndarray, gen: torch.Generator, min_width: int = 0,
 
 def _dense_rows(n: int, gen: torch.Generator, fmt: str):
     """n random rows of a row format: (rows, scales or None); rows are uint8
-    [n, 512] (fp8), uint8 [n, 640] (packed) or bf16 [n, 512]."""
+    [n, 512] (fp8), uint8 [n, 640] or [n, 384] (packed) or bf16 [n, 512]."""
     if fmt == "packed640":
         return _random_packed_rows(n, gen), None
+    if fmt == "packed384":
+        return _random_packed384_rows(n, gen), None
     if fmt == "bf16":
         return _random_bf16_rows(n, gen), None
     return _random_rows(n, gen)
@@ -325,7 +367,7 @@ def build(
     assert len(s2) == B
     T = int(q_lens.sum())
     q = (torch.randn(T, n1, HEAD_DIM, generator=gen) * q_scale).to(torch.bfloat16)
-    assert kv_format in ("fp8_fp32_scales", "packed640", "bf16")
+    assert kv_format in ("fp8_fp32_scales", "packed640", "packed384", "bf16")
     assert layout_kv in ("PA_BBND", "BSND", "TND")
     paged = layout_kv == "PA_BBND"
     cu_ori = cu_cmp = None
