@@ -181,6 +181,9 @@ qsfm_status validate(const qsfm_params* pp, bool need_outputs) {
   if (!aligned(p.q, 16) || !aligned(p.ori_kv, 16) || !aligned(p.cmp_kv, 16) ||
       !aligned(p.attn_out, 16))
     return QSFM_ERR_INVALID_ARG;
+  // 4-bit rows are read in 32-byte sectors
+  if (p.kv_layout == QSFM_KV_PACKED384 && (!aligned(p.ori_kv, 32) || !aligned(p.cmp_kv, 32)))
+    return QSFM_ERR_INVALID_ARG;
   const void* words[] = {p.ori_scale, p.cmp_scale, p.cmp_sparse_indices, p.ori_block_table,
                          p.cmp_block_table, p.cu_seqlens_q, p.seqused_q, p.seqused_ori_kv,
                          p.seqused_cmp_kv, p.cmp_residual_kv, p.cmp_topk_length, p.sinks,

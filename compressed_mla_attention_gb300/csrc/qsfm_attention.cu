@@ -56,14 +56,7 @@
 // exceeds it by more than 8 (log2 units); a named-barrier vote detects that
 // case, so most tiles need no cross-row max reduction. When it moves, O^T
 // and the row sums are rescaled exactly. P <= 2^8 in bf16.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_runtime.h>
-
-#include <mutex>
-
-#include "qsfm_device.cuh"
-#include "qsfm_internal.h"
+#include "qsfm_attention_common.cuh"
 
 namespace qsfm {
 namespace {
@@ -80,8 +73,6 @@ constexpr int kMmaWarp = kWorkWarps;
 constexpr int kResolverWarp = kMmaWarp + 1;
 constexpr int kThreads = (kResolverWarp + 1) * 32;
 constexpr int kRing = 8;     // tiles of resolved rows in flight
-constexpr int kResolveTiles = 1;  // tiles per resolver pass (more keeps more loads in flight, at a
-                                  // larger instruction footprint; the ring already runs 8 tiles ahead)
 constexpr int kBarWork = 1;  // named barrier id of the worker warps
 
 // shared memory map (byte offsets from a 1024-aligned base)
@@ -118,9 +109,6 @@ static_assert(kNumBars * 8 <= 224, "barriers overlap the tmem slot");
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0;
 constexpr uint32_t kTmemO = 256;  // + 64 * chunk
-constexpr float kRescaleLog2 = 8.0f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 // Operand type of the products: fp8 rows are dequantised to f16 (one exact
 // e4m3 -> f16 conversion and one f16 multiply per pair of values; q is
 // converted to f16 when it lands, with an exact power-of-two prescale);
@@ -134,79 +122,13 @@ constexpr uint32_t kIdescPV = make_idesc_bf16(128, 64, /*a_mn=*/1, /*b_mn=*/1, k
 // Largest per-row power-of-two prescale of fp8 rows: P (<= 2^8 by the lazy
 // max) times 2^7 stays inside f16.
 constexpr int kMaxRowShift = 7;
-constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per wait
-
-struct Range {
-  int t0, k0, t1, k1;
-};
-
-// Walks the (unit, tile-range) pieces of a CTA's range in order.
-struct PieceIter {
-  const qsfm_params* p;
-  Range r;
-  int T;
-  int t;
-  __device__ PieceIter(const qsfm_params* p_, Range r_, int T_) : p(p_), r(r_), T(T_), t(r_.t0) {}
-  __device__ bool next(int& tok, TokenGeom& g, int& lo, int& hi) {
-    if (t > r.t1 || t >= T || (t == r.t1 && r.k1 == 0)) return false;
-    tok = t;
-    g = token_geom(*p, t);
-    lo = (t == r.t0) ? min(r.k0, g.n_tiles) : 0;
-    hi = (t == r.t1) ? min(r.k1, g.n_tiles) : g.n_tiles;
-    ++t;
-    return true;
-  }
-};
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Max (kMax) or sum of kN (16 or 32) values per lane over the 32 lanes of a
-// warp, by halving exchanges (for kN = 16, lanes l and l ^ 16 are combined
-// first): afterwards lane l holds the result for value index l % kN. The
-// array is consumed.
-template <bool kMax, int kN>
-__device__ __forceinline__ float reduce_lanes(float (&v)[kN]) {
-  const int lane = threadIdx.x & 31;
-  if constexpr (kN == 16) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float got = __shfl_xor_sync(0xffffffffu, v[i], 16);
-      v[i] = kMax ? fmaxf(v[i], got) : v[i] + got;
-    }
-  }
-#pragma unroll
-  for (int w = kN / 2; w >= 1; w >>= 1) {
-    const bool up = lane & w;
-#pragma unroll
-    for (int i = 0; i < w; ++i) {
-      const float keep = up ? v[w + i] : v[i];
-      const float send = up ? v[i] : v[w + i];
-      const float got = __shfl_xor_sync(0xffffffffu, send, w);
-      v[i] = kMax ? fmaxf(keep, got) : keep + got;
-    }
-  }
-  return v[0];
-}
-
-// kN consecutive tensor-memory columns of the warp's 32 lanes, one lane per
-// thread.
-template <int kN>
-__device__ __forceinline__ void tmem_load(uint32_t taddr, float (&v)[kN]) {
-  if constexpr (kN == 32) tmem_ld32(taddr, v);
-  else tmem_ld16(taddr, v);
-}
-template <int kN>
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const float (&v)[kN]) {
-  if constexpr (kN == 32) tmem_st32(taddr, v);
-  else tmem_st16(taddr, v);
-}
 
 struct Smem {
+  static constexpr int kRing = qsfm::kRing, kBarRowsFull = qsfm::kBarRowsFull, kBarRowsEmpty = qsfm::kBarRowsEmpty;
   uint32_t base;
   uint8_t* ptr;
+  __device__ int* ring_rows() const { return reinterpret_cast<int*>(ptr + kSRows); }
+  __device__ int* ring_kind() const { return reinterpret_cast<int*>(ptr + kSRowKind); }
   __device__ float* f(uint32_t off) const { return reinterpret_cast<float*>(ptr + off); }
   __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(ptr + kSBar) + i; }
   __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + kSBar + 224); }
@@ -214,105 +136,6 @@ struct Smem {
     return reinterpret_cast<volatile int*>(ptr + kSBar + 232);
   }
 };
-
-// Bounded wait; on timeout raises the CTA's abort flag and the fault bit.
-__device__ __forceinline__ bool wait_or_abort(const Smem& sm, int bar, uint32_t parity, int* fault) {
-  if (mbar_wait_bounded(sm.bar(bar), parity, sm.abort_flag(), kTimeoutNs)) return true;
-  if (!*sm.abort_flag()) {
-    *sm.abort_flag() = 1;
-    atomicOr(fault, QSFM_FAULT_TIMEOUT);
-  }
-  return false;
-}
-
-// Warp-uniform bounded wait: lane 0 polls, the result is broadcast, so the
-// lanes of a warp never split on a timeout.
-__device__ __forceinline__ bool warp_wait_or_abort(const Smem& sm, int bar, uint32_t parity,
-                                                   int* fault) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_or_abort(sm, bar, parity, fault);
-  __syncwarp();  // the other lanes wait here (and are ordered after lane 0's acquire)
-  return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-}
-
-// Asks L2 for the bytes of physical row `prow` of a pool (and its scale row).
-template <int kFmt>
-__device__ __forceinline__ void prefetch_row(const uint8_t* pool, const float* spool, int prow) {
-  constexpr uint32_t kRowB = kv_row_bytes(kFmt);
-  bulk_prefetch_l2(pool + size_t(prow) * kRowB, kRowB);
-  if constexpr (kFmt == QSFM_KV_FP8_FP32_SCALES) prefetch_l2(spool + size_t(prow) * kScales);
-}
-
-// ------------------------------------------------------------- resolver
-// Tile n's rows go to ring slot n % kRing: 128 physical rows (block * 128 +
-// offset, -1 = masked) and the pool they come from. After the CTA's last tile
-// the resolver writes an end mark (-1) in the next slot. Up to kResolveTiles
-// tiles of one unit per pass: all their index loads are in flight together,
-// then all their block-table loads, so a pass costs two memory round trips
-// whatever its tile count.
-template <int kFmt>
-__device__ void resolver_role(const qsfm_params& p, const Smem& sm, Range rg, int T, int* fault) {
-  constexpr int kN = kResolveTiles;
-  const int lane = threadIdx.x & 31;
-  int* rows = reinterpret_cast<int*>(sm.ptr + kSRows);
-  int* kind = reinterpret_cast<int*>(sm.ptr + kSRowKind);
-  const uint8_t* q8 = static_cast<const uint8_t*>(p.q);
-  PieceIter pieces(&p, rg, T);
-  uint32_t n = 0;  // next ring position
-  int unit, lo, hi;
-  TokenGeom g;
-  while (pieces.next(unit, g, lo, hi)) {
-    if (lo >= hi) continue;
-    // the unit's Q goes to L2 a few tiles before its first product; the next
-    // token's index list while this one is resolved
-    if (lane == 0) bulk_prefetch_l2(q8 + size_t(unit) * kHeads * kDim * 2, kHeads * kDim * 2);
-    if (p.cmp_sparse_indices != nullptr && g.tok + 1 < (T >> unit_shift(p))) {
-      const uint8_t* ix = reinterpret_cast<const uint8_t*>(p.cmp_sparse_indices + (size_t)(g.tok + 1) * p.k2);
-      for (int off = 128 * lane; off < 4 * p.k2; off += 32 * 128) prefetch_l2(ix + off);
-    }
-    // passes of up to kN tiles of this unit
-    for (int k0 = lo; k0 < hi; k0 += kN) {
-      int k[kN];
-      bool live[kN];
-#pragma unroll
-      for (int t = 0; t < kN; ++t) {
-        k[t] = k0 + t;
-        live[t] = k0 + t < hi;
-      }
-#pragma unroll
-      for (int t = 0; t < kN; ++t) {
-        const uint32_t m = n + t;
-        if (live[t] && !warp_wait_or_abort(sm, kBarRowsEmpty + m % kRing, ((m / kRing) & 1) ^ 1, fault)) return;
-      }
-      int lg[kN][4], pr[kN][4];
-      bool cmp[kN];
-      resolve_tile_rows<kN>(p, g, k, live, lane, fault, lg, pr, cmp);
-#pragma unroll
-      for (int t = 0; t < kN; ++t) {
-        if (!live[t]) continue;
-        const uint32_t slot = (n + t) % kRing;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) rows[slot * kTileRows + lane + 32 * u] = pr[t][u];
-        if (lane == 0) kind[slot] = cmp[t] ? 1 : 0;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm.bar(kBarRowsFull + slot));
-      }
-      n += min(kN, hi - k0);
-    }
-  }
-  // end mark after the CTA's last tile
-  const uint32_t slot = n % kRing;
-  if (!warp_wait_or_abort(sm, kBarRowsEmpty + slot, ((n / kRing) & 1) ^ 1, fault)) return;
-  if (lane == 0) kind[slot] = -1;
-  __syncwarp();
-  if (lane == 0) mbar_arrive(sm.bar(kBarRowsFull + slot));
-}
-
-__device__ __forceinline__ float e8m0_value(uint32_t e) {
-  // 2^(e - 127): the fp32 with biased exponent e (e = 0: the subnormal 2^-127)
-  return e == 0xFFu ? __uint_as_float(0x7FC00000u) : e == 0u ? __uint_as_float(0x00400000u)
-                                                             : __uint_as_float(e << 23);
-}
 
 // ------------------------------------------------------------- MMA issue
 // QK^T of chunk c (d-blocks 2c, 2c + 1), k-step s of d-block db: A (K~,
@@ -447,11 +270,6 @@ __device__ void mma_role(const qsfm_params& p, const Smem& sm, Range rg, int T, 
 //                nope bytes 64 + 128 c + 16 j .. + 15 (the same d as fp8
 //                rows, e8m0 scale 2 c - 1 + j / 4); lane j = 4 of each row
 //                loads the seven scale bytes (576 .. 583);
-//   4-bit rows   chunk 0: bf16 rope bytes 16 j .. + 15 and, for j < 4, the 16
-//                codes of nope bytes 128 + 8 j .. + 7 (d 64 + 16 j .., scale
-//                j); chunk c >= 1: the 16 codes of bytes 96 + 64 c + 8 j ..
-//                + 7 (d 128 c + 16 j .., scale 8 c - 4 + j); lane j holds
-//                word j of the row's 28 scales and exponent;
 //   bf16 rows    bytes 256 c + 16 j and 256 c + 128 + 16 j: unit j of
 //                d-blocks 2 c and 2 c + 1, copied as they are (chunks 2 and
 //                3 are loaded into the registers of chunks 0 and 1 once
@@ -514,8 +332,6 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
         scl[u].x = ldg_pred_u32(spool + size_t(v ? prr[u] : 0) * kScales + j, v);
       } else if constexpr (kFmt == QSFM_KV_PACKED640) {
         scl[u] = (v && j == 4) ? ldg_stream_v2(row + 576) : make_uint2(0, 0);
-      } else if constexpr (kFmt == QSFM_KV_PACKED384) {
-        scl[u].x = ldg_pred_u32(row + 352 + 4 * j, v);
       }
     }
     if constexpr (kFmt == QSFM_KV_FP8_FP32_SCALES) {
@@ -523,16 +339,6 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
     } else if constexpr (kFmt == QSFM_KV_BF16) {
       R[2 * (c & 1)][u] = v ? ldg_stream_v4(row + 256 * c + 16 * j) : z;
       R[2 * (c & 1) + 1][u] = v ? ldg_stream_v4(row + 256 * c + 128 + 16 * j) : z;
-    } else if constexpr (kFmt == QSFM_KV_PACKED384) {
-      uint2 codes = make_uint2(0, 0);
-      if (c == 0) {
-        RR[u] = v ? ldg_stream_v4(row + 16 * j) : z;
-        if (v && j < 4) codes = ldg_stream_v2(row + 128 + 8 * j);
-      } else if (v) {
-        codes = ldg_stream_v2(row + 96 + 64 * c + 8 * j);
-      }
-      R[c][u].x = codes.x;
-      R[c][u].y = codes.y;
     } else {
       if (c == 0) {
         RR[u] = v ? ldg_stream_v4(row + 16 * j) : z;
@@ -565,24 +371,6 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
         const float s = fminf(__shfl_sync(0xffffffffu, __uint_as_float(sc[u].x), grp | (2 * c + odd)) * rsc[u],
                               65504.f / 448.f);
         dequant16_f16(R[c][u], pack_f16(s, s), lo, hi);
-      } else if constexpr (kFmt == QSFM_KV_PACKED384) {
-        const uint32_t w7 = __shfl_sync(0xffffffffu, sc[u].x, grp | 7);  // the row's exponent
-        const int word = c == 0 ? 0 : 2 * c - 1 + odd;
-        const uint32_t ws = __shfl_sync(0xffffffffu, sc[u].x, grp | word);
-        const float s = scale_e4m3(ws, j & 3, e8m0_value(w7 & 0xFFu));
-        const uint2 a = dequant4_e2m1(R[c][u].x, s), b = dequant4_e2m1(R[c][u].x >> 16, s);
-        const uint2 d = dequant4_e2m1(R[c][u].y, s), e = dequant4_e2m1(R[c][u].y >> 16, s);
-        lo = make_uint4(a.x, a.y, b.x, b.y);
-        hi = make_uint4(d.x, d.y, e.x, e.y);
-        if (c == 0) {
-          sts_v4(tile + rr * 128 + ((uint32_t(j) ^ sw) << 4), RR[u]);  // rope: d-block 0
-          if (j < 4) {
-            const uint32_t rowb = tile + kSlabBytes + rr * 128;  // nope d 64..127: d-block 1
-            sts_v4(rowb + ((uint32_t(2 * j) ^ sw) << 4), lo);
-            sts_v4(rowb + ((uint32_t(2 * j + 1) ^ sw) << 4), hi);
-          }
-          continue;
-        }
       } else {
         const uint32_t w0 = __shfl_sync(0xffffffffu, sc[u].x, grp | 4);  // scale bytes 0..3
         const uint32_t w1 = __shfl_sync(0xffffffffu, sc[u].y, grp | 4);  // scale bytes 4..6
@@ -984,22 +772,6 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
   }
 }
 
-// Runs before the plan is readable, while the plan kernel still runs: warms
-// L2 with the Q and the sparse-index row of the unit this CTA most likely
-// starts with (the plan cuts equal-cost units evenly, so CTA c of G starts
-// near unit c T / G). Prefetches only, no loads to wait for, no fault bits:
-// a wrong guess costs bandwidth, never results or time.
-__device__ __forceinline__ void warm_first_token(const qsfm_params& p, int T, int c, int G, int lane) {
-  const int t = int((long long)c * T / G);
-  if (t >= T) return;
-  if (lane == 0)
-    bulk_prefetch_l2(static_cast<const uint8_t*>(p.q) + size_t(t) * kHeads * kDim * 2, kHeads * kDim * 2);
-  if (p.cmp_sparse_indices != nullptr) {
-    const uint8_t* ix = reinterpret_cast<const uint8_t*>(p.cmp_sparse_indices + size_t(t >> unit_shift(p)) * p.k2);
-    for (int off = 128 * lane; off < 4 * p.k2; off += 32 * 128) prefetch_l2(ix + off);
-  }
-}
-
 template <int kFmt>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const qsfm_params p, const int T, const Workspace ws, int* fault,
@@ -1068,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_or_abort(sm, kBarDrain, 0, fault);
     }
   } else {
-    resolver_role<kFmt>(p, sm, rg, T, fault);
+    resolver_role(p, sm, rg, T, fault);
   }
 
   // Roles run on single lanes (the MMA issue): each warp's lanes meet before
@@ -1082,39 +854,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Tensor map of q viewed as [T * 64 rows, 512 bf16 columns], boxes of
-// 64 rows x 64 columns (128 B) with the 128-B swizzle of the MMA operand.
-cudaError_t make_q_map(const void* q, int T, CUtensorMap* map) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult qres;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &qres) == cudaSuccess &&
-        qres == cudaDriverEntryPointSuccess)
-      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {cuuint64_t(kDim), cuuint64_t(T) * kHeads};
-  const cuuint64_t strides[1] = {cuuint64_t(kDim) * 2};
-  const cuuint32_t box[2] = {64, 64};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims,
-                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t launch_attention(const qsfm_params& p, int num_tokens, int num_ctas,
                              const Workspace& ws, int* fault, cudaStream_t s) {
+  if (p.kv_layout == QSFM_KV_PACKED384) return launch_attention4(p, num_tokens, num_ctas, ws, fault, s);
   // one instantiation per KV row format, so none pays for the others
   auto* kernel = p.kv_layout == QSFM_KV_PACKED640 ? attention_kernel<QSFM_KV_PACKED640>
                  : p.kv_layout == QSFM_KV_BF16    ? attention_kernel<QSFM_KV_BF16>
-                 : p.kv_layout == QSFM_KV_PACKED384 ? attention_kernel<QSFM_KV_PACKED384>
                                                   : attention_kernel<QSFM_KV_FP8_FP32_SCALES>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;

@@ -1,0 +1,756 @@
+// Attention kernel over 4-bit cache rows (packed384) (sm_103a).
+//
+// The same function, plan, pieces and transposed products as the kernel of
+// the other row formats (qsfm_attention.cu):
+//   S^T[j, h]  = sum_d K~[j, d] Q[h, d]      (M = 128 rows, N = 64 heads, K = 512)
+//   O^T[d, h] += sum_j V~[j, d] P[h, j]      (M = 128 d per chunk, N = 64, K = 128 rows)
+// with K~ = V~ = code * scale * 2^(exponent - 127): two, four and one
+// significant bits, so a dequantised element is exact in bf16 and both
+// operands of the score product are the inputs' own values.
+//
+// What differs is the division of labour: the softmax warps never wait for a
+// load, and the conversion of the codes is off the chain.
+//   warps 0-7    softmax and epilogue: warp w reads tensor-memory lanes
+//                32 (w % 4) .. + 31 and heads 32 (w / 4) .. + 31;
+//   warps 8-15   producers: thread (row r, half h) converts and stores d-block
+//                2c + h of chunk c of its row: 32-byte loads, so a warp's load
+//                touches whole sectors, and a row's 16-byte units land in the
+//                eight bank groups of the swizzle. Two chunks are converted to
+//                registers ahead of PV freeing their places, so that only
+//                their stores follow;
+//   warp 16      MMA issue (one thread);
+//   warp 17      resolver (18 and 19 only complete the warpgroup).
+// Chain per tile: PV(n) frees chunk pairs -> stores of tile n + 1 -> QK^T(n + 1)
+// chunk by chunk -> softmax(n + 1) -> PV(n + 1). The epilogue of a unit runs on
+// the softmax warps while the next unit's first tile is stored and multiplied,
+// and the next unit's q is requested as soon as the last score product of the
+// unit has completed.
+#include "qsfm_attention_common.cuh"
+
+namespace qsfm {
+namespace {
+
+constexpr int kSmWarps = 8;                  // softmax / epilogue
+constexpr int kSmThreads = kSmWarps * 32;
+constexpr int kPrWarps = 8;                  // producers
+constexpr int kMmaWarp = kSmWarps + kPrWarps;
+constexpr int kResolverWarp = kMmaWarp + 1;
+constexpr int kThreads = (kMmaWarp + 4) * 32;
+// Registers per thread: 96 at launch (five warps on an SM sub-partition), then
+// 96 for the softmax warps, 112 for the producers, 64 for the last warpgroup.
+constexpr int kPrRegs = 112, kLastRegs = 64;
+static_assert(kSmThreads * 96 + kPrWarps * 32 * kPrRegs + 128 * kLastRegs <= kThreads * 96, "register split");
+constexpr int kHPT = 32;                     // heads per softmax thread
+constexpr int kBarSm = 1;                    // named barrier of the softmax warps
+constexpr int kBarSlab = 2;                  // [2]: of the four warps that write a slab of the output
+constexpr int kRowB = QSFM_PACKED384_ROW_BYTES;
+
+// shared memory map (byte offsets from a 1024-aligned base)
+constexpr uint32_t kSlabBytes = kTileRows * 128;              // 128 rows x 64 d (bf16): 16 KB
+constexpr uint32_t kSK = 0;                                   // K~ tile: 8 slabs
+constexpr uint32_t kSQ = kSK + 8 * kSlabBytes;                // Q: 8 d-blocks x 64 heads x 128 B
+constexpr uint32_t kSP = kSQ + 8 * 64 * 128;                  // P: 128 rows x 64 heads (bf16)
+constexpr uint32_t kSRows = kSP + kTileRows * 128;            // [8][128] i32 physical rows
+constexpr uint32_t kSRowKind = kSRows + 8 * kTileRows * 4;    // [8] i32: 0 ori, 1 cmp, -1 end
+constexpr uint32_t kSValid = kSRowKind + 64;                  // [128] i32: row of the tile valid
+constexpr uint32_t kSRed = kSValid + kTileRows * 4;           // [4][64] f32 per-quadrant partials
+constexpr uint32_t kSMUsed = kSRed + 1024;                    // [64] f32
+constexpr uint32_t kSAlpha = kSMUsed + 256;                   // [64] f32
+constexpr uint32_t kSInv = kSAlpha + 256;                     // [64] f32
+constexpr uint32_t kSAny = kSInv + 256;                       // [4] i32: a row of the quadrant valid
+constexpr uint32_t kSBar = kSAny + 16;                        // mbarriers, tmem base, flags
+constexpr uint32_t kSmemBytes = kSBar + 256;
+// staging of the output: P's place as two slabs [64 heads][64 d] (bf16, 128-byte swizzle)
+constexpr uint32_t kSStage = kSP;
+constexpr uint32_t kSmemAlloc = kSmemBytes + 1024;
+static_assert(kSmemAlloc <= 232448, "more than the 227 KB a CTA may use");
+
+// mbarrier slots
+constexpr int kBarQFull = 0;
+constexpr int kBarFull = 1;        // [chunk]: stored (one arrive per producer warp)
+constexpr int kBarFree = 5;        // [chunk pair]: PV of chunks 2i, 2i + 1 completed (commit)
+constexpr int kBarSFull = 7;       // S^T of the tile complete (commit)
+constexpr int kBarPFull = 8;       // P of the tile written (one arrive per softmax warp)
+constexpr int kBarOFree = 9;       // O^T read by the epilogue (one arrive per softmax warp)
+constexpr int kBarDrain = 10;      // every MMA of the CTA completed (commit)
+
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemS = 0;
+constexpr uint32_t kTmemO = 256;  // + 64 * chunk
+constexpr float kGuessLog2 = 60.0f;  // below a guessed maximum
+constexpr uint32_t kIdescQK = make_idesc_bf16(128, 64, /*a_mn=*/0, /*b_mn=*/0);
+constexpr uint32_t kIdescPV = make_idesc_bf16(128, 64, /*a_mn=*/1, /*b_mn=*/1);
+
+struct Smem {
+  static constexpr int kRing = 8;           // tiles of resolved rows in flight
+  static constexpr int kBarRowsFull = 11;   // [ring slot]
+  static constexpr int kBarRowsEmpty = 19;  // [ring slot], one arrive per producer warp
+  static constexpr int kNumBars = 27;
+  uint32_t base;
+  uint8_t* ptr;
+  __device__ float* f(uint32_t off) const { return reinterpret_cast<float*>(ptr + off); }
+  __device__ int* ring_rows() const { return reinterpret_cast<int*>(ptr + kSRows); }
+  __device__ int* ring_kind() const { return reinterpret_cast<int*>(ptr + kSRowKind); }
+  __device__ int* valid() const { return reinterpret_cast<int*>(ptr + kSValid); }
+  __device__ int* any() const { return reinterpret_cast<int*>(ptr + kSAny); }
+  __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(ptr + kSBar) + i; }
+  __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + kSBar + 224); }
+  __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(ptr + kSBar + 232); }
+};
+static_assert(Smem::kNumBars * 8 <= 224, "barriers overlap the tmem slot");
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// 2-D tiled TMA store of one box; the issuing thread's bulk groups.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n"
+               "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tmap)),
+               "r"(src), "r"(x), "r"(y)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Bounded waits as wait_or_abort(), but suspended in hardware: try_wait gets a
+// time to stay blocked (20 us), so a waiting warp takes no issue slots from the
+// producers, and no sleep delays it once the phase completes. All lanes of a
+// warp wait together.
+constexpr uint32_t kSuspendNs = 20000;
+__device__ __forceinline__ bool mbar_suspend(uint32_t addr, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(addr), "r"(parity), "r"(kSuspendNs)
+      : "memory");
+  return done != 0;
+}
+__device__ __forceinline__ uint32_t globaltimer_lo() {  // wraps after 4.3 s, past the limit of a wait
+  uint32_t t;
+  asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(t));
+  return t;
+}
+__device__ __forceinline__ bool wait_fast(const Smem& sm, int bar, uint32_t parity, int* fault) {
+  const uint32_t addr = smem_u32(sm.bar(bar));
+  if (mbar_suspend(addr, parity)) return true;
+  const uint32_t start = globaltimer_lo();
+  while (!mbar_suspend(addr, parity)) {
+    if (*sm.abort_flag()) return false;
+    if (globaltimer_lo() - start > uint32_t(kTimeoutNs)) {
+      *sm.abort_flag() = 1;
+      atomicOr(fault, QSFM_FAULT_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool warp_wait_fast(const Smem& sm, int bar, uint32_t parity, int* fault) {
+  const bool ok = wait_fast(sm, bar, parity, fault);
+  return __all_sync(0xffffffffu, ok);  // the lanes of a warp never split on a timeout
+}
+
+// Waits for the tensor-memory loads into v (the registers pass through the
+// statement, so nothing that uses them moves above it).
+__device__ __forceinline__ void tmem_ld_wait_for(float (&v)[32]) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// ------------------------------------------------------------- MMA issue
+// QK^T of chunk c (d-blocks 2c, 2c + 1), k-step s of d-block db: A (K~,
+// K-major) at + db * 16 KB + s * 32 B, B (Q, K-major) at + db * 8 KB + s * 32 B.
+template <uint32_t kDb, uint32_t kS>
+__device__ __forceinline__ void qk_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  mma_f16_at<((kDb * kSlabBytes + kS * 32) >> 4), ((kDb * 8192 + kS * 32) >> 4)>(d, a, b, kIdescQK, acc);
+}
+__device__ __forceinline__ void qk_chunk(uint32_t d, uint64_t a0, uint64_t b0, int c) {
+  const uint64_t a = a0 + ((uint32_t(c) * 2 * kSlabBytes) >> 4);
+  const uint64_t b = b0 + ((uint32_t(c) * 2 * 8192) >> 4);
+  qk_mma<0, 0>(d, a, b, c != 0 ? 1u : 0u);
+  qk_mma<0, 1>(d, a, b, 1u); qk_mma<0, 2>(d, a, b, 1u); qk_mma<0, 3>(d, a, b, 1u);
+  qk_mma<1, 0>(d, a, b, 1u); qk_mma<1, 1>(d, a, b, 1u);
+  qk_mma<1, 2>(d, a, b, 1u); qk_mma<1, 3>(d, a, b, 1u);
+}
+
+// PV of head-dim chunk c, k-step s: A (V~^T, MN-major: 64-d atoms 16 KB apart,
+// 8-row groups 1 KB apart) at + c * 32 KB + s * 2 KB, B (P^T, MN-major) at
+// + s * 2 KB; accumulates into O^T columns 64 c .. + 63.
+template <uint32_t kS>
+__device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
+  mma_f16_at<((kS * 2048) >> 4), ((kS * 2048) >> 4)>(d, a, b, kIdescPV, acc);
+}
+__device__ __forceinline__ void pv_chunk(uint32_t tmem, uint64_t a0, uint64_t b0, uint32_t acc0, int c) {
+  const uint32_t d = tmem + kTmemO + uint32_t(c) * 64;
+  const uint64_t a = a0 + ((uint32_t(c) * 2 * kSlabBytes) >> 4);
+  pv_mma<0>(d, a, b0, acc0);
+  pv_mma<1>(d, a, b0, 1u); pv_mma<2>(d, a, b0, 1u); pv_mma<3>(d, a, b0, 1u);
+  pv_mma<4>(d, a, b0, 1u); pv_mma<5>(d, a, b0, 1u); pv_mma<6>(d, a, b0, 1u); pv_mma<7>(d, a, b0, 1u);
+}
+
+// Tile n of the CTA's sequence: every per-tile barrier completes once per
+// tile, so a wait for tile n uses phase parity n & 1.
+__device__ void mma_role(const qsfm_params& p, const Smem& sm, Range rg, int T, uint32_t tmem, int* fault) {
+  if ((threadIdx.x & 31) != 0) return;
+  PieceIter pieces(&p, rg, T);
+  const uint64_t qa = make_sdesc_sw128(sm.base + kSK, 16, 1024);
+  const uint64_t qb = make_sdesc_sw128(sm.base + kSQ, 16, 1024);
+  const uint64_t pa = make_sdesc_sw128(sm.base + kSK, kSlabBytes, 1024);
+  const uint64_t pb = make_sdesc_sw128(sm.base + kSP, 16, 1024);
+  const uint32_t ds = tmem + kTmemS;
+  TokenGeom g;
+  int unit, lo, hi;
+  uint32_t n = 0, piece = 0;
+  while (pieces.next(unit, g, lo, hi)) {
+    if (lo >= hi) continue;
+#pragma unroll 1
+    for (int k = lo; k < hi; ++k, ++n) {
+      const uint32_t par = n & 1;
+      if (k == lo && !wait_fast(sm, kBarQFull, piece & 1, fault)) return;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        if (!wait_fast(sm, kBarFull + c, par, fault)) return;
+        tc_fence_after();
+        qk_chunk(ds, qa, qb, c);
+      }
+      mma_commit(sm.bar(kBarSFull));
+      // P(n) written (so S^T(n) has been read)
+      if (!wait_fast(sm, kBarPFull, par, fault)) return;
+      tc_fence_after();
+      if (k == lo && piece > 0) {
+        // the previous piece's epilogue must have read O^T before it is overwritten
+        if (!wait_fast(sm, kBarOFree, (piece - 1) & 1, fault)) return;
+        tc_fence_after();
+      }
+      const uint32_t acc0 = k == lo ? 0u : 1u;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        pv_chunk(tmem, pa, pb, acc0, c);
+        if (c & 1) mma_commit(sm.bar(kBarFree + (c >> 1)));
+      }
+    }
+    ++piece;
+  }
+}
+
+// ------------------------------------------------------------- producers
+// 32 bytes (32-byte aligned), read once.
+struct Raw8 {
+  uint32_t w[8];
+};
+__device__ __forceinline__ Raw8 ldg_stream_v8(const void* ptr) {
+  Raw8 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]), "=r"(r.w[4]), "=r"(r.w[5]), "=r"(r.w[6]),
+                 "=r"(r.w[7])
+               : "l"(ptr));
+  return r;
+}
+
+// 64 codes with four scales (word ws) to 64 bf16.
+__device__ __forceinline__ void convert64(const Raw8& codes, uint32_t ws, uint32_t exponent, uint32_t (&out)[32]) {
+  const float power = e8m0_value(exponent & 0xFFu);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const float s = scale_e4m3(ws, g, power);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = codes.w[2 * g + i];
+      const uint2 x = dequant4_e2m1(w, s), y = dequant4_e2m1(w >> 16, s);
+      out[8 * g + 4 * i] = x.x;
+      out[8 * g + 4 * i + 1] = x.y;
+      out[8 * g + 4 * i + 2] = y.x;
+      out[8 * g + 4 * i + 3] = y.y;
+    }
+  }
+}
+
+// d-block 2c + half of row r, every chunk c. The block of chunk 0, half 0 is the
+// bf16 rope: loaded as it is stored.
+__device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) {
+  const int tid = int(threadIdx.x) - kSmThreads, lane = tid & 31;
+  const int half = tid >> 7, r = tid & 127;
+  const bool rope = half == 0;
+  const int* rows = sm.ring_rows();
+  const int* kind = sm.ring_kind();
+  const uint32_t rowb = sm.base + kSK + uint32_t(half) * kSlabBytes + uint32_t(r) * 128;
+  const uint32_t sw = uint32_t(r & 7);
+  uint32_t ca[32], cb[32];  // converted blocks: chunks 0 and 1, then 2 and 3
+  Raw8 ra, rb;              // codes of the blocks to convert next
+  uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0, ex = 0;  // scale words of the four blocks, the rows' exponents
+
+  auto take_rows = [&](uint32_t n, const uint8_t*& row, bool& v) -> bool {
+    const uint32_t slot = n % Smem::kRing;
+    if (!warp_wait_fast(sm, Smem::kBarRowsFull + slot, (n / Smem::kRing) & 1, fault)) return false;
+    const int kd = kind[slot], pr = rows[slot * kTileRows + r];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.bar(Smem::kBarRowsEmpty + slot));
+    v = pr >= 0;
+    row = static_cast<const uint8_t*>(kd == 1 ? p.cmp_kv : p.ori_kv) + size_t(v ? pr : 0) * kRowB;
+    return kd >= 0;
+  };
+  // Codes of chunk c's block: bytes 96 + 64 c + 32 half (none for the rope
+  // block). A masked row's codes are read all the same (row 0 of the pool) and
+  // times a scale of zero.
+  auto load_codes = [&](int c, const uint8_t* row) { return ldg_stream_v8(row + 96 + 64 * c + 32 * half); };
+  auto load_scales = [&](const uint8_t* row, bool v) {
+    const Raw8 q = ldg_stream_v8(row + 352);
+    s0 = v ? q.w[0] : 0u;
+    s1 = v ? (half ? q.w[2] : q.w[1]) : 0u;
+    s2 = v ? (half ? q.w[4] : q.w[3]) : 0u;
+    s3 = v ? (half ? q.w[6] : q.w[5]) : 0u;
+    ex = v ? q.w[7] : 0u;
+  };
+  auto load_rope = [&](const uint8_t* row, bool v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Raw8 q = ldg_stream_v8(row + 32 * i);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ca[8 * i + k] = v ? q.w[k] : 0u;
+    }
+  };
+  auto store = [&](int c, const uint32_t (&conv)[32]) {  // into chunk c's place, published
+    const uint32_t at = rowb + uint32_t(2 * c) * kSlabBytes;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      sts_v4(at + ((uint32_t(i) ^ sw) << 4), make_uint4(conv[4 * i], conv[4 * i + 1], conv[4 * i + 2], conv[4 * i + 3]));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.bar(kBarFull + c));
+  };
+
+  const uint8_t* row;
+  bool v;
+  if (!take_rows(0, row, v)) return;
+  load_scales(row, v);
+  if (rope) load_rope(row, v);
+  else ra = load_codes(0, row);
+  rb = load_codes(1, row);
+  if (!rope) convert64(ra, s0, ex, ca);
+  convert64(rb, s1, ex, cb);
+  ra = load_codes(2, row);
+  rb = load_codes(3, row);
+#pragma unroll 1
+  for (uint32_t n = 0;; ++n) {
+    // chunks 0 and 1 are converted, the codes of 2 and 3 loaded
+    if (n > 0 && !warp_wait_fast(sm, kBarFree, (n - 1) & 1, fault)) return;
+    if (rope) {
+      // the tile's valid flags: the softmax has read the last tile's (its P was
+      // written) and reads these after chunk 0 is published
+      sm.valid()[r] = v ? 1 : 0;
+      const bool any = __any_sync(0xffffffffu, v);
+      if (lane == 0) sm.any()[r >> 5] = any ? 1 : 0;
+    }
+    store(0, ca);
+    store(1, cb);
+    convert64(ra, s2, ex, ca);
+    if (n > 0 && !warp_wait_fast(sm, kBarFree + 1, (n - 1) & 1, fault)) return;
+    store(2, ca);
+    convert64(rb, s3, ex, cb);
+    store(3, cb);
+    // the next tile: its loads after the last store (stores queue behind loads
+    // in the load/store unit), its first conversions once P is published (they
+    // would take the softmax's issue slots)
+    if (!take_rows(n + 1, row, v)) return;
+    load_scales(row, v);
+    if (rope) load_rope(row, v);
+    else ra = load_codes(0, row);
+    rb = load_codes(1, row);
+    if (!warp_wait_fast(sm, kBarPFull, n & 1, fault)) return;
+    if (!rope) convert64(ra, s0, ex, ca);
+    ra = load_codes(2, row);
+    convert64(rb, s1, ex, cb);
+    rb = load_codes(3, row);
+  }
+}
+
+// ------------------------------------------------------------- softmax, epilogue
+__device__ void softmax_role(const qsfm_params& p, const Smem& sm, Range rg, int T, uint32_t tmem, const Workspace& ws,
+                             int c_idx, const CUtensorMap* qmap, const CUtensorMap* omap, int* fault) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int qd = warp & 3;            // tensor-memory lane quadrant
+  const int h0 = kHPT * (warp >> 2);  // first of this warp's heads
+  const int r = 32 * qd + lane;       // tile row of this thread
+  const uint32_t lane_base = uint32_t(32 * qd) << 16;
+  const uint32_t s_addr = tmem + kTmemS + h0 + lane_base;
+  const uint32_t prow_addr = sm.base + kSP + uint32_t(r) * 128;
+  float* m_used = sm.f(kSMUsed);
+  float* alpha = sm.f(kSAlpha);
+  float* inv = sm.f(kSInv);
+  float* red = sm.f(kSRed);
+  const float qk_scale = p.softmax_scale * kLog2e;
+
+  // q of a unit by TMA (thread 0)
+  auto load_q = [&](int unit) {
+    mbar_arrive_expect_tx(sm.bar(kBarQFull), kHeads * kDim * 2);
+#pragma unroll
+    for (int db = 0; db < 8; ++db)
+      tma_load_2d(sm.base + kSQ + db * 8192, qmap, db * 64, unit * 64, sm.bar(kBarQFull));
+  };
+
+  if (tid < 64) m_used[tid] = -INFINITY;  // no guess for the first unit
+  named_sync(kBarSm, kSmThreads);
+  PieceIter pieces(&p, rg, T);
+  uint32_t n = 0;
+  // A piece (work unit, its range of tiles), and the one after: the geometry of
+  // the piece after that is read while the current piece's last PV runs.
+  struct Piece {
+    int t, lo, hi, n_tiles;
+    bool have;
+  };
+  auto next_piece = [&]() {
+    Piece q;
+    TokenGeom g;
+    q.have = pieces.next(q.t, g, q.lo, q.hi);
+    q.n_tiles = g.n_tiles;
+    return q;
+  };
+  Piece cur = next_piece();
+  if (tid == 0 && cur.have && cur.lo < cur.hi) load_q(cur.t);
+  Piece nxt = cur.have ? next_piece() : cur;
+  while (cur.have) {
+    const int t = cur.t, lo = cur.lo, hi = cur.hi;
+    const bool whole = (lo == 0 && hi == cur.n_tiles), any = lo < hi;
+    // the next piece's q is requested once this piece's last score product has
+    // completed
+    const bool q_next = tid == 0 && nxt.have && nxt.lo < nxt.hi;
+    if (!any && q_next && !*sm.abort_flag()) load_q(nxt.t);
+    // this thread's head sink (log2 units); the unit's heads start at unit_head0
+    const float sink2 =
+        (tid < 64 && p.sinks != nullptr) ? __ldg(p.sinks + unit_head0(p, t) + tid) * kLog2e : -INFINITY;
+    const int slot = (t == rg.t0) ? 2 * c_idx : 2 * c_idx + 1;
+    const bool writable = whole || slot < ws.slots;  // split pieces need the workspace
+    if (!writable && tid == 0) atomicOr(fault, QSFM_FAULT_METADATA);
+    // Lane i of the warp keeps the running sum of P for head h0 + i over this
+    // warp's 32 rows: each tile's P is folded in with a lane reduction once P
+    // is published (one register instead of kHPT).
+    float l_sum = 0.f;
+    // The first tile takes the last unit's maxima as a guess: any reference is
+    // right that leaves no t above 8 (P stays in range) and none of the first
+    // rows' below -60 (P and its sum keep their precision; bf16 has the range
+    // of fp32). Where the guess fails the vote sends the tile down the slow
+    // path. `seen`: a tile with a valid row has set or confirmed the maxima.
+    bool seen = false;
+    Piece after = nxt;
+#pragma unroll 1
+    for (int k = lo; k < hi; ++k, ++n) {
+      const uint32_t par = n & 1;
+      // Lane 0 of each warp polls. After an abort the waits fall through at
+      // once; the warps keep running the same named-barrier sequence so that
+      // none of them blocks.
+      warp_wait_fast(sm, kBarFull + 0, par, fault);  // the tile's valid flags
+      const bool v = sm.valid()[r] != 0;
+      const int4 quadrants = *reinterpret_cast<const int4*>(sm.any());
+      warp_wait_fast(sm, kBarSFull, par, fault);
+      if (k == hi - 1 && q_next && !*sm.abort_flag()) load_q(nxt.t);  // q is free: the unit's last score product is complete
+      tc_fence_after();
+      float x[kHPT];
+      tmem_load(s_addr, x);
+      tmem_ld_wait_for(x);
+      // Fast path: t = score * scale - m (log2 units), P = 2^t computed before
+      // the vote; valid only if no t exceeds 8 anywhere in the tile.
+      float tmax = -INFINITY, tmin = INFINITY;
+#pragma unroll
+      for (int i = 0; i < kHPT; i += 4) {
+        const float4 m4 = *reinterpret_cast<const float4*>(m_used + h0 + i);
+        const float t0 = v ? fmaf(x[i], qk_scale, -m4.x) : -INFINITY;
+        const float t1 = v ? fmaf(x[i + 1], qk_scale, -m4.y) : -INFINITY;
+        const float t2 = v ? fmaf(x[i + 2], qk_scale, -m4.z) : -INFINITY;
+        const float t3 = v ? fmaf(x[i + 3], qk_scale, -m4.w) : -INFINITY;
+        tmax = fmaxf(tmax, fmaxf(fmaxf(t0, t1), fmaxf(t2, t3)));
+        if (!seen) tmin = fminf(tmin, fminf(fminf(t0, t1), fminf(t2, t3)));
+        x[i] = ex2_approx(t0);
+        x[i + 1] = ex2_approx(t1);
+        x[i + 2] = ex2_approx(t2);
+        x[i + 3] = ex2_approx(t3);
+      }
+      // also true against a maximum of -inf (t = inf)
+      const bool move = named_sync_or(kBarSm, kSmThreads, tmax > kRescaleLog2 || (v && !seen && tmin < -kGuessLog2));
+      float lscale = 1.f;  // 0 after a moved max: the running sums take alpha first
+      if (move) {
+        // Slow path: the scores again, the tile max per head over its 128
+        // rows, the new running max, then O^T and the row sums rescaled.
+        tmem_load(s_addr, x);
+        tmem_ld_wait_for(x);
+#pragma unroll
+        for (int i = 0; i < kHPT; ++i) x[i] = v ? x[i] * qk_scale : -INFINITY;
+        const float mx = reduce_lanes<true>(x);  // head h0 + lane, this quadrant's rows
+        red[qd * 64 + h0 + lane] = mx;
+        named_sync(kBarSm, kSmThreads);
+        if (tid < 64) {
+          const float mt = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
+          const float mu = m_used[tid];
+          float a = 1.f;
+          if (!seen) {  // nothing is accumulated yet
+            if (mt > -INFINITY) m_used[tid] = mt;
+          } else if (mt > -INFINITY && (mu == -INFINITY || mt > mu + kRescaleLog2)) {
+            a = (mu == -INFINITY) ? 0.f : exp2f(mu - mt);
+            m_used[tid] = mt;
+          }
+          alpha[tid] = a;
+        }
+        named_sync(kBarSm, kSmThreads);
+        if (seen) {
+          // O^T at this thread's lane, its heads, every chunk. The PV products
+          // of the earlier tiles have completed: S^T(n) was committed after
+          // them.
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            float o[kHPT];
+            const uint32_t addr = tmem + kTmemO + 64 * c + h0 + lane_base;
+            tmem_load(addr, o);
+            tmem_ld_wait_for(o);
+#pragma unroll
+            for (int i = 0; i < kHPT; ++i) o[i] *= alpha[h0 + i];
+            tmem_store(addr, o);
+          }
+          tmem_st_wait();
+        }
+        tmem_load(s_addr, x);
+        tmem_ld_wait_for(x);
+#pragma unroll
+        for (int i = 0; i < kHPT; ++i) {
+          const float m = m_used[h0 + i];
+          const float mz = m == -INFINITY ? 0.f : m;
+          x[i] = ex2_approx(v ? fmaf(x[i], qk_scale, -mz) : -INFINITY);
+        }
+        lscale = 0.f;
+      }
+      // P into the P buffer as [128 rows][64 heads] bf16 with the 128-B
+      // swizzle (the MN-major B operand of PV): this thread's row, its
+      // 16-byte units of 8 heads
+#pragma unroll
+      for (int vv = 0; vv < kHPT / 8; ++vv) {
+        const uint32_t u = uint32_t((h0 >> 3) + vv);
+        const uint4 pk = make_uint4(pack_bf16(x[8 * vv + 0], x[8 * vv + 1]), pack_bf16(x[8 * vv + 2], x[8 * vv + 3]),
+                                    pack_bf16(x[8 * vv + 4], x[8 * vv + 5]), pack_bf16(x[8 * vv + 6], x[8 * vv + 7]));
+        sts_v4(prow_addr + ((u ^ uint32_t(r & 7)) << 4), pk);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.bar(kBarPFull));
+      {
+        // running sums += this tile's P, folded over the warp's rows (after
+        // P is published: off the PV path); a moved max rescales them first
+        const float tile_sum = reduce_lanes<false>(x);
+        if (lscale == 0.f) l_sum *= alpha[h0 + lane];
+        l_sum += tile_sum;
+      }
+      seen = seen || (quadrants.x | quadrants.y | quadrants.z | quadrants.w) != 0;
+    }
+    if (nxt.have) after = next_piece();
+    // ---------------- epilogue of the piece
+    if (any) red[qd * 64 + h0 + lane] = l_sum;
+    named_sync(kBarSm, kSmThreads);
+    if (tid < 64 && writable) {
+      const float lt = any ? (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]) : 0.f;
+      const float mu = m_used[tid];
+      const float lse2 = lt > 0.f ? mu + log2f(lt) : -INFINITY;
+      if (whole) {
+        float den = lt;
+        if (p.sinks != nullptr && lt > 0.f) den += exp2f(sink2 - mu);
+        inv[tid] = lt > 0.f ? 1.f / den : 0.f;
+        if (p.return_lse) p.softmax_lse[size_t(t) * 64 + tid] = lse2 * kLn2;
+      } else {
+        inv[tid] = lt > 0.f ? 1.f / lt : 0.f;
+        ws.lse[size_t(slot) * 64 + tid] = lse2 * kLn2;
+      }
+    }
+    named_sync(kBarSm, kSmThreads);
+    if (any) {
+      warp_wait_fast(sm, kBarFree, (n - 1) & 1, fault);
+      warp_wait_fast(sm, kBarFree + 1, (n - 1) & 1, fault);
+      tc_fence_after();
+    }
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.attn_out) + size_t(t) * 64 * kDim;
+    if (!any) {
+      if (whole) {
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < 64 * kDim / 8; i += kSmThreads) reinterpret_cast<uint4*>(out)[i] = z;
+      }
+    } else if (whole) {
+      // Chunk by chunk through shared memory (P's place: PV is complete), two
+      // slabs of 64 d. A warp reads 16 lanes (d) x 64 heads as 8 x 8 fragments,
+      // scales them and stores them transposed as [head][64 d], 16-byte units
+      // swizzled by the head; the four warps of a slab then hand it to TMA,
+      // whose read of it runs beside the next chunk's arithmetic.
+      const int dl = 32 * qd + 16 * (warp >> 2);  // first of the warp's 16 lanes
+      const uint32_t o_addr = tmem + kTmemO + (uint32_t(dl) << 16);
+      const int slab = qd >> 1;
+      const bool leader = lane == 0 && warp == 2 * slab;
+      const uint32_t slab_addr = sm.base + kSStage + uint32_t(slab) * 8192;
+      const uint32_t unit = uint32_t((dl & 63) / 8 + ((lane >> 3) & 1)) ^ uint32_t(lane & 7);
+      const uint32_t st_addr = slab_addr + uint32_t(8 * (lane >> 4) + (lane & 7)) * 128 + unit * 16;
+      float o[32];
+      tmem_ld16x256b_x8(o_addr, o);
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        tmem_ld_wait_for(o);
+        uint32_t f[16];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 iv = *reinterpret_cast<const float2*>(inv + 8 * j + 2 * (lane & 3));
+          f[2 * j] = pack_bf16(o[4 * j] * iv.x, o[4 * j + 1] * iv.y);
+          f[2 * j + 1] = pack_bf16(o[4 * j + 2] * iv.x, o[4 * j + 3] * iv.y);
+        }
+        if (c < 3) {
+          tmem_ld16x256b_x8(o_addr + 64 * (c + 1), o);
+        } else {  // O^T is in registers: the next unit's PV may overwrite it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sm.bar(kBarOFree));
+        }
+        if (c > 0) {  // the last chunk has been read from the slab
+          if (leader) bulk_wait_read();
+          named_sync(kBarSlab + slab, 128);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2)
+          stmatrix_x4_trans(st_addr + uint32_t(j) * 8 * 128, f[2 * j], f[2 * j + 1], f[2 * j + 2], f[2 * j + 3]);
+        fence_proxy_async_smem();
+        named_sync(kBarSlab + slab, 128);
+        if (leader) tma_store_2d(omap, slab_addr, 128 * c + 64 * slab, t * 64);
+      }
+      if (leader) bulk_wait_read();
+    } else {
+      // split pieces: fp32 rows in the workspace, this thread element
+      // d = 128 c + 32 qd + lane of its heads (128 bytes per head per warp)
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[kHPT];
+        tmem_load(tmem + kTmemO + 64 * c + h0 + lane_base, o);
+        tmem_ld_wait_for(o);
+        if (writable) {
+          float* part = ws.out + (size_t(slot) * 64 + h0) * kDim + 128 * c + 32 * qd + lane;
+#pragma unroll
+          for (int i = 0; i < kHPT; ++i) part[size_t(i) * kDim] = o[i] * inv[h0 + i];
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sm.bar(kBarOFree));
+    }
+    named_sync(kBarSm, kSmThreads);  // m_used / inv / red are reused by the next piece
+    if (*sm.abort_flag()) break;     // uniform: read after the barrier
+    cur = nxt;
+    nxt = after;
+  }
+  if (lane == 0) bulk_wait();  // the leaders' stores
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    attention4_kernel(const qsfm_params p, const int T, const Workspace ws, int* fault,
+                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  Smem sm;
+  sm.base = (raw_addr + 1023u) & ~1023u;
+  sm.ptr = smem_raw + (sm.base - raw_addr);
+
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (warp == 0) warm_first_token(p, T, blockIdx.x, gridDim.x, tid);
+  grid_dependency_wait();    // the plan (and every input) is written by now
+  grid_launch_dependents();  // the combine kernel may take SMs as CTAs finish
+  const int* meta = p.metadata;
+  if (meta[0] != kMetaMagic || meta[2] != T) {
+    if (tid == 0 && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_METADATA);
+    return;
+  }
+  const int G = meta[1];
+  if (G < 0 || G > int(gridDim.x) || G > QSFM_MAX_CTAS) {
+    if (tid == 0 && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_METADATA);
+    return;
+  }
+  const int c = blockIdx.x;
+  if (c >= G) return;
+  const Range rg{meta[kMetaHeader + 2 * c], meta[kMetaHeader + 2 * c + 1],
+                 meta[kMetaHeader + 2 * c + 2], meta[kMetaHeader + 2 * c + 3]};
+  if (rg.t0 < 0 || rg.t1 > T || rg.t0 > rg.t1 || rg.k0 < 0 || rg.k1 < 0 ||
+      (rg.t1 == T && rg.k1 != 0)) {
+    if (tid == 0) atomicOr(fault, QSFM_FAULT_METADATA);
+    return;
+  }
+  if (rg.t0 == rg.t1 && rg.k0 == rg.k1) return;
+
+  if (tid == 0) {
+    mbar_init(sm.bar(kBarQFull), 1);
+    for (int i = 0; i < 4; ++i) mbar_init(sm.bar(kBarFull + i), kPrWarps);
+    for (int i = 0; i < 2; ++i) mbar_init(sm.bar(kBarFree + i), 1);
+    mbar_init(sm.bar(kBarSFull), 1);
+    mbar_init(sm.bar(kBarPFull), kSmWarps);
+    mbar_init(sm.bar(kBarOFree), kSmWarps);
+    for (int i = 0; i < Smem::kRing; ++i) {
+      mbar_init(sm.bar(Smem::kBarRowsFull + i), 1);
+      mbar_init(sm.bar(Smem::kBarRowsEmpty + i), kPrWarps);
+    }
+    mbar_init(sm.bar(kBarDrain), 1);
+    *sm.abort_flag() = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tmem_alloc(sm.tmem_slot(), kTmemCols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *sm.tmem_slot();
+
+  if (warp < kSmWarps) {
+    softmax_role(p, sm, rg, T, tmem, ws, c, &qmap, &omap, fault);
+  } else if (warp < kMmaWarp) {
+    more_registers<kPrRegs>();
+    producer_role(p, sm, fault);
+  } else {
+    fewer_registers<kLastRegs>();
+    if (warp == kMmaWarp) {
+      mma_role(p, sm, rg, T, tmem, fault);
+      if ((tid & 31) == 0) {
+        // every MMA issued above has completed before tensor memory is freed
+        // (after an abort some may still be in flight)
+        mma_commit(sm.bar(kBarDrain));
+        wait_or_abort(sm, kBarDrain, 0, fault);
+      }
+    } else if (warp == kResolverWarp) {
+      resolver_role(p, sm, rg, T, fault);
+    }
+  }
+
+  // After an abort a copy of q may still be on its way into this CTA's shared
+  // memory: give it a millisecond, far more than it takes.
+  if (tid == 0 && *sm.abort_flag())
+    for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+
+  // Roles run on single lanes (the MMA issue): each warp's lanes meet before
+  // the barrier (a barrier reached by part of a warp counts the whole warp).
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_attention4(const qsfm_params& p, int num_tokens, int num_ctas, const Workspace& ws, int* fault,
+                              cudaStream_t s) {
+  cudaError_t e = cudaFuncSetAttribute(attention4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
+  if (e != cudaSuccess) return e;
+  CUtensorMap qmap, omap;  // attn_out has q's layout
+  e = make_q_map(p.q, num_tokens, &qmap);
+  if (e == cudaSuccess) e = make_q_map(p.attn_out, num_tokens, &omap);
+  if (e != cudaSuccess) return e;
+  return launch_after_predecessor(attention4_kernel, dim3(num_ctas), dim3(kThreads), kSmemAlloc, s, p, num_tokens,
+                                  ws, fault, qmap, omap);
+}
+
+}  // namespace qsfm

@@ -592,6 +592,15 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t saddr, uint32_t r0, uint32_
                : "memory");
 }
 
+// The same with each matrix stored transposed: memory row t%8 of matrix t/8
+// gets the matrix's column t%8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                                  uint32_t r3) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(saddr),
+               "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+
 // 2^x by the hardware approximation (relative error about 2^-22; subnormal
 // results flush to zero, 2^-inf = 0).
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -697,10 +706,16 @@ __device__ __forceinline__ uint2 dequant4_e2m1(uint32_t four, float scale) {
       " cvt.rn.f16x2.e2m1x2 %0, x;\n cvt.rn.f16x2.e2m1x2 %1, y;\n}"
       : "=r"(a), "=r"(b)
       : "r"(four));
+  // both products of a pair in one packed fp32 multiply
+  const uint64_t s2 = (uint64_t(__float_as_uint(scale)) << 32) | __float_as_uint(scale);
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&a));
   const float2 g = __half22float2(*reinterpret_cast<const __half2*>(&b));
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(f.x * scale, f.y * scale);
-  const __nv_bfloat162 hi = __floats2bfloat162_rn(g.x * scale, g.y * scale);
+  uint64_t x = (uint64_t(__float_as_uint(f.y)) << 32) | __float_as_uint(f.x);
+  uint64_t y = (uint64_t(__float_as_uint(g.y)) << 32) | __float_as_uint(g.x);
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(x) : "l"(s2));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(y) : "l"(s2));
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(__uint_as_float(uint32_t(x)), __uint_as_float(uint32_t(x >> 32)));
+  const __nv_bfloat162 hi = __floats2bfloat162_rn(__uint_as_float(uint32_t(y)), __uint_as_float(uint32_t(y >> 32)));
   return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 

@@ -47,6 +47,9 @@ cudaError_t launch_plan(const qsfm_params& p, int num_tokens, int num_ctas, int 
                         int32_t* metadata, int* fault, cudaStream_t s);
 cudaError_t launch_attention(const qsfm_params& p, int num_tokens, int num_ctas,
                              const Workspace& ws, int* fault, cudaStream_t s);
+// The kernel of packed384 rows; launch_attention() passes them on.
+cudaError_t launch_attention4(const qsfm_params& p, int num_tokens, int num_ctas,
+                              const Workspace& ws, int* fault, cudaStream_t s);
 cudaError_t launch_combine(const qsfm_params& p, int num_tokens, int num_ctas,
                            const Workspace& ws, int* fault, cudaStream_t s);
 // Lightning indexer: score kernel then select kernel; the workspace holds

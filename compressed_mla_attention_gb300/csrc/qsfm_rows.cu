@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * kRowWarps;
+constexpr int kFewRows = 152 * 16;  // query rows up to which a warp has one
 constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
@@ -38,25 +39,37 @@ __device__ __forceinline__ float2 of_bf16x2(uint32_t v) {
 }
 __device__ __forceinline__ float round_bf16(float a) { return __uint_as_float(bf16x2(0.f, a) & 0xFFFF0000u); }
 
-// 8 consecutive elements of an input row in fp32.
+// 8 consecutive elements of an input row as they are read, and in fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* src, float (&v)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(src);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+struct Raw {
+  uint4 v[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* src) {
+#pragma unroll
+    for (int i = 0; i < int(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(src)[i];
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float2 f;
-      if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) f = of_bf16x2(w[i]);
-      else f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
+      if constexpr (sizeof(T) == 4) {
+        const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        f[2 * i] = __uint_as_float(x[2 * i]);
+        f[2 * i + 1] = __uint_as_float(x[2 * i + 1]);
+      } else {
+        const uint32_t x[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+        float2 p;
+        if constexpr (__is_same(T, __half)) p = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+        else p = of_bf16x2(x[i]);
+        f[2 * i] = p.x;
+        f[2 * i + 1] = p.y;
+      }
     }
   }
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* src, float (&f)[8]) {
+  Raw<T> raw;
+  raw.load(src);
+  raw.get(f);
 }
 
 __device__ __forceinline__ void store8_bf16(__nv_bfloat16* dst, const float (&v)[8]) {
@@ -106,26 +119,28 @@ __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bo
     const bool in = r >= 0 && r < p.rope_dim;
     if (p.interleaved) {
       if (in) {
+        const float4 c = *reinterpret_cast<const float4*>(table + r / 2);
+        const float4 s = *reinterpret_cast<const float4*>(table + half + r / 2);
+        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float c = table[r / 2 + i], s = table[half + r / 2 + i];
           const float a = y[h][2 * i], b = y[h][2 * i + 1];
-          y[h][2 * i] = a * c - b * s;
-          y[h][2 * i + 1] = b * c + a * s;
+          y[h][2 * i] = a * cs[i] - b * sn[i];
+          y[h][2 * i + 1] = b * cs[i] + a * sn[i];
         }
       }
-    } else {
+    } else if (__any_sync(kAll, in)) {
       // the range starts at a multiple of its (power of two) length, so the
       // other half's lane is this lane with one bit flipped, in the same h
       const bool upper = r >= half;
+      const int k = in ? (upper ? r - half : r) : 0;
+      float cs[8], sn[8];
+      load8(table + k, cs);
+      load8(table + half + k, sn);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float other = __shfl_xor_sync(kAll, y[h][i], p.rope_dim / 16);
-        if (in) {
-          const int k = (upper ? r - half : r) + i;
-          const float c = table[k], s = table[half + k];
-          y[h][i] = upper ? y[h][i] * c + other * s : y[h][i] * c - other * s;
-        }
+        if (in) y[h][i] = upper ? y[h][i] * cs[i] + other * sn[i] : y[h][i] * cs[i] - other * sn[i];
       }
     }
   }
@@ -308,16 +323,18 @@ __device__ __forceinline__ bool token_position(const qsfm_norm_rope_params& p, i
   return true;
 }
 
-template <typename T>
+// kG query rows per warp and turn: their loads are in flight together.
+template <typename T, int kG>
 __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const qsfm_norm_rope_params p, const int kv_blocks,
                                                                 int* fault) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float w[2][8], y[2][8];
+  float w[2][8];
   if (int(blockIdx.x) < kv_blocks) {
     load_weights(p.kv_weight, p.weights_bf16 != 0, lane, w);
     for (int t = blockIdx.x * kRowWarps + warp; t < p.tokens; t += kv_blocks * kRowWarps) {
       int pos;
       if (!token_position(p, t, fault, pos)) continue;
+      float y[2][8];
       const T* src = static_cast<const T*>(p.kv) + size_t(t) * p.kv_token_stride + 8 * lane;
       load8(src, y[0]);
       load8(src + 256, y[1]);
@@ -337,31 +354,64 @@ __global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const qsfm_norm_
     return;
   }
   load_weights(p.q_weight, p.weights_bf16 != 0, lane, w);
-  const int rows = p.tokens * p.heads, step = (gridDim.x - kv_blocks) * kRowWarps;
-  for (int r = (blockIdx.x - kv_blocks) * kRowWarps + warp; r < rows; r += step) {
-    const int t = r / p.heads, head = r - t * p.heads;
-    int pos;
-    if (!token_position(p, t, fault, pos)) continue;
-    const T* src = static_cast<const T*>(p.q) + size_t(t) * p.q_token_stride + size_t(head) * p.q_head_stride + 8 * lane;
-    load8(src, y[0]);
-    load8(src + 256, y[1]);
-    norm_rope_row(p, p.norm_q != 0, w, pos, lane, y);
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q_out) + size_t(r) * kDim + 8 * lane;
-    store8_bf16(out, y[0]);
-    store8_bf16(out + 256, y[1]);
+  const int rows = p.tokens * p.heads, step = (gridDim.x - kv_blocks) * kRowWarps * kG;
+  for (int r0 = ((blockIdx.x - kv_blocks) * kRowWarps + warp) * kG; r0 < rows; r0 += step) {
+    Raw<T> raw[kG][2];
+    int pos[kG];
+    bool live[kG];
+    const int t0 = r0 / p.heads, head0 = r0 - t0 * p.heads;
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      int t = t0, head = head0 + g;
+      while (head >= p.heads) {  // at most kG turns
+        head -= p.heads;
+        ++t;
+      }
+      live[g] = r0 + g < rows;
+      if (!live[g]) continue;
+      pos[g] = p.positions != nullptr ? __ldg(p.positions + t) : 0;
+      const T* src = static_cast<const T*>(p.q) + size_t(t) * p.q_token_stride + size_t(head) * p.q_head_stride + 8 * lane;
+      raw[g][0].load(src);
+      raw[g][1].load(src + 256);
+    }
+#pragma unroll
+    for (int g = 0; g < kG; ++g) {
+      if (!live[g] || pos[g] < 0) continue;
+      if (p.rope_dim != 0 && pos[g] >= p.max_positions) {
+        if (lane == 0) atomicOr(fault, QSFM_FAULT_POSITION);
+        continue;
+      }
+      float y[2][8];
+      raw[g][0].get(y[0]);
+      raw[g][1].get(y[1]);
+      norm_rope_row(p, p.norm_q != 0, w, pos[g], lane, y);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q_out) + size_t(r0 + g) * kDim + 8 * lane;
+      store8_bf16(out, y[0]);
+      store8_bf16(out + 256, y[1]);
+    }
   }
+}
+
+template <typename T>
+void launch_rows(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s) {
+  auto blocks = [](long long warps) { return int((warps + kRowWarps - 1) / kRowWarps); };
+  const int kv_blocks = p.kv != nullptr ? min(blocks(p.tokens), 1 << 14) : 0;
+  const long long rows = p.q != nullptr ? (long long)p.tokens * p.heads : 0;
+  // Few rows: one per warp, as many warps as rows (latency). Many: four per
+  // turn (two of fp32), so that a warp's loads overlap.
+  constexpr int kG = sizeof(T) == 4 ? 2 : 4;
+  if (rows <= kFewRows)
+    norm_rope_kernel<T, 1><<<kv_blocks + blocks(rows), kRowThreads, 0, s>>>(p, kv_blocks, fault);
+  else
+    norm_rope_kernel<T, kG><<<kv_blocks + min(blocks((rows + kG - 1) / kG), 1 << 14), kRowThreads, 0, s>>>(p, kv_blocks, fault);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s) {
-  auto blocks = [](long long rows) { return int((rows + kRowWarps - 1) / kRowWarps); };
-  const int kv_blocks = p.kv != nullptr ? min(blocks(p.tokens), 1 << 14) : 0;
-  const int q_blocks = p.q != nullptr ? min(blocks((long long)p.tokens * p.heads), 1 << 14) : 0;
-  auto* kernel = p.in_type == QSFM_F32   ? norm_rope_kernel<float>
-                 : p.in_type == QSFM_F16 ? norm_rope_kernel<__half>
-                                         : norm_rope_kernel<__nv_bfloat16>;
-  kernel<<<kv_blocks + q_blocks, kRowThreads, 0, s>>>(p, kv_blocks, fault);
+  if (p.in_type == QSFM_F32) launch_rows<float>(p, fault, s);
+  else if (p.in_type == QSFM_F16) launch_rows<__half>(p, fault, s);
+  else launch_rows<__nv_bfloat16>(p, fault, s);
   return cudaGetLastError();
 }
 

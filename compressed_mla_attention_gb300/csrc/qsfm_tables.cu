@@ -11,15 +11,17 @@
 // the blocks given back in order", so each output element follows from the
 // three prefix sums alone and no thread waits for another's write.
 //
-// One launch of one cluster: every CTA computes the prefix sums over the
-// batch for itself (8 KB to 100 KB of shared memory; the lengths come from L2)
-// and takes a share of the output elements, each of which finds its request
-// by a binary search in shared memory. The cluster barrier separates the
-// reads of free_count from its update in place. Everything else is read and
-// written at disjoint places: columns below h_b are read, columns from h_b on
-// written; entries below the count are read, entries from it on written.
-// Bound by latency: the launch, one round trip for the lengths, the scan, the
-// search and one or two round trips for a block id.
+// Every CTA computes the prefix sums over the batch for itself (up to 160 KB of
+// shared memory; the lengths come from L2) and takes a share of the output
+// elements: a thread has four consecutive new rows at a time, finds the request
+// of the first by a binary search in shared memory and stores 16 bytes. Reads
+// and writes are of disjoint places: columns below h_b are read, columns from
+// h_b on written; free entries below the count are read, entries from it on
+// written. Only free_count itself is both, so with more than one CTA its update
+// in place is a launch of its own (one CTA, the sums again).
+// Bound by latency up to some ten thousand rows (the launch, one round trip for
+// the lengths, the scan, the search and one or two round trips for a block id),
+// then by the stores.
 #include <cub/block/block_scan.cuh>
 #include <cuda_runtime.h>
 
@@ -30,7 +32,10 @@ namespace qsfm {
 namespace {
 
 constexpr int kTabThreads = 512;
-constexpr int kTabMaxCtas = 8;  // the portable cluster size
+constexpr int kTabRows = 4;  // consecutive rows of a thread
+// Rows one CTA takes alone: more CTAs read the lengths as often, and an update
+// in place costs a second launch.
+constexpr int kTabAlone = 4 * kTabThreads * kTabRows;
 
 // Prefix sums; the row counts of absurd lengths stop at the largest int (the
 // table has at most 2^30 entries, so the block counts cannot pass it).
@@ -56,7 +61,10 @@ __device__ __forceinline__ int find_request(const int* at, int n, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_block_table_params p, int* fault) {
+// update: 0 leaves free_count alone, 1 updates it (and free_count_out), 2 does
+// nothing else.
+__global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_block_table_params p, const int update,
+                                                                  int* fault) {
   using Scan = cub::BlockScan<Sums, kTabThreads>;
   __shared__ typename Scan::TempStorage scan_tmp;
   extern __shared__ int s_dyn[];
@@ -76,7 +84,7 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
   for (int b = b0; b < b1; ++b) {
     const int n0 = max(0, __ldg(p.prev_lens + b)), n1 = max(0, __ldg(p.lens + b));
     int prev = n0 / p.cmp_ratio, rows = n1 / p.cmp_ratio;
-    if (cta == 0 && p.residual != nullptr) p.residual[b] = n1 - rows * p.cmp_ratio;
+    if (cta == 0 && update < 2 && p.residual != nullptr) p.residual[b] = n1 - rows * p.cmp_ratio;
     wide |= prev > cap_rows || rows > cap_rows;
     // a table row that is too narrow: its last columns are missing, the rows
     // behind them get slots of -1
@@ -90,37 +98,30 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
     mine.taken += max(0, need - held);
     mine.given += max(0, held - need);
   }
-  if (wide && cta == 0) atomicOr(fault, QSFM_FAULT_ORI_TABLE_COL);
+  if (wide && cta == 0 && update < 2) atomicOr(fault, QSFM_FAULT_ORI_TABLE_COL);
   Sums before, total;
   Scan(scan_tmp).ExclusiveScan(mine, before, Sums{0, 0, 0}, AddSums(), total);
   for (int b = b0; b < b1; ++b) {
     s_rows[b] = add_rows(s_rows[b], before.rows);
     s_taken[b] += before.taken;
     s_given[b] += before.given;
-    if (cta == 0 && p.cu_rows != nullptr) p.cu_rows[b] = s_rows[b];
+    if (cta == 0 && update < 2 && p.cu_rows != nullptr) p.cu_rows[b] = s_rows[b];
   }
   __syncthreads();
 
   const int count = max(0, min(stack, p.free_capacity));
   const long long left = (long long)count + total.given - total.taken;  // negative: the pool is short
   if (cta == 0 && tid == 0) {
-    if (p.cu_rows != nullptr) p.cu_rows[p.batch] = total.rows;
-    if (left < 0 || left > p.free_capacity || stack != count) atomicOr(fault, QSFM_FAULT_BLOCK_POOL);
-    if (total.rows > p.max_rows) atomicOr(fault, QSFM_FAULT_SLOT);
-  }
-  if (ctas > 1) {  // every CTA has read the count
-    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
-  }
-  if (cta == 0 && tid == 0)
-    *(p.free_count_out != nullptr ? p.free_count_out : p.free_count) =
-        int(left < 0 ? 0 : left > p.free_capacity ? p.free_capacity : left);
-  if (p.batch == 0) {
-    for (int i = cta * kTabThreads + tid; i < p.max_rows; i += ctas * kTabThreads) {
-      p.slot_map[i] = -1;
-      if (p.positions != nullptr) p.positions[i] = -1;
+    if (update < 2) {
+      if (p.cu_rows != nullptr) p.cu_rows[p.batch] = total.rows;
+      if (left < 0 || left > p.free_capacity || stack != count) atomicOr(fault, QSFM_FAULT_BLOCK_POOL);
+      if (total.rows > p.max_rows) atomicOr(fault, QSFM_FAULT_SLOT);
     }
-    return;
+    if (update > 0)
+      *(p.free_count_out != nullptr ? p.free_count_out : p.free_count) =
+          int(left < 0 ? 0 : left > p.free_capacity ? p.free_capacity : left);
   }
+  if (update == 2) return;
 
   // the i-th block given back, and the i-th taken (-1: none left)
   auto given_block = [&](int i) {
@@ -141,21 +142,49 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
   };
 
   const int step = ctas * kTabThreads;
-  for (int i = cta * kTabThreads + tid; i < p.max_rows; i += step) {
-    int slot = -1, pos = -1;
-    if (i < total.rows) {
-      const int b = find_request(s_rows, p.batch, i);
+  const bool vec = ((reinterpret_cast<uintptr_t>(p.slot_map) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
+  for (int i0 = kTabRows * (cta * kTabThreads + tid); i0 < p.max_rows; i0 += kTabRows * step) {
+    int slot[kTabRows], pos[kTabRows];
+    int b = 0, next = 0, col_of = -1, block = -1;  // request of the row, start of the next, the block at hand
+    if (i0 < total.rows) {
+      b = find_request(s_rows, p.batch, i0);
+      next = b + 1 < p.batch ? s_rows[b + 1] : total.rows;
+    }
+#pragma unroll
+    for (int k = 0; k < kTabRows; ++k) {
+      const int i = i0 + k;
+      slot[k] = -1;
+      pos[k] = -1;
+      if (i >= total.rows) continue;
+      while (i >= next) {  // empty requests are passed over; i < total.rows ends it
+        ++b;
+        next = b + 1 < p.batch ? s_rows[b + 1] : total.rows;
+        col_of = -1;
+      }
       const int row = s_prev[b] + (i - s_rows[b]);
-      const int col = row / kBlock, held = held_of(b);
-      pos = row * p.cmp_ratio;
-      if (col < p.max_blocks) {
-        const int block = checked(col < held ? p.block_table[size_t(b) * p.max_blocks + col]
-                                             : taken_block(s_taken[b] + col - held));
-        if (block >= 0) slot = block * kBlock + row % kBlock;
+      const int col = row / kBlock;
+      pos[k] = row * p.cmp_ratio;
+      if (col >= p.max_blocks) continue;
+      if (col != col_of) {
+        const int held = held_of(b);
+        block = checked(col < held ? p.block_table[size_t(b) * p.max_blocks + col]
+                                   : taken_block(s_taken[b] + col - held));
+        col_of = col;
+      }
+      if (block >= 0) slot[k] = block * kBlock + row % kBlock;
+    }
+    if (vec && i0 + kTabRows <= p.max_rows) {
+      *reinterpret_cast<int4*>(p.slot_map + i0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+      if (p.positions != nullptr)
+        *reinterpret_cast<int4*>(p.positions + i0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTabRows; ++k) {
+        if (i0 + k >= p.max_rows) break;
+        p.slot_map[i0 + k] = slot[k];
+        if (p.positions != nullptr) p.positions[i0 + k] = pos[k];
       }
     }
-    p.slot_map[i] = slot;
-    if (p.positions != nullptr) p.positions[i] = pos;
   }
   for (int i = cta * kTabThreads + tid; i < total.taken; i += step) {
     const int b = find_request(s_taken, p.batch, i);
@@ -173,21 +202,21 @@ cudaError_t launch_block_tables(const qsfm_block_table_params& p, int* fault, cu
   cudaError_t e = cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        5 * 8192 * int(sizeof(int)));
   if (e != cudaSuccess) return e;
-  const int work = p.max_rows > 2 * p.batch ? p.max_rows : 2 * p.batch;
   int ctas = 1;
-  while (ctas < kTabMaxCtas && ctas * kTabThreads < work) ctas *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTabThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, block_table_kernel, p, fault);
+  if (p.max_rows > kTabAlone) {
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int per = kTabThreads * kTabRows;
+    ctas = (p.max_rows + per - 1) / per;
+    if (ctas > 2 * sms) ctas = 2 * sms;
+  }
+  const bool in_place = p.free_count_out == nullptr || p.free_count_out == p.free_count;
+  const int update = ctas > 1 && in_place ? 0 : 1;
+  block_table_kernel<<<ctas, kTabThreads, smem, s>>>(p, update, fault);
+  if (update == 0) block_table_kernel<<<1, kTabThreads, smem, s>>>(p, 2, fault);
+  return cudaGetLastError();
 }
 
 }  // namespace qsfm

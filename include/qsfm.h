@@ -173,7 +173,8 @@ typedef enum {
 /*
  * All inputs, attributes and outputs of one forward call. Pointers are
  * device pointers; NULL marks an absent optional input. q, ori_kv, cmp_kv and
- * attn_out must be 16-byte aligned and every other pointer 4-byte aligned
+ * attn_out must be 16-byte aligned (packed384 ori_kv and cmp_kv 32-byte
+ * aligned) and every other pointer 4-byte aligned
  * (QSFM_ERR_INVALID_ARG otherwise). The parameter names follow
  * QuantSparseFlashMla, "参数说明" (parameter table).
  * Size limits of the kernels' 32-bit index arithmetic (QSFM_ERR_UNSUPPORTED
