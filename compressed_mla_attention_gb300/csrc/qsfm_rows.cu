@@ -7,13 +7,13 @@
 // row format (bf16, e4m3 with fp32 or e8m0 scales, e2m1 with e4m3 scales).
 //
 // One warp per row: lane l holds elements 8 l .. + 7 of each 256-element half
-// (two 16-byte loads of a bf16 row), so the sum of squares is five shuffles,
+// (two 16-byte vectors of a bf16 row), so the sum of squares is five shuffles,
 // the pairs of a rotation are in the lane (adjacent) or rope_dim / 16 lanes
 // apart (halves), and a quantisation group of 16 or 64 elements is 2 or 8
-// neighbouring lanes. A row is read once, held in registers and written once:
-// the kernel moves the bytes it cannot do without and is bound by HBM for
-// long inputs, by latency for single tokens. The key rows, which take longer,
-// are the first warps of the grid.
+// neighbouring lanes. A row is read once, held in registers and written once.
+// Query rows are bound by HBM, so what counts is bytes in flight: a warp streams
+// its rows through a ring in shared memory. The key rows are few; they are the
+// first blocks of the grid, one warp each, bound by latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -27,7 +27,12 @@ namespace {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kFewRows = 152 * 16;  // query rows up to which a warp has one
+constexpr int kRowBlocks = 3;  // blocks of query rows on an SM
+// query rows a warp has in flight: 8 KB (1 KB a row, fp32 2 KB)
+template <typename T>
+constexpr int stages() {
+  return sizeof(T) == 4 ? 4 : 8;
+}
 constexpr uint32_t kAll = 0xffffffffu;
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
@@ -72,9 +77,10 @@ __device__ __forceinline__ void load8(const T* src, float (&f)[8]) {
   raw.get(f);
 }
 
+// (streaming: the rows are not read again here; 256 tokens 7.4 -> 6.3 us)
 __device__ __forceinline__ void store8_bf16(__nv_bfloat16* dst, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(dst) =
-      make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7]));
+  __stcs(reinterpret_cast<uint4*>(dst),
+      make_uint4(bf16x2(v[0], v[1]), bf16x2(v[2], v[3]), bf16x2(v[4], v[5]), bf16x2(v[6], v[7])));
 }
 
 // The lane's weights (ones without a weight tensor).
@@ -93,9 +99,57 @@ __device__ __forceinline__ void load_weights(const void* w, bool bf16, int lane,
   }
 }
 
+// The lane's cosines and sines for a token: interleaved pairs use four of each,
+// halves eight. `h`: the half row that holds the rotated range (a range never
+// crosses the middle: it starts at a multiple of its power-of-two length).
+struct Turn {
+  float c[8], s[8];
+};
+__device__ __forceinline__ int rotated_half(const qsfm_norm_rope_params& p) { return p.rope_offset >> 8; }
+__device__ __forceinline__ int rotated_element(const qsfm_norm_rope_params& p, int lane) {
+  return 8 * lane + (p.rope_offset & ~255) - p.rope_offset;  // the lane's first, counted from the range's start
+}
+__device__ __forceinline__ void load_turn(const qsfm_norm_rope_params& p, int pos, int lane, Turn& t) {
+  const int r = rotated_element(p, lane), half = p.rope_dim / 2;
+  if (r < 0 || r >= p.rope_dim) return;
+  const float* table = p.cos_sin + size_t(pos) * p.rope_dim;
+  if (p.interleaved) {
+    const float4 c = *reinterpret_cast<const float4*>(table + r / 2);
+    const float4 s = *reinterpret_cast<const float4*>(table + half + r / 2);
+    t.c[0] = c.x; t.c[1] = c.y; t.c[2] = c.z; t.c[3] = c.w;
+    t.s[0] = s.x; t.s[1] = s.y; t.s[2] = s.z; t.s[3] = s.w;
+  } else {
+    const int k = r >= half ? r - half : r;
+    load8(table + k, t.c);
+    load8(table + half + k, t.s);
+  }
+}
+__device__ __forceinline__ void turn8(const qsfm_norm_rope_params& p, int lane, const Turn& t, float (&y)[8]) {
+  const int r = rotated_element(p, lane);
+  const bool in = r >= 0 && r < p.rope_dim;
+  if (p.interleaved) {
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = y[2 * i], b = y[2 * i + 1];
+        y[2 * i] = a * t.c[i] - b * t.s[i];
+        y[2 * i + 1] = b * t.c[i] + a * t.s[i];
+      }
+    }
+  } else {
+    // the other half's lane is this lane with one bit flipped
+    const bool upper = r >= p.rope_dim / 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(kAll, y[i], p.rope_dim / 16);
+      if (in) y[i] = upper ? y[i] * t.c[i] + other * t.s[i] : y[i] * t.c[i] - other * t.s[i];
+    }
+  }
+}
+
 // Norm and rotation of the row held by the warp.
 __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bool norm, const float (&w)[2][8],
-                                              int pos, int lane, float (&y)[2][8]) {
+                                              const Turn& turn, int lane, float (&y)[2][8]) {
   if (norm) {
     float sum = 0.f;
 #pragma unroll
@@ -111,39 +165,8 @@ __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bo
       for (int i = 0; i < 8; ++i) y[h][i] *= inv * w[h][i];
   }
   if (p.rope_dim == 0) return;
-  const float* table = p.cos_sin + size_t(pos) * p.rope_dim;
-  const int half = p.rope_dim / 2;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int r = 256 * h + 8 * lane - p.rope_offset;  // the lane's first element in the rotated range
-    const bool in = r >= 0 && r < p.rope_dim;
-    if (p.interleaved) {
-      if (in) {
-        const float4 c = *reinterpret_cast<const float4*>(table + r / 2);
-        const float4 s = *reinterpret_cast<const float4*>(table + half + r / 2);
-        const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float a = y[h][2 * i], b = y[h][2 * i + 1];
-          y[h][2 * i] = a * cs[i] - b * sn[i];
-          y[h][2 * i + 1] = b * cs[i] + a * sn[i];
-        }
-      }
-    } else if (__any_sync(kAll, in)) {
-      // the range starts at a multiple of its (power of two) length, so the
-      // other half's lane is this lane with one bit flipped, in the same h
-      const bool upper = r >= half;
-      const int k = in ? (upper ? r - half : r) : 0;
-      float cs[8], sn[8];
-      load8(table + k, cs);
-      load8(table + half + k, sn);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float other = __shfl_xor_sync(kAll, y[h][i], p.rope_dim / 16);
-        if (in) y[h][i] = upper ? y[h][i] * cs[i] + other * sn[i] : y[h][i] * cs[i] - other * sn[i];
-      }
-    }
-  }
+  if (rotated_half(p) == 0) turn8(p, lane, turn, y[0]);
+  else turn8(p, lane, turn, y[1]);
 }
 
 __device__ __forceinline__ float max8(const float (&v)[8]) {
@@ -312,107 +335,157 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
   if (put && lane == 0) *reinterpret_cast<uint32_t*>(row + 380) = uint32_t(127 + e);
 }
 
-// The token's position; false: nothing of the token is read or written.
-__device__ __forceinline__ bool token_position(const qsfm_norm_rope_params& p, int t, int* fault, int& pos) {
-  pos = p.positions != nullptr ? __ldg(p.positions + t) : 0;
+__device__ __forceinline__ int position_of(const qsfm_norm_rope_params& p, int t) {
+  return p.positions != nullptr ? __ldg(p.positions + t) : 0;
+}
+// False: nothing is written for the token (padding, or a position past the table).
+__device__ __forceinline__ bool position_ok(const qsfm_norm_rope_params& p, int pos, int lane, int* fault) {
   if (pos < 0) return false;
   if (p.rope_dim != 0 && pos >= p.max_positions) {
-    atomicOr(fault, QSFM_FAULT_POSITION);
+    if (lane == 0) atomicOr(fault, QSFM_FAULT_POSITION);
     return false;
   }
   return true;
 }
 
-// kG query rows per warp and turn: their loads are in flight together.
-template <typename T, int kG>
-__global__ void __launch_bounds__(kRowThreads) norm_rope_kernel(const qsfm_norm_rope_params p, const int kv_blocks,
-                                                                int* fault) {
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Blocks 0 .. kv_blocks - 1: one key row per warp, its input, position and slot
+// requested together. The others: query rows, `per` consecutive ones per block.
+// A warp streams them through a ring of its own in shared memory, kStages rows
+// in flight (asynchronous copies; each lane reads back only what it copied, so
+// no barrier), and keeps the token's cosines and sines from head to head.
+// Without queries (kQueries false) the key rows take fewer registers, so that
+// more of them are in flight: 8191 fp32 rows in 8.7 us instead of 10.4.
+template <typename T, bool kQueries>
+__global__ void __launch_bounds__(kRowThreads, kQueries ? kRowBlocks : 4) norm_rope_kernel(const qsfm_norm_rope_params p, const int kv_blocks,
+                                                                const int per, int* fault) {
+  extern __shared__ __align__(16) uint8_t s_rows[];
+  constexpr int kStages = stages<T>();
+  constexpr int kVec = sizeof(T) / 2;  // 16-byte vectors of 8 elements
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float w[2][8];
-  if (int(blockIdx.x) < kv_blocks) {
+  float w[2][8], y[2][8];
+  Turn turn;
+  if (!kQueries || int(blockIdx.x) < kv_blocks) {
+    const int t = blockIdx.x * kRowWarps + warp;
+    if (t >= p.tokens) return;
+    const T* src = static_cast<const T*>(p.kv) + size_t(t) * p.kv_token_stride + 8 * lane;
+    const int pos = position_of(p, t);
+    int slot = p.kv_cache != nullptr ? __ldg(p.slot_map + t) : -1;
+    Raw<T> raw[2];
+    raw[0].load(src);
+    raw[1].load(src + 256);
     load_weights(p.kv_weight, p.weights_bf16 != 0, lane, w);
-    for (int t = blockIdx.x * kRowWarps + warp; t < p.tokens; t += kv_blocks * kRowWarps) {
-      int pos;
-      if (!token_position(p, t, fault, pos)) continue;
-      float y[2][8];
-      const T* src = static_cast<const T*>(p.kv) + size_t(t) * p.kv_token_stride + 8 * lane;
-      load8(src, y[0]);
-      load8(src + 256, y[1]);
-      int slot = p.kv_cache != nullptr ? __ldg(p.slot_map + t) : -1;
-      norm_rope_row(p, p.norm_kv != 0, w, pos, lane, y);
-      if (slot >= 0 && (slot >> 7) >= p.num_blocks) {
-        atomicOr(fault, QSFM_FAULT_SLOT);
-        slot = -1;
-      }
-      store_row(p, slot, lane, y);
-      if (p.kv_out != nullptr) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.kv_out) + size_t(t) * kDim + 8 * lane;
-        store8_bf16(out, y[0]);
-        store8_bf16(out + 256, y[1]);
-      }
+    if (!position_ok(p, pos, lane, fault)) return;
+    if (p.rope_dim != 0) load_turn(p, pos, lane, turn);
+    raw[0].get(y[0]);
+    raw[1].get(y[1]);
+    norm_rope_row(p, p.norm_kv != 0, w, turn, lane, y);
+    if (slot >= 0 && (slot >> 7) >= p.num_blocks) {
+      if (lane == 0) atomicOr(fault, QSFM_FAULT_SLOT);
+      slot = -1;
+    }
+    store_row(p, slot, lane, y);
+    if (p.kv_out != nullptr) {
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.kv_out) + size_t(t) * kDim + 8 * lane;
+      store8_bf16(out, y[0]);
+      store8_bf16(out + 256, y[1]);
     }
     return;
   }
-  load_weights(p.q_weight, p.weights_bf16 != 0, lane, w);
-  const int rows = p.tokens * p.heads, step = (gridDim.x - kv_blocks) * kRowWarps * kG;
-  for (int r0 = ((blockIdx.x - kv_blocks) * kRowWarps + warp) * kG; r0 < rows; r0 += step) {
-    Raw<T> raw[kG][2];
-    int pos[kG];
-    bool live[kG];
-    const int t0 = r0 / p.heads, head0 = r0 - t0 * p.heads;
+  const int rows = p.tokens * p.heads;
+  // `per` rows of the block, its warps side by side: a turn of the block is
+  // contiguous where q is
+  const int b0 = (blockIdx.x - kv_blocks) * per, r0 = b0 + warp, r1 = min(rows, b0 + per);
+  if (r0 >= r1) return;
+  // row r as (token, head), advanced by the block's warps
+  int t_in = r0 / p.heads, head_in = r0 - t_in * p.heads;
+  int t = t_in, head = head_in;
+  const uint32_t ring = smem_u32(s_rows) + uint32_t(warp * kStages) * kDim * sizeof(T) + 16 * lane;
+  auto request = [&](int r) {
+    if (r < r1) {
+      const T* src = static_cast<const T*>(p.q) + size_t(t_in) * p.q_token_stride + size_t(head_in) * p.q_head_stride + 8 * lane;
+      const uint32_t dst = ring + uint32_t((r - r0) / kRowWarps % kStages) * kDim * sizeof(T);
 #pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      int t = t0, head = head0 + g;
-      while (head >= p.heads) {  // at most kG turns
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          copy_async16(dst + uint32_t(h * kVec + i) * 512, reinterpret_cast<const uint4*>(src + 256 * h) + i);
+      head_in += kRowWarps;
+      while (head_in >= p.heads) {
+        head_in -= p.heads;
+        ++t_in;
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) request(r0 + i * kRowWarps);
+  int pos = position_of(p, t);
+  load_weights(p.q_weight, p.weights_bf16 != 0, lane, w);
+  bool ok = position_ok(p, pos, lane, fault);
+  if (ok && p.rope_dim != 0) load_turn(p, pos, lane, turn);
+  for (int r = r0; r < r1; r += kRowWarps) {
+    request(r + (kStages - 1) * kRowWarps);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    if (ok) {
+      const uint32_t src = ring + uint32_t((r - r0) / kRowWarps % kStages) * kDim * sizeof(T);
+      Raw<T> raw[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) raw[h].v[i] = lds_v4(src + uint32_t(h * kVec + i) * 512);
+      raw[0].get(y[0]);
+      raw[1].get(y[1]);
+      norm_rope_row(p, p.norm_q != 0, w, turn, lane, y);
+      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q_out) + size_t(r) * kDim + 8 * lane;
+      store8_bf16(out, y[0]);
+      store8_bf16(out + 256, y[1]);
+    }
+    head += kRowWarps;
+    if (head >= p.heads && r + kRowWarps < r1) {
+      while (head >= p.heads) {
         head -= p.heads;
         ++t;
       }
-      live[g] = r0 + g < rows;
-      if (!live[g]) continue;
-      pos[g] = p.positions != nullptr ? __ldg(p.positions + t) : 0;
-      const T* src = static_cast<const T*>(p.q) + size_t(t) * p.q_token_stride + size_t(head) * p.q_head_stride + 8 * lane;
-      raw[g][0].load(src);
-      raw[g][1].load(src + 256);
-    }
-#pragma unroll
-    for (int g = 0; g < kG; ++g) {
-      if (!live[g] || pos[g] < 0) continue;
-      if (p.rope_dim != 0 && pos[g] >= p.max_positions) {
-        if (lane == 0) atomicOr(fault, QSFM_FAULT_POSITION);
-        continue;
-      }
-      float y[2][8];
-      raw[g][0].get(y[0]);
-      raw[g][1].get(y[1]);
-      norm_rope_row(p, p.norm_q != 0, w, pos[g], lane, y);
-      __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.q_out) + size_t(r0 + g) * kDim + 8 * lane;
-      store8_bf16(out, y[0]);
-      store8_bf16(out + 256, y[1]);
+      pos = position_of(p, t);
+      ok = position_ok(p, pos, lane, fault);
+      if (ok && p.rope_dim != 0) load_turn(p, pos, lane, turn);
     }
   }
 }
 
 template <typename T>
-void launch_rows(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s) {
-  auto blocks = [](long long warps) { return int((warps + kRowWarps - 1) / kRowWarps); };
-  const int kv_blocks = p.kv != nullptr ? min(blocks(p.tokens), 1 << 14) : 0;
-  const long long rows = p.q != nullptr ? (long long)p.tokens * p.heads : 0;
-  // Few rows: one per warp, as many warps as rows (latency). Many: four per
-  // turn (two of fp32), so that a warp's loads overlap.
-  constexpr int kG = sizeof(T) == 4 ? 2 : 4;
-  if (rows <= kFewRows)
-    norm_rope_kernel<T, 1><<<kv_blocks + blocks(rows), kRowThreads, 0, s>>>(p, kv_blocks, fault);
-  else
-    norm_rope_kernel<T, kG><<<kv_blocks + min(blocks((rows + kG - 1) / kG), 1 << 14), kRowThreads, 0, s>>>(p, kv_blocks, fault);
+cudaError_t launch_rows(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s) {
+  const int kv_blocks = p.kv != nullptr ? (p.tokens + kRowWarps - 1) / kRowWarps : 0;
+  if (p.q == nullptr) {
+    norm_rope_kernel<T, false><<<kv_blocks, kRowThreads, 0, s>>>(p, kv_blocks, 0, fault);
+    return cudaGetLastError();
+  }
+  constexpr int kSmem = kRowWarps * stages<T>() * kDim * int(sizeof(T));
+  cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  int dev = 0, sms = 0;
+  if (e == cudaSuccess) e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const int rows = p.tokens * p.heads;
+  // as many blocks of query rows as run at once, and their share of the rows
+  const int blocks = sms * kRowBlocks;
+  int per = (rows + blocks - 1) / blocks;
+  per = (per + kRowWarps - 1) / kRowWarps * kRowWarps;
+  const int q_blocks = (rows + per - 1) / per;
+  norm_rope_kernel<T, true><<<kv_blocks + q_blocks, kRowThreads, kSmem, s>>>(p, kv_blocks, per, fault);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s) {
-  if (p.in_type == QSFM_F32) launch_rows<float>(p, fault, s);
-  else if (p.in_type == QSFM_F16) launch_rows<__half>(p, fault, s);
-  else launch_rows<__nv_bfloat16>(p, fault, s);
-  return cudaGetLastError();
+  return p.in_type == QSFM_F32   ? launch_rows<float>(p, fault, s)
+         : p.in_type == QSFM_F16 ? launch_rows<__half>(p, fault, s)
+                                 : launch_rows<__nv_bfloat16>(p, fault, s);
 }
 
 }  // namespace qsfm

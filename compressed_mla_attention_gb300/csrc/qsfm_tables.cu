@@ -65,7 +65,7 @@ __device__ __forceinline__ int find_request(const int* at, int n, int i) {
 // nothing else.
 __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_block_table_params p, const int update,
                                                                   int* fault) {
-  using Scan = cub::BlockScan<Sums, kTabThreads>;
+  using Scan = cub::BlockScan<Sums, kTabThreads, cub::BLOCK_SCAN_WARP_SCANS>;
   __shared__ typename Scan::TempStorage scan_tmp;
   extern __shared__ int s_dyn[];
   int* s_rows = s_dyn;             // N_b
@@ -141,9 +141,12 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
     return block;
   };
 
-  const int step = ctas * kTabThreads;
+  // Rows, taken and returned blocks start at different warps, so that their
+  // dependent loads overlap when there are few of each.
+  const int step = ctas * kTabThreads, me = cta * kTabThreads + tid;
+  const int me_taken = me >= step / 2 ? me - step / 2 : me + step / 2, me_given = step - 1 - me;
   const bool vec = ((reinterpret_cast<uintptr_t>(p.slot_map) | reinterpret_cast<uintptr_t>(p.positions)) & 15) == 0;
-  for (int i0 = kTabRows * (cta * kTabThreads + tid); i0 < p.max_rows; i0 += kTabRows * step) {
+  for (int i0 = kTabRows * me; i0 < p.max_rows; i0 += kTabRows * step) {
     int slot[kTabRows], pos[kTabRows];
     int b = 0, next = 0, col_of = -1, block = -1;  // request of the row, start of the next, the block at hand
     if (i0 < total.rows) {
@@ -186,13 +189,13 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
       }
     }
   }
-  for (int i = cta * kTabThreads + tid; i < total.taken; i += step) {
+  for (int i = me_taken; i < total.taken; i += step) {
     const int b = find_request(s_taken, p.batch, i);
     p.block_table[size_t(b) * p.max_blocks + held_of(b) + (i - s_taken[b])] = checked(taken_block(i));
   }
   // blocks given back and not taken again go onto the free list
   const int pushed = min(max(0, total.given - total.taken), p.free_capacity - count);
-  for (int i = cta * kTabThreads + tid; i < pushed; i += step) p.free_list[count + i] = given_block(i);
+  for (int i = me_given; i < pushed; i += step) p.free_list[count + i] = given_block(i);
 }
 
 }  // namespace

@@ -478,8 +478,8 @@ qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* p, void* workspace
  *              e4m3(y / scale)
  *   A scale group with an element that is not finite stores a scale of NaN
  *   (packed formats); the other groups are as without it.
- * A token whose position is negative is padding: nothing of it is read or
- * written. A slot that is negative stores no row (q_out and kv_out are
+ * A token whose position is negative is padding: nothing is written for it. A
+ * slot that is negative stores no row (q_out and kv_out are
  * written); each slot is named by at most one token (of two, the row's bytes
  * are a mixture). A position past the table skips the token
  * (QSFM_FAULT_POSITION), a slot past the cache the store (QSFM_FAULT_SLOT).
