@@ -19,12 +19,16 @@
 //                registers ahead of PV freeing their places, so that only
 //                their stores follow;
 //   warp 16      MMA issue (one thread);
-//   warp 17      resolver (18 and 19 only complete the warpgroup).
+//   warp 17      resolver: walks the CTA's pieces (work units, or parts of one)
+//                and publishes them and their tiles' rows in two rings, so that
+//                no other warp waits for a length or an index (18 and 19 only
+//                complete the warpgroup).
 // Chain per tile: PV(n) frees chunk pairs -> stores of tile n + 1 -> QK^T(n + 1)
-// chunk by chunk -> softmax(n + 1) -> PV(n + 1). The epilogue of a unit runs on
-// the softmax warps while the next unit's first tile is stored and multiplied,
-// and the next unit's q is requested as soon as the last score product of the
-// unit has completed.
+// chunk by chunk -> softmax(n + 1) -> PV(n + 1). A unit's output is read, scaled
+// and written after the next unit's first P is on its way: O^T takes four of
+// seven blocks of tensor memory, the next unit's the following four (modulo
+// seven), so its PV waits only for the first chunk to be read. The next unit's q
+// is requested as soon as the last score product of the unit has completed.
 #include "qsfm_attention_common.cuh"
 
 namespace qsfm {
@@ -42,7 +46,6 @@ constexpr int kPrRegs = 112, kLastRegs = 64;
 static_assert(kSmThreads * 96 + kPrWarps * 32 * kPrRegs + 128 * kLastRegs <= kThreads * 96, "register split");
 constexpr int kHPT = 32;                     // heads per softmax thread
 constexpr int kBarSm = 1;                    // named barrier of the softmax warps
-constexpr int kBarSlab = 2;                  // [2]: of the four warps that write a slab of the output
 constexpr int kRowB = QSFM_PACKED384_ROW_BYTES;
 
 // shared memory map (byte offsets from a 1024-aligned base)
@@ -51,17 +54,18 @@ constexpr uint32_t kSK = 0;                                   // K~ tile: 8 slab
 constexpr uint32_t kSQ = kSK + 8 * kSlabBytes;                // Q: 8 d-blocks x 64 heads x 128 B
 constexpr uint32_t kSP = kSQ + 8 * 64 * 128;                  // P: 128 rows x 64 heads (bf16)
 constexpr uint32_t kSRows = kSP + kTileRows * 128;            // [8][128] i32 physical rows
-constexpr uint32_t kSRowKind = kSRows + 8 * kTileRows * 4;    // [8] i32: 0 ori, 1 cmp, -1 end
-constexpr uint32_t kSValid = kSRowKind + 64;                  // [128] i32: row of the tile valid
+constexpr uint32_t kSTile = kSRows + 8 * kTileRows * 4;       // [8] i32: what the ring slot holds
+constexpr uint32_t kSPiece = kSTile + 32;                     // [8] pieces, then the one being handed over
+constexpr uint32_t kSValid = kSPiece + 9 * 16 + 16;           // [128] i32: row of the tile valid
 constexpr uint32_t kSRed = kSValid + kTileRows * 4;           // [4][64] f32 per-quadrant partials
 constexpr uint32_t kSMUsed = kSRed + 1024;                    // [64] f32
 constexpr uint32_t kSAlpha = kSMUsed + 256;                   // [64] f32
-constexpr uint32_t kSInv = kSAlpha + 256;                     // [64] f32
-constexpr uint32_t kSAny = kSInv + 256;                       // [4] i32: a row of the quadrant valid
+constexpr uint32_t kSInv = kSAlpha + 256;                     // [2][64] f32: by the unit's parity
+constexpr uint32_t kSSink = kSInv + 512;                      // [128] f32: the heads' sinks, log2 units
+constexpr uint32_t kSAny = kSSink + 512;                      // [4] i32: a row of the quadrant valid
 constexpr uint32_t kSBar = kSAny + 16;                        // mbarriers, tmem base, flags
-constexpr uint32_t kSmemBytes = kSBar + 256;
-// staging of the output: P's place as two slabs [64 heads][64 d] (bf16, 128-byte swizzle)
-constexpr uint32_t kSStage = kSP;
+constexpr uint32_t kSmemBytes = kSBar + 384;
+static_assert(kSValid % 16 == 0 && kSAny % 16 == 0 && kSBar % 16 == 0, "alignment");
 constexpr uint32_t kSmemAlloc = kSmemBytes + 1024;
 static_assert(kSmemAlloc <= 232448, "more than the 227 KB a CTA may use");
 
@@ -71,33 +75,47 @@ constexpr int kBarFull = 1;        // [chunk]: stored (one arrive per producer w
 constexpr int kBarFree = 5;        // [chunk pair]: PV of chunks 2i, 2i + 1 completed (commit)
 constexpr int kBarSFull = 7;       // S^T of the tile complete (commit)
 constexpr int kBarPFull = 8;       // P of the tile written (one arrive per softmax warp)
-constexpr int kBarOFree = 9;       // O^T read by the epilogue (one arrive per softmax warp)
+constexpr int kBarOFree = 9;       // chunk 0 of O^T read by the epilogue (one arrive per softmax warp)
 constexpr int kBarDrain = 10;      // every MMA of the CTA completed (commit)
 
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemS = 0;
-constexpr uint32_t kTmemO = 256;  // + 64 * chunk
+// O^T of the CTA's i-th piece with tiles: chunk c in columns 64 .. 127 of block
+// (4 i + c) mod 7 behind S^T
+__device__ __forceinline__ uint32_t o_column(uint32_t piece, int c) { return 64 + 64 * ((4 * piece + uint32_t(c)) % 7); }
 constexpr float kGuessLog2 = 60.0f;  // below a guessed maximum
 constexpr uint32_t kIdescQK = make_idesc_bf16(128, 64, /*a_mn=*/0, /*b_mn=*/0);
 constexpr uint32_t kIdescPV = make_idesc_bf16(128, 64, /*a_mn=*/1, /*b_mn=*/1);
 
+// What the resolver says of a ring slot (a KV tile): its pool, and its place in
+// the piece; or the end.
+constexpr int kTileEnd = -1, kTileCmp = 1, kTileFirst = 2, kTileLast = 4;
+// A piece: tiles of a work unit (none: a unit without rows), all or a part of
+// them; unit -1: the end.
+struct __align__(16) Piece {
+  int unit, tiles, whole, unused;
+};
+
 struct Smem {
-  static constexpr int kRing = 8;           // tiles of resolved rows in flight
-  static constexpr int kBarRowsFull = 11;   // [ring slot]
-  static constexpr int kBarRowsEmpty = 19;  // [ring slot], one arrive per producer warp
-  static constexpr int kNumBars = 27;
+  static constexpr int kRing = 8;            // tiles, and pieces, in flight
+  static constexpr int kBarRowsFull = 11;    // [ring slot]
+  static constexpr int kBarRowsEmpty = 19;   // [ring slot]: one arrive per producer warp and the MMA thread
+  static constexpr int kBarPieceFull = 27;   // [ring slot]
+  static constexpr int kBarPieceEmpty = 35;  // [ring slot]
+  static constexpr int kNumBars = 43;
   uint32_t base;
   uint8_t* ptr;
   __device__ float* f(uint32_t off) const { return reinterpret_cast<float*>(ptr + off); }
   __device__ int* ring_rows() const { return reinterpret_cast<int*>(ptr + kSRows); }
-  __device__ int* ring_kind() const { return reinterpret_cast<int*>(ptr + kSRowKind); }
+  __device__ int* tiles() const { return reinterpret_cast<int*>(ptr + kSTile); }
+  __device__ Piece* pieces() const { return reinterpret_cast<Piece*>(ptr + kSPiece); }
   __device__ int* valid() const { return reinterpret_cast<int*>(ptr + kSValid); }
   __device__ int* any() const { return reinterpret_cast<int*>(ptr + kSAny); }
   __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(ptr + kSBar) + i; }
-  __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + kSBar + 224); }
-  __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(ptr + kSBar + 232); }
+  __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + kSBar + 352); }
+  __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(ptr + kSBar + 360); }
 };
-static_assert(Smem::kNumBars * 8 <= 224, "barriers overlap the tmem slot");
+static_assert(Smem::kNumBars * 8 <= 352, "barriers overlap the tmem slot");
 
 template <int kRegs>
 __device__ __forceinline__ void more_registers() {
@@ -107,16 +125,6 @@ template <int kRegs>
 __device__ __forceinline__ void fewer_registers() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-
-// 2-D tiled TMA store of one box; the issuing thread's bulk groups.
-__device__ __forceinline__ void tma_store_2d(const void* tmap, uint32_t src, int x, int y) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];\n"
-               "cp.async.bulk.commit_group;" ::"l"(reinterpret_cast<uint64_t>(tmap)),
-               "r"(src), "r"(x), "r"(y)
-               : "memory");
-}
-__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
-__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Bounded waits as wait_or_abort(), but suspended in hardware: try_wait gets a
 // time to stay blocked (20 us), so a waiting warp takes no issue slots from the
@@ -184,62 +192,125 @@ __device__ __forceinline__ void qk_chunk(uint32_t d, uint64_t a0, uint64_t b0, i
 
 // PV of head-dim chunk c, k-step s: A (V~^T, MN-major: 64-d atoms 16 KB apart,
 // 8-row groups 1 KB apart) at + c * 32 KB + s * 2 KB, B (P^T, MN-major) at
-// + s * 2 KB; accumulates into O^T columns 64 c .. + 63.
+// + s * 2 KB; accumulates into 64 columns of O^T.
 template <uint32_t kS>
 __device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
   mma_f16_at<((kS * 2048) >> 4), ((kS * 2048) >> 4)>(d, a, b, kIdescPV, acc);
 }
-__device__ __forceinline__ void pv_chunk(uint32_t tmem, uint64_t a0, uint64_t b0, uint32_t acc0, int c) {
-  const uint32_t d = tmem + kTmemO + uint32_t(c) * 64;
+__device__ __forceinline__ void pv_chunk(uint32_t d, uint64_t a0, uint64_t b0, uint32_t acc0, int c) {
   const uint64_t a = a0 + ((uint32_t(c) * 2 * kSlabBytes) >> 4);
   pv_mma<0>(d, a, b0, acc0);
   pv_mma<1>(d, a, b0, 1u); pv_mma<2>(d, a, b0, 1u); pv_mma<3>(d, a, b0, 1u);
   pv_mma<4>(d, a, b0, 1u); pv_mma<5>(d, a, b0, 1u); pv_mma<6>(d, a, b0, 1u); pv_mma<7>(d, a, b0, 1u);
 }
 
+// What tile n's ring slot holds, once published; kTileEnd after an abort.
+__device__ __forceinline__ int read_tile(const Smem& sm, uint32_t n, int* fault) {
+  const uint32_t slot = n % Smem::kRing;
+  return wait_fast(sm, Smem::kBarRowsFull + slot, (n / Smem::kRing) & 1, fault) ? sm.tiles()[slot] : kTileEnd;
+}
+__device__ __forceinline__ void tile_done(const Smem& sm, uint32_t n) {
+  mbar_arrive(sm.bar(Smem::kBarRowsEmpty + n % Smem::kRing));
+}
+
 // Tile n of the CTA's sequence: every per-tile barrier completes once per
 // tile, so a wait for tile n uses phase parity n & 1.
-__device__ void mma_role(const qsfm_params& p, const Smem& sm, Range rg, int T, uint32_t tmem, int* fault) {
+__device__ void mma_role(const Smem& sm, uint32_t tmem, int* fault) {
   if ((threadIdx.x & 31) != 0) return;
-  PieceIter pieces(&p, rg, T);
   const uint64_t qa = make_sdesc_sw128(sm.base + kSK, 16, 1024);
   const uint64_t qb = make_sdesc_sw128(sm.base + kSQ, 16, 1024);
   const uint64_t pa = make_sdesc_sw128(sm.base + kSK, kSlabBytes, 1024);
   const uint64_t pb = make_sdesc_sw128(sm.base + kSP, 16, 1024);
   const uint32_t ds = tmem + kTmemS;
-  TokenGeom g;
-  int unit, lo, hi;
-  uint32_t n = 0, piece = 0;
-  while (pieces.next(unit, g, lo, hi)) {
-    if (lo >= hi) continue;
+  uint32_t piece = 0;
 #pragma unroll 1
-    for (int k = lo; k < hi; ++k, ++n) {
-      const uint32_t par = n & 1;
-      if (k == lo && !wait_fast(sm, kBarQFull, piece & 1, fault)) return;
+  for (uint32_t n = 0;; ++n) {
+    const int tile = read_tile(sm, n, fault);
+    if (tile == kTileEnd) return;
+    tile_done(sm, n);
+    const bool first = tile & kTileFirst;
+    const uint32_t par = n & 1;
+    if (first && !wait_fast(sm, kBarQFull, piece & 1, fault)) return;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        if (!wait_fast(sm, kBarFull + c, par, fault)) return;
-        tc_fence_after();
-        qk_chunk(ds, qa, qb, c);
-      }
-      mma_commit(sm.bar(kBarSFull));
-      // P(n) written (so S^T(n) has been read)
-      if (!wait_fast(sm, kBarPFull, par, fault)) return;
+    for (int c = 0; c < 4; ++c) {
+      if (!wait_fast(sm, kBarFull + c, par, fault)) return;
       tc_fence_after();
-      if (k == lo && piece > 0) {
-        // the previous piece's epilogue must have read O^T before it is overwritten
+      qk_chunk(ds, qa, qb, c);
+    }
+    mma_commit(sm.bar(kBarSFull));
+    // P(n) written (so S^T(n) has been read; and the piece before the last has
+    // been read out, which these warps did before)
+    if (!wait_fast(sm, kBarPFull, par, fault)) return;
+    tc_fence_after();
+    const uint32_t acc0 = first ? 0u : 1u;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      if (c == 3 && first && piece > 0) {
+        // chunk 3 takes the place of the last piece's chunk 0
         if (!wait_fast(sm, kBarOFree, (piece - 1) & 1, fault)) return;
         tc_fence_after();
       }
-      const uint32_t acc0 = k == lo ? 0u : 1u;
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        pv_chunk(tmem, pa, pb, acc0, c);
-        if (c & 1) mma_commit(sm.bar(kBarFree + (c >> 1)));
-      }
+      pv_chunk(tmem + o_column(piece, c), pa, pb, acc0, c);
+      if (c & 1) mma_commit(sm.bar(kBarFree + (c >> 1)));
     }
-    ++piece;
+    if (tile & kTileLast) ++piece;
   }
+}
+
+// ------------------------------------------------------------- resolver
+// Walks the pieces of the CTA's range: each piece goes to the ring of pieces,
+// each tile's 128 physical rows (-1 = masked) to the ring of tiles; both end
+// with a mark.
+__device__ void resolver_role(const qsfm_params& p, const Smem& sm, Range rg, int T, int* fault) {
+  const int lane = threadIdx.x & 31;
+  int* rows = sm.ring_rows();
+  const uint8_t* q8 = static_cast<const uint8_t*>(p.q);
+  PieceIter pieces(&p, rg, T);
+  uint32_t n = 0, m = 0;  // next tile, next piece
+  auto put_piece = [&](int unit, int tiles, int whole) -> bool {
+    const uint32_t slot = m % Smem::kRing;
+    if (!warp_wait_or_abort(sm, Smem::kBarPieceEmpty + slot, ((m / Smem::kRing) & 1) ^ 1, fault)) return false;
+    if (lane == 0) {
+      sm.pieces()[slot] = Piece{unit, tiles, whole, 0};
+      mbar_arrive(sm.bar(Smem::kBarPieceFull + slot));
+    }
+    ++m;
+    return true;
+  };
+  auto wait_tile = [&]() {
+    return warp_wait_or_abort(sm, Smem::kBarRowsEmpty + n % Smem::kRing, ((n / Smem::kRing) & 1) ^ 1, fault);
+  };
+  auto put_tile = [&](int what) {
+    if (lane == 0) sm.tiles()[n % Smem::kRing] = what;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.bar(Smem::kBarRowsFull + n % Smem::kRing));
+    ++n;
+  };
+  int unit, lo, hi;
+  TokenGeom g;
+  while (pieces.next(unit, g, lo, hi)) {
+    if (!put_piece(unit, max(hi - lo, 0), lo == 0 && hi == g.n_tiles ? 1 : 0)) return;
+    if (lo >= hi) continue;
+    // the unit's Q goes to L2 a few tiles before its first product; the next
+    // token's index list while this one is resolved
+    if (lane == 0) bulk_prefetch_l2(q8 + size_t(unit) * kHeads * kDim * 2, kHeads * kDim * 2);
+    if (p.cmp_sparse_indices != nullptr && g.tok + 1 < (T >> unit_shift(p))) {
+      const uint8_t* ix = reinterpret_cast<const uint8_t*>(p.cmp_sparse_indices + (size_t)(g.tok + 1) * p.k2);
+      for (int off = 128 * lane; off < 4 * p.k2; off += 32 * 128) prefetch_l2(ix + off);
+    }
+    for (int k0 = lo; k0 < hi; ++k0) {
+      if (!wait_tile()) return;
+      const int k[1] = {k0};
+      const bool live[1] = {true};
+      int lg[1][4], pr[1][4];
+      bool cmp[1];
+      resolve_tile_rows<1>(p, g, k, live, lane, fault, lg, pr, cmp);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) rows[(n % Smem::kRing) * kTileRows + lane + 32 * u] = pr[0][u];
+      put_tile((cmp[0] ? kTileCmp : 0) | (k0 == lo ? kTileFirst : 0) | (k0 == hi - 1 ? kTileLast : 0));
+    }
+  }
+  if (put_piece(-1, 0, 0) && wait_tile()) put_tile(kTileEnd);
 }
 
 // ------------------------------------------------------------- producers
@@ -281,7 +352,6 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
   const int half = tid >> 7, r = tid & 127;
   const bool rope = half == 0;
   const int* rows = sm.ring_rows();
-  const int* kind = sm.ring_kind();
   const uint32_t rowb = sm.base + kSK + uint32_t(half) * kSlabBytes + uint32_t(r) * 128;
   const uint32_t sw = uint32_t(r & 7);
   uint32_t ca[32], cb[32];  // converted blocks: chunks 0 and 1, then 2 and 3
@@ -289,14 +359,14 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
   uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0, ex = 0;  // scale words of the four blocks, the rows' exponents
 
   auto take_rows = [&](uint32_t n, const uint8_t*& row, bool& v) -> bool {
-    const uint32_t slot = n % Smem::kRing;
-    if (!warp_wait_fast(sm, Smem::kBarRowsFull + slot, (n / Smem::kRing) & 1, fault)) return false;
-    const int kd = kind[slot], pr = rows[slot * kTileRows + r];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(sm.bar(Smem::kBarRowsEmpty + slot));
+    const int tile = read_tile(sm, n, fault);
+    const int pr = rows[(n % Smem::kRing) * kTileRows + r];
+    // uniform even where a wait ran out for some lanes
+    if (__any_sync(0xffffffffu, tile == kTileEnd)) return false;
+    if (lane == 0) tile_done(sm, n);
     v = pr >= 0;
-    row = static_cast<const uint8_t*>(kd == 1 ? p.cmp_kv : p.ori_kv) + size_t(v ? pr : 0) * kRowB;
-    return kd >= 0;
+    row = static_cast<const uint8_t*>(tile & kTileCmp ? p.cmp_kv : p.ori_kv) + size_t(v ? pr : 0) * kRowB;
+    return true;
   };
   // Codes of chunk c's block: bytes 96 + 64 c + 32 half (none for the rope
   // block). A masked row's codes are read all the same (row 0 of the pool) and
@@ -374,8 +444,8 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
 }
 
 // ------------------------------------------------------------- softmax, epilogue
-__device__ void softmax_role(const qsfm_params& p, const Smem& sm, Range rg, int T, uint32_t tmem, const Workspace& ws,
-                             int c_idx, const CUtensorMap* qmap, const CUtensorMap* omap, int* fault) {
+__device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_unit, uint32_t tmem, const Workspace& ws, int c_idx,
+                             const CUtensorMap* qmap, int* fault) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qd = warp & 3;            // tensor-memory lane quadrant
   const int h0 = kHPT * (warp >> 2);  // first of this warp's heads
@@ -397,61 +467,114 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, Range rg, int
       tma_load_2d(sm.base + kSQ + db * 8192, qmap, db * 64, unit * 64, sm.bar(kBarQFull));
   };
 
-  if (tid < 64) m_used[tid] = -INFINITY;  // no guess for the first unit
-  named_sync(kBarSm, kSmThreads);
-  PieceIter pieces(&p, rg, T);
-  uint32_t n = 0;
-  // A piece (work unit, its range of tiles), and the one after: the geometry of
-  // the piece after that is read while the current piece's last PV runs.
-  struct Piece {
-    int t, lo, hi, n_tiles;
-    bool have;
-  };
-  auto next_piece = [&]() {
-    Piece q;
-    TokenGeom g;
-    q.have = pieces.next(q.t, g, q.lo, q.hi);
-    q.n_tiles = g.n_tiles;
+  // The next piece from the resolver, by thread 0, handed to the other warps
+  // through shared memory at the next barrier (so that all of them go the same
+  // way, whatever an abort does to the ring).
+  uint32_t taken = 0;
+  auto fetch_piece = [&]() {
+    const uint32_t slot = taken % Smem::kRing;
+    Piece q = {-1, 0, 0, 0};
+    if (wait_fast(sm, Smem::kBarPieceFull + slot, (taken / Smem::kRing) & 1, fault)) {
+      q = sm.pieces()[slot];
+      mbar_arrive(sm.bar(Smem::kBarPieceEmpty + slot));
+      ++taken;
+    }
+    sm.pieces()[Smem::kRing] = q;
     return q;
   };
-  Piece cur = next_piece();
-  if (tid == 0 && cur.have && cur.lo < cur.hi) load_q(cur.t);
-  Piece nxt = cur.have ? next_piece() : cur;
-  while (cur.have) {
-    const int t = cur.t, lo = cur.lo, hi = cur.hi;
-    const bool whole = (lo == 0 && hi == cur.n_tiles), any = lo < hi;
+  float* sinks = sm.f(kSSink);
+  if (tid < p.n1) sinks[tid] = p.sinks != nullptr ? __ldg(p.sinks + tid) * kLog2e : -INFINITY;
+  if (tid < 64) m_used[tid] = 0.f;  // the first unit's guess
+  if (tid == 0) {
+    const Piece q = fetch_piece();
+    if (q.tiles > 0) load_q(q.unit);
+  }
+  named_sync(kBarSm, kSmThreads);
+  Piece cur = sm.pieces()[Smem::kRing];
+  named_sync(kBarSm, kSmThreads);
+  if (tid == 0 && cur.unit >= 0) fetch_piece();
+  named_sync(kBarSm, kSmThreads);
+  Piece nxt = sm.pieces()[Smem::kRing];
+
+  // The output of the piece before: O^T in tensor memory, its 1 / den in inv.
+  struct Out {
+    int unit, whole, slot;  // unit -1: none; slot -1: not written
+    uint32_t piece, tile;   // among the pieces with tiles; the piece's last tile
+  };
+  // Reads, scales and writes it: thread (lane d of a chunk) has one element of
+  // each of its 32 heads. bf16 outputs are 64 contiguous bytes per head and warp
+  // in 2-byte stores: no exchange between lanes, nothing to wait for.
+  auto write_out = [&](const Out& o) {
+    // Free[1] of its last tile: every PV product is complete. (Free[0] may be a
+    // phase ahead: the next piece's PV has begun.)
+    warp_wait_fast(sm, kBarFree + 1, o.tile & 1, fault);
+    tc_fence_after();
+    const float* iv = inv + 64 * (o.piece & 1) + h0;
+    const int d0 = 32 * qd + lane;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.attn_out) + (size_t(o.unit) * 64 + h0) * kDim + d0;
+    float* part = ws.out + (size_t(o.slot < 0 ? 0 : o.slot) * 64 + h0) * kDim + d0;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      float x[kHPT];
+      tmem_load(tmem + o_column(o.piece, c) + h0 + lane_base, x);
+      tmem_ld_wait_for(x);
+      if (c == 0) {  // the next piece's last chunk may overwrite it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.bar(kBarOFree));
+      }
+      if (o.whole) {
+#pragma unroll
+        for (int i = 0; i < kHPT; i += 4) {
+          const float4 v4 = *reinterpret_cast<const float4*>(iv + i);
+          const uint32_t a = pack_bf16(x[i] * v4.x, x[i + 1] * v4.y), b = pack_bf16(x[i + 2] * v4.z, x[i + 3] * v4.w);
+          uint16_t* at = reinterpret_cast<uint16_t*>(out + 128 * c) + size_t(i) * kDim;
+          at[0] = uint16_t(a);
+          at[kDim] = uint16_t(a >> 16);
+          at[2 * kDim] = uint16_t(b);
+          at[3 * kDim] = uint16_t(b >> 16);
+        }
+      } else if (o.slot >= 0) {
+#pragma unroll
+        for (int i = 0; i < kHPT; ++i) part[128 * c + size_t(i) * kDim] = x[i] * iv[i];
+      }
+    }
+    tc_fence_before();  // before this warp's next arrival at a barrier the MMA thread waits on
+  };
+
+  uint32_t n = 0, live = 0;  // tiles, pieces with tiles so far
+  Out pending = {-1, 0, -1, 0, 0};
+#pragma unroll 1
+  while (cur.unit >= 0) {
+    const int t = cur.unit;
+    const bool whole = cur.whole, any = cur.tiles > 0;
     // the next piece's q is requested once this piece's last score product has
     // completed
-    const bool q_next = tid == 0 && nxt.have && nxt.lo < nxt.hi;
-    if (!any && q_next && !*sm.abort_flag()) load_q(nxt.t);
-    // this thread's head sink (log2 units); the unit's heads start at unit_head0
-    const float sink2 =
-        (tid < 64 && p.sinks != nullptr) ? __ldg(p.sinks + unit_head0(p, t) + tid) * kLog2e : -INFINITY;
-    const int slot = (t == rg.t0) ? 2 * c_idx : 2 * c_idx + 1;
+    const bool q_next = tid == 0 && nxt.tiles > 0;
+    if (!any && q_next && !*sm.abort_flag()) load_q(nxt.unit);
+    const int slot = (t == first_unit) ? 2 * c_idx : 2 * c_idx + 1;
     const bool writable = whole || slot < ws.slots;  // split pieces need the workspace
     if (!writable && tid == 0) atomicOr(fault, QSFM_FAULT_METADATA);
     // Lane i of the warp keeps the running sum of P for head h0 + i over this
     // warp's 32 rows: each tile's P is folded in with a lane reduction once P
     // is published (one register instead of kHPT).
     float l_sum = 0.f;
-    // The first tile takes the last unit's maxima as a guess: any reference is
+    // The first tile takes the last unit's maxima (0 at first) as a guess: any reference is
     // right that leaves no t above 8 (P stays in range) and none of the first
     // rows' below -60 (P and its sum keep their precision; bf16 has the range
     // of fp32). Where the guess fails the vote sends the tile down the slow
     // path. `seen`: a tile with a valid row has set or confirmed the maxima.
     bool seen = false;
-    Piece after = nxt;
 #pragma unroll 1
-    for (int k = lo; k < hi; ++k, ++n) {
+    for (int k = 0; k < cur.tiles; ++k, ++n) {
       const uint32_t par = n & 1;
-      // Lane 0 of each warp polls. After an abort the waits fall through at
-      // once; the warps keep running the same named-barrier sequence so that
-      // none of them blocks.
+      // After an abort the waits fall through at once; the warps keep running
+      // the same named-barrier sequence so that none of them blocks.
       warp_wait_fast(sm, kBarFull + 0, par, fault);  // the tile's valid flags
       const bool v = sm.valid()[r] != 0;
       const int4 quadrants = *reinterpret_cast<const int4*>(sm.any());
       warp_wait_fast(sm, kBarSFull, par, fault);
-      if (k == hi - 1 && q_next && !*sm.abort_flag()) load_q(nxt.t);  // q is free: the unit's last score product is complete
+      if (k == cur.tiles - 1 && q_next && !*sm.abort_flag()) load_q(nxt.unit);  // q is free: the last score product is complete
       tc_fence_after();
       float x[kHPT];
       tmem_load(s_addr, x);
@@ -506,7 +629,7 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, Range rg, int
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             float o[kHPT];
-            const uint32_t addr = tmem + kTmemO + 64 * c + h0 + lane_base;
+            const uint32_t addr = tmem + o_column(live, c) + h0 + lane_base;
             tmem_load(addr, o);
             tmem_ld_wait_for(o);
 #pragma unroll
@@ -547,110 +670,54 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, Range rg, int
         l_sum += tile_sum;
       }
       seen = seen || (quadrants.x | quadrants.y | quadrants.z | quadrants.w) != 0;
+      if (k == 0 && pending.unit >= 0) {
+        write_out(pending);
+        pending.unit = -1;
+      }
     }
-    if (nxt.have) after = next_piece();
-    // ---------------- epilogue of the piece
+    // ---------------- the piece's sums, lse and 1 / den; the piece after next
     if (any) red[qd * 64 + h0 + lane] = l_sum;
     named_sync(kBarSm, kSmThreads);
-    if (tid < 64 && writable) {
-      const float lt = any ? (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]) : 0.f;
-      const float mu = m_used[tid];
+    if (tid == 0 && nxt.unit >= 0) fetch_piece();
+    if (tid >= kSmThreads - 64 && writable) {
+      const int h = tid - (kSmThreads - 64);
+      const float lt = any ? (red[h] + red[64 + h]) + (red[128 + h] + red[192 + h]) : 0.f;
+      const float mu = m_used[h];
       const float lse2 = lt > 0.f ? mu + log2f(lt) : -INFINITY;
+      float den = lt;
       if (whole) {
-        float den = lt;
-        if (p.sinks != nullptr && lt > 0.f) den += exp2f(sink2 - mu);
-        inv[tid] = lt > 0.f ? 1.f / den : 0.f;
-        if (p.return_lse) p.softmax_lse[size_t(t) * 64 + tid] = lse2 * kLn2;
+        const float sink2 = sinks[unit_head0(p, t) + h];  // -inf without sinks
+        if (lt > 0.f) den += exp2f(sink2 - mu);
+        if (p.return_lse) p.softmax_lse[size_t(t) * 64 + h] = lse2 * kLn2;
       } else {
-        inv[tid] = lt > 0.f ? 1.f / lt : 0.f;
-        ws.lse[size_t(slot) * 64 + tid] = lse2 * kLn2;
+        ws.lse[size_t(slot) * 64 + h] = lse2 * kLn2;
       }
+      inv[64 * (live & 1) + h] = lt > 0.f ? 1.f / den : 0.f;
     }
     named_sync(kBarSm, kSmThreads);
     if (any) {
-      warp_wait_fast(sm, kBarFree, (n - 1) & 1, fault);
-      warp_wait_fast(sm, kBarFree + 1, (n - 1) & 1, fault);
-      tc_fence_after();
+      pending = Out{t, whole, writable ? slot : -1, live, n - 1};
+      ++live;
+    } else if (writable) {  // no rows: zeros
+      const uint4 z = make_uint4(0, 0, 0, 0);
+      uint4* zeros = whole ? reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.attn_out) + size_t(t) * 64 * kDim)
+                           : reinterpret_cast<uint4*>(ws.out + size_t(slot) * 64 * kDim);
+      for (int i = tid; i < 64 * kDim * (whole ? 2 : 4) / 16; i += kSmThreads) zeros[i] = z;
     }
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.attn_out) + size_t(t) * 64 * kDim;
-    if (!any) {
-      if (whole) {
-        const uint4 z = make_uint4(0, 0, 0, 0);
-        for (int i = tid; i < 64 * kDim / 8; i += kSmThreads) reinterpret_cast<uint4*>(out)[i] = z;
-      }
-    } else if (whole) {
-      // Chunk by chunk through shared memory (P's place: PV is complete), two
-      // slabs of 64 d. A warp reads 16 lanes (d) x 64 heads as 8 x 8 fragments,
-      // scales them and stores them transposed as [head][64 d], 16-byte units
-      // swizzled by the head; the four warps of a slab then hand it to TMA,
-      // whose read of it runs beside the next chunk's arithmetic.
-      const int dl = 32 * qd + 16 * (warp >> 2);  // first of the warp's 16 lanes
-      const uint32_t o_addr = tmem + kTmemO + (uint32_t(dl) << 16);
-      const int slab = qd >> 1;
-      const bool leader = lane == 0 && warp == 2 * slab;
-      const uint32_t slab_addr = sm.base + kSStage + uint32_t(slab) * 8192;
-      const uint32_t unit = uint32_t((dl & 63) / 8 + ((lane >> 3) & 1)) ^ uint32_t(lane & 7);
-      const uint32_t st_addr = slab_addr + uint32_t(8 * (lane >> 4) + (lane & 7)) * 128 + unit * 16;
-      float o[32];
-      tmem_ld16x256b_x8(o_addr, o);
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        tmem_ld_wait_for(o);
-        uint32_t f[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 iv = *reinterpret_cast<const float2*>(inv + 8 * j + 2 * (lane & 3));
-          f[2 * j] = pack_bf16(o[4 * j] * iv.x, o[4 * j + 1] * iv.y);
-          f[2 * j + 1] = pack_bf16(o[4 * j + 2] * iv.x, o[4 * j + 3] * iv.y);
-        }
-        if (c < 3) {
-          tmem_ld16x256b_x8(o_addr + 64 * (c + 1), o);
-        } else {  // O^T is in registers: the next unit's PV may overwrite it
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sm.bar(kBarOFree));
-        }
-        if (c > 0) {  // the last chunk has been read from the slab
-          if (leader) bulk_wait_read();
-          named_sync(kBarSlab + slab, 128);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; j += 2)
-          stmatrix_x4_trans(st_addr + uint32_t(j) * 8 * 128, f[2 * j], f[2 * j + 1], f[2 * j + 2], f[2 * j + 3]);
-        fence_proxy_async_smem();
-        named_sync(kBarSlab + slab, 128);
-        if (leader) tma_store_2d(omap, slab_addr, 128 * c + 64 * slab, t * 64);
-      }
-      if (leader) bulk_wait_read();
-    } else {
-      // split pieces: fp32 rows in the workspace, this thread element
-      // d = 128 c + 32 qd + lane of its heads (128 bytes per head per warp)
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        float o[kHPT];
-        tmem_load(tmem + kTmemO + 64 * c + h0 + lane_base, o);
-        tmem_ld_wait_for(o);
-        if (writable) {
-          float* part = ws.out + (size_t(slot) * 64 + h0) * kDim + 128 * c + 32 * qd + lane;
-#pragma unroll
-          for (int i = 0; i < kHPT; ++i) part[size_t(i) * kDim] = o[i] * inv[h0 + i];
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sm.bar(kBarOFree));
-    }
-    named_sync(kBarSm, kSmThreads);  // m_used / inv / red are reused by the next piece
-    if (*sm.abort_flag()) break;     // uniform: read after the barrier
+    const Piece after = nxt.unit >= 0 ? sm.pieces()[Smem::kRing] : nxt;
+    const bool aborted = *sm.abort_flag();
+    // red, m_used and the handed piece are written again behind the next barrier
+    // of all softmax warps (the first tile's vote, or the next piece's)
     cur = nxt;
     nxt = after;
+    if (named_sync_or(kBarSm, kSmThreads, aborted)) break;  // the same for all
   }
-  if (lane == 0) bulk_wait();  // the leaders' stores
+  if (pending.unit >= 0 && !*sm.abort_flag()) write_out(pending);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
     attention4_kernel(const qsfm_params p, const int T, const Workspace ws, int* fault,
-                      const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap omap) {
+                      const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   Smem sm;
@@ -691,7 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(sm.bar(kBarOFree), kSmWarps);
     for (int i = 0; i < Smem::kRing; ++i) {
       mbar_init(sm.bar(Smem::kBarRowsFull + i), 1);
-      mbar_init(sm.bar(Smem::kBarRowsEmpty + i), kPrWarps);
+      mbar_init(sm.bar(Smem::kBarRowsEmpty + i), kPrWarps + 1);
+      mbar_init(sm.bar(Smem::kBarPieceFull + i), 1);
+      mbar_init(sm.bar(Smem::kBarPieceEmpty + i), 1);
     }
     mbar_init(sm.bar(kBarDrain), 1);
     *sm.abort_flag() = 0;
@@ -704,14 +773,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *sm.tmem_slot();
 
   if (warp < kSmWarps) {
-    softmax_role(p, sm, rg, T, tmem, ws, c, &qmap, &omap, fault);
+    softmax_role(p, sm, rg.t0, tmem, ws, c, &qmap, fault);
   } else if (warp < kMmaWarp) {
     more_registers<kPrRegs>();
     producer_role(p, sm, fault);
   } else {
     fewer_registers<kLastRegs>();
     if (warp == kMmaWarp) {
-      mma_role(p, sm, rg, T, tmem, fault);
+      mma_role(sm, tmem, fault);
       if ((tid & 31) == 0) {
         // every MMA issued above has completed before tensor memory is freed
         // (after an abort some may still be in flight)
@@ -745,12 +814,11 @@ cudaError_t launch_attention4(const qsfm_params& p, int num_tokens, int num_ctas
                               cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(attention4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
-  CUtensorMap qmap, omap;  // attn_out has q's layout
+  CUtensorMap qmap;
   e = make_q_map(p.q, num_tokens, &qmap);
-  if (e == cudaSuccess) e = make_q_map(p.attn_out, num_tokens, &omap);
   if (e != cudaSuccess) return e;
   return launch_after_predecessor(attention4_kernel, dim3(num_ctas), dim3(kThreads), kSmemAlloc, s, p, num_tokens,
-                                  ws, fault, qmap, omap);
+                                  ws, fault, qmap);
 }
 
 }  // namespace qsfm
