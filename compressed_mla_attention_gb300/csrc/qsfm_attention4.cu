@@ -492,9 +492,6 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
   named_sync(kBarSm, kSmThreads);
   Piece cur = sm.pieces()[Smem::kRing];
   named_sync(kBarSm, kSmThreads);
-  if (tid == 0 && cur.unit >= 0) fetch_piece();
-  named_sync(kBarSm, kSmThreads);
-  Piece nxt = sm.pieces()[Smem::kRing];
 
   // The output of the piece before: O^T in tensor memory, its 1 / den in inv.
   struct Out {
@@ -548,10 +545,6 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
   while (cur.unit >= 0) {
     const int t = cur.unit;
     const bool whole = cur.whole, any = cur.tiles > 0;
-    // the next piece's q is requested once this piece's last score product has
-    // completed
-    const bool q_next = tid == 0 && nxt.tiles > 0;
-    if (!any && q_next && !*sm.abort_flag()) load_q(nxt.unit);
     const int slot = (t == first_unit) ? 2 * c_idx : 2 * c_idx + 1;
     const bool writable = whole || slot < ws.slots;  // split pieces need the workspace
     if (!writable && tid == 0) atomicOr(fault, QSFM_FAULT_METADATA);
@@ -573,8 +566,13 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
       warp_wait_fast(sm, kBarFull + 0, par, fault);  // the tile's valid flags
       const bool v = sm.valid()[r] != 0;
       const int4 quadrants = *reinterpret_cast<const int4*>(sm.any());
+      // The next piece, and its q as soon as this one's last score product has
+      // completed. Not earlier: at the start the resolver is still at the first
+      // piece's tiles, and the softmax of the first would wait for the last.
+      Piece next = {-1, 0, 0, 0};
+      if (k == cur.tiles - 1 && tid == 0) next = fetch_piece();
       warp_wait_fast(sm, kBarSFull, par, fault);
-      if (k == cur.tiles - 1 && q_next && !*sm.abort_flag()) load_q(nxt.unit);  // q is free: the last score product is complete
+      if (next.tiles > 0 && !*sm.abort_flag()) load_q(next.unit);
       tc_fence_after();
       float x[kHPT];
       tmem_load(s_addr, x);
@@ -675,10 +673,13 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
         pending.unit = -1;
       }
     }
-    // ---------------- the piece's sums, lse and 1 / den; the piece after next
+    // ---------------- the piece's sums, lse and 1 / den; the next piece
     if (any) red[qd * 64 + h0 + lane] = l_sum;
     named_sync(kBarSm, kSmThreads);
-    if (tid == 0 && nxt.unit >= 0) fetch_piece();
+    if (!any && tid == 0) {
+      const Piece next = fetch_piece();
+      if (next.tiles > 0 && !*sm.abort_flag()) load_q(next.unit);
+    }
     if (tid >= kSmThreads - 64 && writable) {
       const int h = tid - (kSmThreads - 64);
       const float lt = any ? (red[h] + red[64 + h]) + (red[128 + h] + red[192 + h]) : 0.f;
@@ -704,12 +705,10 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
                            : reinterpret_cast<uint4*>(ws.out + size_t(slot) * 64 * kDim);
       for (int i = tid; i < 64 * kDim * (whole ? 2 : 4) / 16; i += kSmThreads) zeros[i] = z;
     }
-    const Piece after = nxt.unit >= 0 ? sm.pieces()[Smem::kRing] : nxt;
+    cur = sm.pieces()[Smem::kRing];
     const bool aborted = *sm.abort_flag();
     // red, m_used and the handed piece are written again behind the next barrier
     // of all softmax warps (the first tile's vote, or the next piece's)
-    cur = nxt;
-    nxt = after;
     if (named_sync_or(kBarSm, kSmThreads, aborted)) break;  // the same for all
   }
   if (pending.unit >= 0 && !*sm.abort_flag()) write_out(pending);
