@@ -48,15 +48,19 @@ constexpr int kHPT = 32;                     // heads per softmax thread
 constexpr int kBarSm = 1;                    // named barrier of the softmax warps
 constexpr int kRowB = QSFM_PACKED384_ROW_BYTES;
 
+#ifndef RING
+#define RING 4
+#endif
+constexpr int kRing4 = RING;
 // shared memory map (byte offsets from a 1024-aligned base)
 constexpr uint32_t kSlabBytes = kTileRows * 128;              // 128 rows x 64 d (bf16): 16 KB
 constexpr uint32_t kSK = 0;                                   // K~ tile: 8 slabs
 constexpr uint32_t kSQ = kSK + 8 * kSlabBytes;                // Q: 8 d-blocks x 64 heads x 128 B
 constexpr uint32_t kSP = kSQ + 8 * 64 * 128;                  // P: 128 rows x 64 heads (bf16)
-constexpr uint32_t kSRows = kSP + kTileRows * 128;            // [8][128] i32 physical rows
-constexpr uint32_t kSTile = kSRows + 8 * kTileRows * 4;       // [8] i32: what the ring slot holds
-constexpr uint32_t kSPiece = kSTile + 32;                     // [8] pieces, then the one being handed over
-constexpr uint32_t kSValid = kSPiece + 9 * 16 + 16;           // [128] i32: row of the tile valid
+constexpr uint32_t kSRows = kSP + kTileRows * 128;            // [ring][128] i32 physical rows
+constexpr uint32_t kSTile = kSRows + kRing4 * kTileRows * 4;    // [ring] i32: what the slot holds
+constexpr uint32_t kSPiece = kSTile + kRing4 * 4;             // [ring] pieces, then two being handed over
+constexpr uint32_t kSValid = kSPiece + (kRing4 + 2) * 16;     // [128] i32: row of the tile valid
 constexpr uint32_t kSRed = kSValid + kTileRows * 4;           // [4][64] f32 per-quadrant partials
 constexpr uint32_t kSMUsed = kSRed + 1024;                    // [64] f32
 constexpr uint32_t kSAlpha = kSMUsed + 256;                   // [64] f32
@@ -97,12 +101,12 @@ struct __align__(16) Piece {
 };
 
 struct Smem {
-  static constexpr int kRing = 8;            // tiles, and pieces, in flight
+  static constexpr int kRing = kRing4;  // tiles, and pieces, in flight
   static constexpr int kBarRowsFull = 11;    // [ring slot]
-  static constexpr int kBarRowsEmpty = 19;   // [ring slot]: one arrive per producer warp and the MMA thread
-  static constexpr int kBarPieceFull = 27;   // [ring slot]
-  static constexpr int kBarPieceEmpty = 35;  // [ring slot]
-  static constexpr int kNumBars = 43;
+  static constexpr int kBarRowsEmpty = 11 + kRing;   // [ring slot]: one arrive per producer warp and the MMA thread
+  static constexpr int kBarPieceFull = 11 + 2 * kRing;   // [ring slot]
+  static constexpr int kBarPieceEmpty = 11 + 3 * kRing;  // [ring slot]
+  static constexpr int kNumBars = 11 + 4 * kRing;
   uint32_t base;
   uint8_t* ptr;
   __device__ float* f(uint32_t off) const { return reinterpret_cast<float*>(ptr + off); }
@@ -175,33 +179,51 @@ __device__ __forceinline__ void tmem_ld_wait_for(float (&v)[32]) {
 }
 
 // ------------------------------------------------------------- MMA issue
+// The whole warp runs the issue loop and one elected lane (always the same one)
+// issues: descriptors and addresses are then provably the same in every lane and
+// stay in uniform registers. A loop on one lane alone takes 60 to 100 cycles per
+// MMA (each operand is moved to a uniform register in issue slots that the
+// producers' conversions contend for); this one the 48 that the operands take to be
+// read from shared memory (128 x 16 + 64 x 16 bf16 at 128 B / cycle).
+// Descriptors of 128-byte-swizzled operands in 8-row groups of 1 KB.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // group stride, version, swizzle
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) {
+  return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+// a, b: low words of the operands' descriptors; the high words are all alike.
+template <uint32_t kAOff, uint32_t kBOff, uint32_t kIdesc>
+__device__ __forceinline__ void mma_elected(uint32_t d, uint32_t a, uint32_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 a, b;\n add.u32 x, %1, %6;\n add.u32 y, %2, %7;\n"
+      " mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
+      " setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+      " mov.b32 x, %3;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, x, p;\n}" ::"r"(d),
+      "r"(a), "r"(b), "n"(kIdesc), "r"(accumulate), "n"(kDescHigh), "n"(kAOff), "n"(kBOff)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elected(uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 // QK^T of chunk c (d-blocks 2c, 2c + 1), k-step s of d-block db: A (K~,
 // K-major) at + db * 16 KB + s * 32 B, B (Q, K-major) at + db * 8 KB + s * 32 B.
-template <uint32_t kDb, uint32_t kS>
-__device__ __forceinline__ void qk_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
-  mma_f16_at<((kDb * kSlabBytes + kS * 32) >> 4), ((kDb * 8192 + kS * 32) >> 4)>(d, a, b, kIdescQK, acc);
-}
-__device__ __forceinline__ void qk_chunk(uint32_t d, uint64_t a0, uint64_t b0, int c) {
-  const uint64_t a = a0 + ((uint32_t(c) * 2 * kSlabBytes) >> 4);
-  const uint64_t b = b0 + ((uint32_t(c) * 2 * 8192) >> 4);
-  qk_mma<0, 0>(d, a, b, c != 0 ? 1u : 0u);
-  qk_mma<0, 1>(d, a, b, 1u); qk_mma<0, 2>(d, a, b, 1u); qk_mma<0, 3>(d, a, b, 1u);
-  qk_mma<1, 0>(d, a, b, 1u); qk_mma<1, 1>(d, a, b, 1u);
-  qk_mma<1, 2>(d, a, b, 1u); qk_mma<1, 3>(d, a, b, 1u);
+template <int kI = 0>
+__device__ __forceinline__ void qk_chunk(uint32_t d, uint32_t a, uint32_t b, uint32_t acc0) {
+  constexpr uint32_t db = kI / 4, st = kI % 4;
+  mma_elected<((db * kSlabBytes + st * 32) >> 4), ((db * 8192 + st * 32) >> 4), kIdescQK>(d, a, b, kI == 0 ? acc0 : 1u);
+  if constexpr (kI < 7) qk_chunk<kI + 1>(d, a, b, acc0);
 }
 
 // PV of head-dim chunk c, k-step s: A (V~^T, MN-major: 64-d atoms 16 KB apart,
 // 8-row groups 1 KB apart) at + c * 32 KB + s * 2 KB, B (P^T, MN-major) at
 // + s * 2 KB; accumulates into 64 columns of O^T.
-template <uint32_t kS>
-__device__ __forceinline__ void pv_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t acc) {
-  mma_f16_at<((kS * 2048) >> 4), ((kS * 2048) >> 4)>(d, a, b, kIdescPV, acc);
-}
-__device__ __forceinline__ void pv_chunk(uint32_t d, uint64_t a0, uint64_t b0, uint32_t acc0, int c) {
-  const uint64_t a = a0 + ((uint32_t(c) * 2 * kSlabBytes) >> 4);
-  pv_mma<0>(d, a, b0, acc0);
-  pv_mma<1>(d, a, b0, 1u); pv_mma<2>(d, a, b0, 1u); pv_mma<3>(d, a, b0, 1u);
-  pv_mma<4>(d, a, b0, 1u); pv_mma<5>(d, a, b0, 1u); pv_mma<6>(d, a, b0, 1u); pv_mma<7>(d, a, b0, 1u);
+template <int kI = 0>
+__device__ __forceinline__ void pv_chunk(uint32_t d, uint32_t a, uint32_t b, uint32_t acc0) {
+  mma_elected<((kI * 2048) >> 4), ((kI * 2048) >> 4), kIdescPV>(d, a, b, kI == 0 ? acc0 : 1u);
+  if constexpr (kI < 7) pv_chunk<kI + 1>(d, a, b, acc0);
 }
 
 // What tile n's ring slot holds, once published; kTileEnd after an abort.
@@ -215,43 +237,43 @@ __device__ __forceinline__ void tile_done(const Smem& sm, uint32_t n) {
 
 // Tile n of the CTA's sequence: every per-tile barrier completes once per
 // tile, so a wait for tile n uses phase parity n & 1.
-__device__ void mma_role(const Smem& sm, uint32_t tmem, int* fault) {
-  if ((threadIdx.x & 31) != 0) return;
-  const uint64_t qa = make_sdesc_sw128(sm.base + kSK, 16, 1024);
-  const uint64_t qb = make_sdesc_sw128(sm.base + kSQ, 16, 1024);
-  const uint64_t pa = make_sdesc_sw128(sm.base + kSK, kSlabBytes, 1024);
-  const uint64_t pb = make_sdesc_sw128(sm.base + kSP, 16, 1024);
-  const uint32_t ds = tmem + kTmemS;
+__device__ void mma_role(const Smem& sm, uint32_t tmem_any, int* fault) {
+  const uint32_t qa = desc_low(sm.base + kSK, 16);
+  const uint32_t qb = desc_low(sm.base + kSQ, 16);
+  const uint32_t pa = desc_low(sm.base + kSK, kSlabBytes);
+  const uint32_t pb = desc_low(sm.base + kSP, 16);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);  // the same in every lane, to the compiler too
   uint32_t piece = 0;
 #pragma unroll 1
   for (uint32_t n = 0;; ++n) {
-    const int tile = read_tile(sm, n, fault);
+    const int tile = __shfl_sync(0xffffffffu, read_tile(sm, n, fault), 0);
     if (tile == kTileEnd) return;
-    tile_done(sm, n);
+    if ((threadIdx.x & 31) == 0) tile_done(sm, n);
+    __syncwarp();
     const bool first = tile & kTileFirst;
     const uint32_t par = n & 1;
-    if (first && !wait_fast(sm, kBarQFull, piece & 1, fault)) return;
+    if (first && !warp_wait_fast(sm, kBarQFull, piece & 1, fault)) return;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      if (!wait_fast(sm, kBarFull + c, par, fault)) return;
+    for (uint32_t c = 0; c < 4; ++c) {
+      if (!warp_wait_fast(sm, kBarFull + c, par, fault)) return;
       tc_fence_after();
-      qk_chunk(ds, qa, qb, c);
+      qk_chunk(tmem + kTmemS, qa + c * (2 * kSlabBytes >> 4), qb + c * (2 * 8192 >> 4), c != 0 ? 1u : 0u);
     }
-    mma_commit(sm.bar(kBarSFull));
+    commit_elected(sm.bar(kBarSFull));
     // P(n) written (so S^T(n) has been read; and the piece before the last has
     // been read out, which these warps did before)
-    if (!wait_fast(sm, kBarPFull, par, fault)) return;
+    if (!warp_wait_fast(sm, kBarPFull, par, fault)) return;
     tc_fence_after();
     const uint32_t acc0 = first ? 0u : 1u;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (uint32_t c = 0; c < 4; ++c) {
       if (c == 3 && first && piece > 0) {
         // chunk 3 takes the place of the last piece's chunk 0
-        if (!wait_fast(sm, kBarOFree, (piece - 1) & 1, fault)) return;
+        if (!warp_wait_fast(sm, kBarOFree, (piece - 1) & 1, fault)) return;
         tc_fence_after();
       }
-      pv_chunk(tmem + o_column(piece, c), pa, pb, acc0, c);
-      if (c & 1) mma_commit(sm.bar(kBarFree + (c >> 1)));
+      pv_chunk(tmem + o_column(piece, c), pa + c * (2 * kSlabBytes >> 4), pb, acc0);
+      if (c & 1) commit_elected(sm.bar(kBarFree + (c >> 1)));
     }
     if (tile & kTileLast) ++piece;
   }
@@ -264,7 +286,6 @@ __device__ void mma_role(const Smem& sm, uint32_t tmem, int* fault) {
 __device__ void resolver_role(const qsfm_params& p, const Smem& sm, Range rg, int T, int* fault) {
   const int lane = threadIdx.x & 31;
   int* rows = sm.ring_rows();
-  const uint8_t* q8 = static_cast<const uint8_t*>(p.q);
   PieceIter pieces(&p, rg, T);
   uint32_t n = 0, m = 0;  // next tile, next piece
   auto put_piece = [&](int unit, int tiles, int whole) -> bool {
@@ -291,9 +312,8 @@ __device__ void resolver_role(const qsfm_params& p, const Smem& sm, Range rg, in
   while (pieces.next(unit, g, lo, hi)) {
     if (!put_piece(unit, max(hi - lo, 0), lo == 0 && hi == g.n_tiles ? 1 : 0)) return;
     if (lo >= hi) continue;
-    // the unit's Q goes to L2 a few tiles before its first product; the next
-    // token's index list while this one is resolved
-    if (lane == 0) bulk_prefetch_l2(q8 + size_t(unit) * kHeads * kDim * 2, kHeads * kDim * 2);
+    // the next token's index list goes to L2 while this one is resolved (q does
+    // not: what every CTA fetches ahead would drive out what the others did)
     if (p.cmp_sparse_indices != nullptr && g.tok + 1 < (T >> unit_shift(p))) {
       const uint8_t* ix = reinterpret_cast<const uint8_t*>(p.cmp_sparse_indices + (size_t)(g.tok + 1) * p.k2);
       for (int off = 128 * lane; off < 4 * p.k2; off += 32 * 128) prefetch_l2(ix + off);
@@ -435,9 +455,9 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
     if (rope) load_rope(row, v);
     else ra = load_codes(0, row);
     rb = load_codes(1, row);
-    if (!warp_wait_fast(sm, kBarPFull, n & 1, fault)) return;
     if (!rope) convert64(ra, s0, ex, ca);
     ra = load_codes(2, row);
+    if (!warp_wait_fast(sm, kBarPFull, n & 1, fault)) return;
     convert64(rb, s1, ex, cb);
     rb = load_codes(3, row);
   }
@@ -471,7 +491,7 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
   // through shared memory at the next barrier (so that all of them go the same
   // way, whatever an abort does to the ring).
   uint32_t taken = 0;
-  auto fetch_piece = [&]() {
+  auto fetch_piece = [&](uint32_t place) {
     const uint32_t slot = taken % Smem::kRing;
     Piece q = {-1, 0, 0, 0};
     if (wait_fast(sm, Smem::kBarPieceFull + slot, (taken / Smem::kRing) & 1, fault)) {
@@ -479,14 +499,15 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
       mbar_arrive(sm.bar(Smem::kBarPieceEmpty + slot));
       ++taken;
     }
-    sm.pieces()[Smem::kRing] = q;
+    sm.pieces()[Smem::kRing + place] = q;
     return q;
   };
   float* sinks = sm.f(kSSink);
   if (tid < p.n1) sinks[tid] = p.sinks != nullptr ? __ldg(p.sinks + tid) * kLog2e : -INFINITY;
   if (tid < 64) m_used[tid] = 0.f;  // the first unit's guess
+  uint32_t handed = 0;
   if (tid == 0) {
-    const Piece q = fetch_piece();
+    const Piece q = fetch_piece(0);
     if (q.tiles > 0) load_q(q.unit);
   }
   named_sync(kBarSm, kSmThreads);
@@ -570,7 +591,7 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
       // completed. Not earlier: at the start the resolver is still at the first
       // piece's tiles, and the softmax of the first would wait for the last.
       Piece next = {-1, 0, 0, 0};
-      if (k == cur.tiles - 1 && tid == 0) next = fetch_piece();
+      if (k == cur.tiles - 1 && tid == 0) next = fetch_piece(handed ^ 1u);
       warp_wait_fast(sm, kBarSFull, par, fault);
       if (next.tiles > 0 && !*sm.abort_flag()) load_q(next.unit);
       tc_fence_after();
@@ -674,12 +695,18 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
       }
     }
     // ---------------- the piece's sums, lse and 1 / den; the next piece
-    if (any) red[qd * 64 + h0 + lane] = l_sum;
-    named_sync(kBarSm, kSmThreads);
-    if (!any && tid == 0) {
-      const Piece next = fetch_piece();
+    if (any) {
+      red[qd * 64 + h0 + lane] = l_sum;
+    } else if (tid == 0) {
+      const Piece next = fetch_piece(handed ^ 1u);
       if (next.tiles > 0 && !*sm.abort_flag()) load_q(next.unit);
     }
+    // One barrier of all softmax warps. red, m_used and inv are used again behind
+    // the next one (the first tile's vote, or a piece's without tiles); of the
+    // two places of the handed piece, this one behind the next but one.
+    const bool stop = named_sync_or(kBarSm, kSmThreads, *sm.abort_flag());  // the same for all
+    handed ^= 1u;
+    cur = sm.pieces()[Smem::kRing + handed];
     if (tid >= kSmThreads - 64 && writable) {
       const int h = tid - (kSmThreads - 64);
       const float lt = any ? (red[h] + red[64 + h]) + (red[128 + h] + red[192 + h]) : 0.f;
@@ -695,7 +722,6 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
       }
       inv[64 * (live & 1) + h] = lt > 0.f ? 1.f / den : 0.f;
     }
-    named_sync(kBarSm, kSmThreads);
     if (any) {
       pending = Out{t, whole, writable ? slot : -1, live, n - 1};
       ++live;
@@ -705,12 +731,9 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
                            : reinterpret_cast<uint4*>(ws.out + size_t(slot) * 64 * kDim);
       for (int i = tid; i < 64 * kDim * (whole ? 2 : 4) / 16; i += kSmThreads) zeros[i] = z;
     }
-    cur = sm.pieces()[Smem::kRing];
-    const bool aborted = *sm.abort_flag();
-    // red, m_used and the handed piece are written again behind the next barrier
-    // of all softmax warps (the first tile's vote, or the next piece's)
-    if (named_sync_or(kBarSm, kSmThreads, aborted)) break;  // the same for all
+    if (stop) return;
   }
+  named_sync(kBarSm, kSmThreads);  // the last piece's inv
   if (pending.unit >= 0 && !*sm.abort_flag()) write_out(pending);
 }
 
@@ -723,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   sm.base = (raw_addr + 1023u) & ~1023u;
   sm.ptr = smem_raw + (sm.base - raw_addr);
 
-  const int tid = threadIdx.x, warp = tid >> 5;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (warp == 0) warm_first_token(p, T, blockIdx.x, gridDim.x, tid);
   grid_dependency_wait();    // the plan (and every input) is written by now
   grid_launch_dependents();  // the combine kernel may take SMs as CTAs finish
@@ -780,12 +803,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     fewer_registers<kLastRegs>();
     if (warp == kMmaWarp) {
       mma_role(sm, tmem, fault);
-      if ((tid & 31) == 0) {
-        // every MMA issued above has completed before tensor memory is freed
-        // (after an abort some may still be in flight)
-        mma_commit(sm.bar(kBarDrain));
-        wait_or_abort(sm, kBarDrain, 0, fault);
-      }
+      // every MMA issued above has completed before tensor memory is freed
+      // (after an abort some may still be in flight)
+      commit_elected(sm.bar(kBarDrain));
+      warp_wait_fast(sm, kBarDrain, 0, fault);
     } else if (warp == kResolverWarp) {
       resolver_role(p, sm, rg, T, fault);
     }
