@@ -9,7 +9,7 @@
 // operands of the score product are the inputs' own values.
 //
 // What differs is the division of labour: the softmax warps never wait for a
-// load, and the conversion of the codes is off the chain.
+// load, and as much of the codes' conversion as registers hold is off the chain.
 //   warps 0-7    softmax and epilogue: warp w reads tensor-memory lanes
 //                32 (w % 4) .. + 31 and heads 32 (w / 4) .. + 31;
 //   warps 8-15   producers: thread (row r, half h) converts and stores d-block
@@ -18,7 +18,7 @@
 //                eight bank groups of the swizzle. Two chunks are converted to
 //                registers ahead of PV freeing their places, so that only
 //                their stores follow;
-//   warp 16      MMA issue (one thread);
+//   warp 16      MMA issue;
 //   warp 17      resolver: walks the CTA's pieces (work units, or parts of one)
 //                and publishes them and their tiles' rows in two rings, so that
 //                no other warp waits for a length or an index (18 and 19 only
@@ -29,6 +29,22 @@
 // seven blocks of tensor memory, the next unit's the following four (modulo
 // seven), so its PV waits only for the first chunk to be read. The next unit's q
 // is requested as soon as the last score product of the unit has completed.
+//
+// What bounds it, per tile of 128 rows x 64 heads: the 64 MMAs read 6 KB of shared
+// memory each, 48 cycles at 128 B / cycle (measured: 48.1 issued back to back, the
+// same at N = 32 and beside busy warps), 3072 in all, where the tensor pipe alone
+// would take 2048; K~ takes 1024 to store and the codes some 2000 issue cycles to
+// convert (28 elements / cycle / SM: the conversion to f16 pairs, to fp32, one packed
+// product, one to bf16). The chain above runs them partly in turn: about 7100
+// cycles per tile, 3.6 us. Measured on 152 SMs: prefill in chunks (128 heads,
+// 640 rows per token) 595 us, 677 TFLOP/s; windows of 128 rows for 8192 tokens 285 us,
+// 3.8 TB/s of q, output and cache (a unit's output takes the softmax warps some
+// 5000 of 9000 cycles: their issue slots and the shared memory are the MMAs' and
+// producers' as well, and all roles' loops together are more code than the
+// instruction caches next to the schedulers hold: every variant with more of it
+// ran slower, whatever it saved); 128 requests of 2 tokens x 640 rows 50 us; 64 of 1 token on up
+// to 1024 rows 39 us, both with the plan (3 us) and most of it start and end: 2 to 4
+// tiles per CTA.
 #include "qsfm_attention_common.cuh"
 
 namespace qsfm {
@@ -42,25 +58,23 @@ constexpr int kResolverWarp = kMmaWarp + 1;
 constexpr int kThreads = (kMmaWarp + 4) * 32;
 // Registers per thread: 96 at launch (five warps on an SM sub-partition), then
 // 96 for the softmax warps, 112 for the producers, 64 for the last warpgroup.
-constexpr int kPrRegs = 112, kLastRegs = 64;
-static_assert(kSmThreads * 96 + kPrWarps * 32 * kPrRegs + 128 * kLastRegs <= kThreads * 96, "register split");
+constexpr int kLaunchRegs = 96, kPrRegs = 112, kLastRegs = 64;
+static_assert(kSmThreads * kLaunchRegs + kPrWarps * 32 * kPrRegs + 128 * kLastRegs <= kThreads * kLaunchRegs,
+              "register split");
 constexpr int kHPT = 32;                     // heads per softmax thread
 constexpr int kBarSm = 1;                    // named barrier of the softmax warps
 constexpr int kRowB = QSFM_PACKED384_ROW_BYTES;
+constexpr int kTileRing = 4;                 // tiles, and pieces, that the resolver may be ahead
 
-#ifndef RING
-#define RING 4
-#endif
-constexpr int kRing4 = RING;
 // shared memory map (byte offsets from a 1024-aligned base)
 constexpr uint32_t kSlabBytes = kTileRows * 128;              // 128 rows x 64 d (bf16): 16 KB
 constexpr uint32_t kSK = 0;                                   // K~ tile: 8 slabs
 constexpr uint32_t kSQ = kSK + 8 * kSlabBytes;                // Q: 8 d-blocks x 64 heads x 128 B
 constexpr uint32_t kSP = kSQ + 8 * 64 * 128;                  // P: 128 rows x 64 heads (bf16)
 constexpr uint32_t kSRows = kSP + kTileRows * 128;            // [ring][128] i32 physical rows
-constexpr uint32_t kSTile = kSRows + kRing4 * kTileRows * 4;    // [ring] i32: what the slot holds
-constexpr uint32_t kSPiece = kSTile + kRing4 * 4;             // [ring] pieces, then two being handed over
-constexpr uint32_t kSValid = kSPiece + (kRing4 + 2) * 16;     // [128] i32: row of the tile valid
+constexpr uint32_t kSTile = kSRows + kTileRing * kTileRows * 4;  // [ring] i32: what the slot holds
+constexpr uint32_t kSPiece = kSTile + kTileRing * 4;          // [ring] pieces, then two being handed over
+constexpr uint32_t kSValid = kSPiece + (kTileRing + 2) * 16;  // [128] i32: row of the tile valid
 constexpr uint32_t kSRed = kSValid + kTileRows * 4;           // [4][64] f32 per-quadrant partials
 constexpr uint32_t kSMUsed = kSRed + 1024;                    // [64] f32
 constexpr uint32_t kSAlpha = kSMUsed + 256;                   // [64] f32
@@ -101,9 +115,9 @@ struct __align__(16) Piece {
 };
 
 struct Smem {
-  static constexpr int kRing = kRing4;  // tiles, and pieces, in flight
-  static constexpr int kBarRowsFull = 11;    // [ring slot]
-  static constexpr int kBarRowsEmpty = 11 + kRing;   // [ring slot]: one arrive per producer warp and the MMA thread
+  static constexpr int kRing = kTileRing;
+  static constexpr int kBarRowsFull = 11;                // [ring slot]
+  static constexpr int kBarRowsEmpty = 11 + kRing;       // [ring slot]: one arrive per producer warp and the MMA warp
   static constexpr int kBarPieceFull = 11 + 2 * kRing;   // [ring slot]
   static constexpr int kBarPieceEmpty = 11 + 3 * kRing;  // [ring slot]
   static constexpr int kNumBars = 11 + 4 * kRing;
@@ -374,9 +388,9 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
   const int* rows = sm.ring_rows();
   const uint32_t rowb = sm.base + kSK + uint32_t(half) * kSlabBytes + uint32_t(r) * 128;
   const uint32_t sw = uint32_t(r & 7);
-  uint32_t ca[32], cb[32];  // converted blocks: chunks 0 and 1, then 2 and 3
+  uint32_t ca[32], cb[32];  // the two converted blocks
   Raw8 ra, rb;              // codes of the blocks to convert next
-  uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0, ex = 0;  // scale words of the four blocks, the rows' exponents
+  uint32_t s0 = 0, s1 = 0, s2 = 0, s3 = 0, ex = 0;  // scale words of the four blocks, the row's exponent
 
   auto take_rows = [&](uint32_t n, const uint8_t*& row, bool& v) -> bool {
     const int tile = read_tile(sm, n, fault);
@@ -422,16 +436,18 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
   bool v;
   if (!take_rows(0, row, v)) return;
   load_scales(row, v);
-  if (rope) load_rope(row, v);
-  else ra = load_codes(0, row);
+  if (!rope) ra = load_codes(0, row);
   rb = load_codes(1, row);
-  if (!rope) convert64(ra, s0, ex, ca);
-  convert64(rb, s1, ex, cb);
-  ra = load_codes(2, row);
-  rb = load_codes(3, row);
 #pragma unroll 1
   for (uint32_t n = 0;; ++n) {
-    // chunks 0 and 1 are converted, the codes of 2 and 3 loaded
+    // chunk 0 is converted at once, chunk 1 behind the last tile's P (its
+    // conversion would take the softmax's issue slots)
+    if (rope) load_rope(row, v);
+    else convert64(ra, s0, ex, ca);
+    ra = load_codes(2, row);
+    if (n > 0 && !warp_wait_fast(sm, kBarPFull, (n - 1) & 1, fault)) return;
+    convert64(rb, s1, ex, cb);
+    rb = load_codes(3, row);
     if (n > 0 && !warp_wait_fast(sm, kBarFree, (n - 1) & 1, fault)) return;
     if (rope) {
       // the tile's valid flags: the softmax has read the last tile's (its P was
@@ -448,18 +464,11 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
     convert64(rb, s3, ex, cb);
     store(3, cb);
     // the next tile: its loads after the last store (stores queue behind loads
-    // in the load/store unit), its first conversions once P is published (they
-    // would take the softmax's issue slots)
+    // in the load/store unit)
     if (!take_rows(n + 1, row, v)) return;
     load_scales(row, v);
-    if (rope) load_rope(row, v);
-    else ra = load_codes(0, row);
+    if (!rope) ra = load_codes(0, row);
     rb = load_codes(1, row);
-    if (!rope) convert64(ra, s0, ex, ca);
-    ra = load_codes(2, row);
-    if (!warp_wait_fast(sm, kBarPFull, n & 1, fault)) return;
-    convert64(rb, s1, ex, cb);
-    rb = load_codes(3, row);
   }
 }
 
@@ -521,7 +530,10 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
   };
   // Reads, scales and writes it: thread (lane d of a chunk) has one element of
   // each of its 32 heads. bf16 outputs are 64 contiguous bytes per head and warp
-  // in 2-byte stores: no exchange between lanes, nothing to wait for.
+  // in 2-byte stores: no exchange between lanes, nothing to wait for, few
+  // instructions. Windows for 8192 tokens: 295 us; with 16-byte stores of what
+  // stmatrix turns in shared memory 303 us, with 8-byte stores of what lanes
+  // exchange 331 us.
   auto write_out = [&](const Out& o) {
     // Free[1] of its last tile: every PV product is complete. (Free[0] may be a
     // phase ahead: the next piece's PV has begun.)
@@ -624,7 +636,7 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
         tmem_load(s_addr, x);
         tmem_ld_wait_for(x);
 #pragma unroll
-        for (int i = 0; i < kHPT; ++i) x[i] = v ? x[i] * qk_scale : -INFINITY;
+        for (int i = 0; i < kHPT; ++i) x[i] = v ? __fmul_rn(x[i], qk_scale) : -INFINITY;
         const float mx = reduce_lanes<true>(x);  // head h0 + lane, this quadrant's rows
         red[qd * 64 + h0 + lane] = mx;
         named_sync(kBarSm, kSmThreads);
@@ -663,7 +675,9 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
         for (int i = 0; i < kHPT; ++i) {
           const float m = m_used[h0 + i];
           const float mz = m == -INFINITY ? 0.f : m;
-          x[i] = ex2_approx(v ? fmaf(x[i], qk_scale, -mz) : -INFINITY);
+          // the product rounded as for the maximum: of a huge score, what a fused
+          // multiply-add keeps of the product's rounding would overflow 2^t
+          x[i] = ex2_approx(v ? __fsub_rn(__fmul_rn(x[i], qk_scale), mz) : -INFINITY);
         }
         lscale = 0.f;
       }
@@ -832,6 +846,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 cudaError_t launch_attention4(const qsfm_params& p, int num_tokens, int num_ctas, const Workspace& ws, int* fault,
                               cudaStream_t s) {
+  // The register split takes from what the launch gives: with fewer registers per
+  // thread than it counts on, the producers would wait for theirs forever.
+  static const cudaError_t split = [] {
+    cudaFuncAttributes a;
+    const cudaError_t q = cudaFuncGetAttributes(&a, attention4_kernel);
+    return q != cudaSuccess ? q : a.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
+  }();
+  if (split != cudaSuccess) return split;
   cudaError_t e = cudaFuncSetAttribute(attention4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
   CUtensorMap qmap;

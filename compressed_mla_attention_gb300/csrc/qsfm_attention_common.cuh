@@ -204,9 +204,10 @@ __device__ __forceinline__ void warm_first_token(const qsfm_params& p, int T, in
   }
 }
 
-// Tensor map of q (or attn_out, which has q's shape) viewed as [T * 64 rows, 512
-// bf16 columns], boxes of 64 rows (the heads of a unit) x `cols` columns.
-cudaError_t make_head_map(const void* base, int T, int cols, CUtensorMapSwizzle swizzle, CUtensorMap* map) {
+// Tensor map of q viewed as [T * 64 rows, 512 bf16 columns], boxes of 64 rows
+// (the heads of a unit) x 64 columns (128 B) with the 128-B swizzle of the MMA
+// operand.
+cudaError_t make_q_map(const void* q, int T, CUtensorMap* map) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -220,17 +221,13 @@ cudaError_t make_head_map(const void* base, int T, int cols, CUtensorMapSwizzle 
   if (encode == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {cuuint64_t(kDim), cuuint64_t(T) * kHeads};
   const cuuint64_t strides[1] = {cuuint64_t(kDim) * 2};
-  const cuuint32_t box[2] = {cuuint32_t(cols), 64};
+  const cuuint32_t box[2] = {64, 64};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
-                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(q), dims,
+                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
-// Boxes of 64 rows x 64 columns (128 B) with the 128-B swizzle of the MMA operand.
-cudaError_t make_q_map(const void* q, int T, CUtensorMap* map) {
-  return make_head_map(q, T, 64, CU_TENSOR_MAP_SWIZZLE_128B, map);
 }
 
 }  // namespace

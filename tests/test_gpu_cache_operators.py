@@ -466,6 +466,47 @@ def test_four_bit_attention_follows_the_bytes(cuda_device):
     assert np.array_equal(out, np.repeat(want[:, None], 64, axis=1)) and np.all(np.abs(lse) <= LSE_ATOL)
 
 
+@pytest.mark.parametrize("ctas", [1, 3])
+def test_four_bit_units_leave_one_another_alone(cuda_device, ctas):
+    """Queries that are tiny, huge, infinite or NaN, in heads of some tokens: the
+    units worked on after them by the same CTA, and their other heads, are what
+    they are without them."""
+    w = W.build("4-bit odd queries", layout="TND", q_lens=[50, 40], s2=[300, 40], cmp_ratio=4, mode="CSA", k2=256,
+                kv_format="packed384", seed=11)
+    q, odd = w.q.clone(), {}
+    for t, h, v in ((3, 0, float("inf")), (4, 1, float("nan")), (5, 2, float("-inf")), (20, 63, float("nan")),
+                    (60, 31, float("inf")), (61, 0, float("nan"))):
+        q[t, h, 17 * h % 512] = v
+        odd.setdefault(t, []).append(h)
+    q[8] *= 2.0 ** 60
+    q[9] *= 2.0 ** -60
+    q[30, ::2] *= -(2.0 ** 40)
+    w = dataclasses.replace(w, q=q)
+    out, lse = run_gpu(w, cuda_device, num_ctas=ctas, lse=True)
+    for t, heads in odd.items():
+        assert not np.isfinite(out[t, heads]).any() and not np.isfinite(lse[t, heads]).any()
+        # their products are not finite in the oracle either: the other heads against a query of ones there
+        q[t, heads] = 1.0
+    w = dataclasses.replace(w, q=q)
+    tokens = list(range(w.total_t))
+    o_ref, l_ref = O.reference(w, tokens)
+    for t, heads in odd.items():
+        out[t, heads], lse[t, heads] = o_ref[t, heads], l_ref[t, heads]
+    assert np.isfinite(out).all() and np.isfinite(lse).all()
+    four_bit_tolerance(out, lse, w, tokens)
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 5])
+def test_four_bit_units_without_rows_in_a_row(cuda_device, ctas):
+    """More units without rows one after the other than any ring holds, at the
+    start, between others, and at the end."""
+    s2 = [0] * 9 + [300, 0, 0, 128, 7] + [0] * 12 + [40] + [0] * 3
+    w = W.build("4-bit empty units", layout="TND", q_lens=[2] * len(s2), s2=s2, cmp_ratio=4, mode="CSA", k2=64,
+                kv_format="packed384", seed=12)
+    out, lse = run_gpu(w, cuda_device, num_ctas=ctas, lse=True)
+    four_bit_tolerance(out, lse, w, list(range(w.total_t)))
+
+
 def test_four_bit_full_decode_batch(cuda_device):
     w = W.config(2, kv_format="packed384")
     out, lse = run_gpu(w, cuda_device, lse=True)
