@@ -62,7 +62,8 @@ constexpr int kLaunchRegs = 96, kPrRegs = 112, kLastRegs = 64;
 static_assert(kSmThreads * kLaunchRegs + kPrWarps * 32 * kPrRegs + 128 * kLastRegs <= kThreads * kLaunchRegs,
               "register split");
 constexpr int kHPT = 32;                     // heads per softmax thread
-constexpr int kBarSm = 1;                    // named barrier of the softmax warps
+constexpr int kBarSm = 1;                    // named barriers: the softmax warps, the start
+constexpr int kBarSetup = 2;
 constexpr int kRowB = QSFM_PACKED384_ROW_BYTES;
 constexpr int kTileRing = 4;                 // tiles, and pieces, that the resolver may be ahead
 
@@ -762,29 +763,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (warp == 0) warm_first_token(p, T, blockIdx.x, gridDim.x, tid);
-  grid_dependency_wait();    // the plan (and every input) is written by now
-  grid_launch_dependents();  // the combine kernel may take SMs as CTAs finish
-  const int* meta = p.metadata;
-  if (meta[0] != kMetaMagic || meta[2] != T) {
-    if (tid == 0 && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_METADATA);
-    return;
-  }
-  const int G = meta[1];
-  if (G < 0 || G > int(gridDim.x) || G > QSFM_MAX_CTAS) {
-    if (tid == 0 && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_METADATA);
-    return;
-  }
-  const int c = blockIdx.x;
-  if (c >= G) return;
-  const Range rg{meta[kMetaHeader + 2 * c], meta[kMetaHeader + 2 * c + 1],
-                 meta[kMetaHeader + 2 * c + 2], meta[kMetaHeader + 2 * c + 3]};
-  if (rg.t0 < 0 || rg.t1 > T || rg.t0 > rg.t1 || rg.k0 < 0 || rg.k1 < 0 ||
-      (rg.t1 == T && rg.k1 != 0)) {
-    if (tid == 0) atomicOr(fault, QSFM_FAULT_METADATA);
-    return;
-  }
-  if (rg.t0 == rg.t1 && rg.k0 == rg.k1) return;
-
   if (tid == 0) {
     mbar_init(sm.bar(kBarQFull), 1);
     for (int i = 0; i < 4; ++i) mbar_init(sm.bar(kBarFull + i), kPrWarps);
@@ -802,9 +780,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     *sm.abort_flag() = 0;
     fence_mbar_init();
   }
+  __syncthreads();
+  grid_dependency_wait();    // the plan (and every input) is written by now
+  grid_launch_dependents();  // the combine kernel may take SMs as CTAs finish
+  const int* meta = p.metadata;
+  const int c = blockIdx.x;
+  // read at once: c is below QSFM_MAX_CTAS, so its range lies in the buffer whatever the header says
+  const int magic = meta[0], G = meta[1], planned = meta[2];
+  const Range rg{meta[kMetaHeader + 2 * c], meta[kMetaHeader + 2 * c + 1],
+                 meta[kMetaHeader + 2 * c + 2], meta[kMetaHeader + 2 * c + 3]};
+  if (magic != kMetaMagic || planned != T || G < 0 || G > int(gridDim.x) || G > QSFM_MAX_CTAS) {
+    if (tid == 0 && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_METADATA);
+    return;
+  }
+  if (c >= G) return;
+  if (rg.t0 < 0 || rg.t1 > T || rg.t0 > rg.t1 || rg.k0 < 0 || rg.k1 < 0 ||
+      (rg.t1 == T && rg.k1 != 0)) {
+    if (tid == 0) atomicOr(fault, QSFM_FAULT_METADATA);
+    return;
+  }
+  if (rg.t0 == rg.t1 && rg.k0 == rg.k1) return;
+
+  // The resolver does not wait for tensor memory: it reads its first lengths.
   if (warp == kMmaWarp) tmem_alloc(sm.tmem_slot(), kTmemCols);
   tc_fence_before();
-  __syncthreads();
+  if (warp != kResolverWarp) named_sync(kBarSetup, kThreads - 32);
   tc_fence_after();
   const uint32_t tmem = *sm.tmem_slot();
 
