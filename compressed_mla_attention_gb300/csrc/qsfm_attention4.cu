@@ -474,8 +474,8 @@ __device__ void producer_role(const qsfm_params& p, const Smem& sm, int* fault) 
 }
 
 // ------------------------------------------------------------- softmax, epilogue
-__device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_unit, uint32_t tmem, const Workspace& ws, int c_idx,
-                             const CUtensorMap* qmap, int* fault) {
+__device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_unit, uint32_t tmem, const Workspace& ws,
+                             int c_idx, const CUtensorMap* qmap, int* fault) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int qd = warp & 3;            // tensor-memory lane quadrant
   const int h0 = kHPT * (warp >> 2);  // first of this warp's heads

@@ -13,7 +13,11 @@
 // neighbouring lanes. A row is read once, held in registers and written once.
 // Query rows are bound by HBM, so what counts is bytes in flight: a warp streams
 // its rows through a ring in shared memory. The key rows are few; they are the
-// first blocks of the grid, one warp each, bound by latency.
+// first blocks of the grid, one warp each, bound by latency and by the
+// instructions of their last bits (below).
+// Measured: 4099 tokens of 128 + 1 bf16 rows 177 us, 6.1 TB/s of rows read and
+// written (90% of a copy's rate); 256 tokens 6.4 us; one token 3.5 us; 8191 fp32
+// key rows alone 12.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -27,7 +31,7 @@ namespace {
 
 constexpr int kRowWarps = 8;
 constexpr int kRowThreads = 32 * kRowWarps;
-constexpr int kRowBlocks = 3;  // blocks of query rows on an SM
+constexpr int kRowBlocks = 3;  // blocks on an SM
 // query rows a warp has in flight: 8 KB (1 KB a row, fp32 2 KB)
 template <typename T>
 constexpr int stages() {
@@ -147,18 +151,21 @@ __device__ __forceinline__ void turn8(const qsfm_norm_rope_params& p, int lane, 
   }
 }
 
+__device__ __forceinline__ float inverse_rms(const qsfm_norm_rope_params& p, const float (&y)[2][8]) {
+  float sum = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(y[h][i], y[h][i], sum);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
+  return rsqrtf(sum * (1.f / kDim) + p.eps);
+}
 // Norm and rotation of the row held by the warp.
 __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bool norm, const float (&w)[2][8],
                                               const Turn& turn, int lane, float (&y)[2][8]) {
   if (norm) {
-    float sum = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fmaf(y[h][i], y[h][i], sum);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-    const float inv = rsqrtf(sum * (1.f / kDim) + p.eps);
+    const float inv = inverse_rms(p, y);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -167,6 +174,140 @@ __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bo
   if (p.rope_dim == 0) return;
   if (rotated_half(p) == 0) turn8(p, lane, turn, y[0]);
   else turn8(p, lane, turn, y[1]);
+}
+
+// ------------------------------------------------------------- key rows
+// A stored row is rounded to few bits, so what matters is on which side of a
+// rounding border a value lies: key rows are computed as y + z, z what fp32 y
+// leaves over. In 8191 rows of 512 that are stored as bf16 fp32 alone puts 50
+// elements on the wrong side, and 3 to 6 of the codes of the other formats; this
+// none (with fp32 scales 1: the codes go by the scale as it is stored). It costs
+// the key rows half of their time (8191 fp32 rows 7.9 -> 12.2 us, one token 3.1
+// -> 3.5 us); the query rows, whose results are not stored codes, go without.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = a + b;
+  const float t = s - a;
+  e = (a - (s - t)) + (b - t);
+}
+__device__ __forceinline__ void two_product(float a, float b, float& p, float& e) {
+  p = __fmul_rn(a, b);
+  e = fmaf(a, b, -p);
+}
+// h + t as y + z; of an h that is not finite nothing is left
+__device__ __forceinline__ void renormed(float h, float t, float& y, float& z) {
+  if (!(fabsf(t) <= 3.402823466e38f)) t = 0.f;
+  y = h + t;
+  z = t - (y - h);
+}
+// a c + b d for a + az, b + bz
+__device__ __forceinline__ void turned(float a, float az, float c, float b, float bz, float d, float& y, float& z) {
+  float u, ue, v, ve, h, t;
+  two_product(a, c, u, ue);
+  two_product(b, d, v, ve);
+  two_sum(u, v, h, t);
+  t += fmaf(az, c, ue) + fmaf(bz, d, ve);
+  renormed(h, t, y, z);
+}
+__device__ __forceinline__ void turn8(const qsfm_norm_rope_params& p, int lane, const Turn& t, float (&y)[8],
+                                      float (&z)[8]) {
+  const int r = rotated_element(p, lane);
+  const bool in = r >= 0 && r < p.rope_dim;
+  if (p.interleaved) {
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = y[2 * i], az = z[2 * i], b = y[2 * i + 1], bz = z[2 * i + 1];
+        turned(a, az, t.c[i], b, bz, -t.s[i], y[2 * i], z[2 * i]);
+        turned(b, bz, t.c[i], a, az, t.s[i], y[2 * i + 1], z[2 * i + 1]);
+      }
+    }
+  } else {
+    const bool upper = r >= p.rope_dim / 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(kAll, y[i], p.rope_dim / 16), oz = __shfl_xor_sync(kAll, z[i], p.rope_dim / 16);
+      if (in) turned(y[i], z[i], t.c[i], other, oz, upper ? t.s[i] : -t.s[i], y[i], z[i]);
+    }
+  }
+}
+template <bool kExactSquares>  // of 16-bit inputs
+__device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bool norm, const float (&w)[2][8],
+                                              const Turn& turn, int lane, float (&y)[2][8], float (&z)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[h][i] = 0.f;
+  if (norm) {
+    float inv, inv_rest = 0.f;
+    if (p.kv_layout == QSFM_KV_FP8_FP32_SCALES) {
+      inv = inverse_rms(p, y);  // common to a value and its group's scale: no code depends on its last bits
+    } else {
+      float sum = 0.f, rest = 0.f;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float q, e, t;
+          two_product(y[h][i], y[h][i], q, e);
+          two_sum(sum, q, sum, t);
+          rest += kExactSquares ? t : t + e;
+        }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        float t;
+        const float other = __shfl_xor_sync(kAll, sum, o), other_rest = __shfl_xor_sync(kAll, rest, o);
+        two_sum(sum, other, sum, t);
+        rest = (rest + other_rest) + t;
+      }
+      float mean, t, q, e;
+      two_sum(sum * (1.f / kDim), p.eps, mean, t);
+      rest = fmaf(rest, 1.f / kDim, t);
+      // one step of Newton's method from the fp32 root: inv + inv_rest
+      inv = rsqrtf(mean);
+      two_product(inv, inv, q, e);
+      const float off = fmaf(-mean, q, 1.f) - fmaf(mean, e, rest * q);
+      inv_rest = 0.5f * inv * off;
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a, b, u, v;
+        two_product(inv, w[h][i], a, b);
+        b = fmaf(inv_rest, w[h][i], b);
+        two_product(y[h][i], a, u, v);
+        v = fmaf(y[h][i], b, v);
+        renormed(u, v, y[h][i], z[h][i]);
+      }
+  }
+  if (p.rope_dim == 0) return;
+  if (rotated_half(p) == 0) turn8(p, lane, turn, y[0], z[0]);
+  else turn8(p, lane, turn, y[1], z[1]);
+}
+
+// y + z in fp32 for a rounding to at most 22 bits: what is left over sets the
+// last bit, so the value lies on a border only where y + z does.
+__device__ __forceinline__ float sticky(float y, float z) {
+  const uint32_t b = __float_as_uint(y);
+  const bool rest = fabsf(z) > 0.f && fabsf(y) <= 3.402823466e38f;
+  return rest ? __uint_as_float(((y < 0.f) == (z < 0.f) ? b : b - 1) | 1u) : y;
+}
+__device__ __forceinline__ void sticky16(float (&y)[2][8], const float (&z)[2][8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[h][i] = sticky(y[h][i], z[h][i]);
+}
+// (y + z) / d, d > 0, in the same sense, for a rounding to at most 18 bits: the
+// quotient by the reciprocal (two ulps off at most) goes to the next multiple of
+// 16 ulps, and the sign of what is left over says on which side of it y + z is.
+__device__ __forceinline__ float sticky_quotient(float y, float z, float d, float reciprocal) {
+  const float a = fabsf(y);
+  uint32_t b = (__float_as_uint(a * reciprocal) + 8u) & ~15u;
+  const float left = fmaf(-__uint_as_float(b), d, a) + (y < 0.f ? -z : z);
+  if (left < 0.f && b > 0) b -= 1;
+  if (left < 0.f || left > 0.f) b |= 1u;
+  return copysignf(__uint_as_float(b), y);
 }
 
 __device__ __forceinline__ float max8(const float (&v)[8]) {
@@ -215,21 +356,34 @@ __device__ __forceinline__ uint2 dequant8(uint32_t codes, float scale, float (&v
   return make_uint2(0, 0);
 }
 
-// The warp's row into row `slot` of the cache (slot < 0: nowhere); y becomes
+// The warp's row y + z into row `slot` of the cache (slot < 0: nowhere); y becomes
 // the values that the stored row stands for.
-__device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int slot, int lane, float (&y)[2][8]) {
+__device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int slot, int lane, float (&y)[2][8],
+                                          const float (&z)[2][8]) {
   const bool put = slot >= 0;
   uint8_t* row = static_cast<uint8_t*>(p.kv_cache) + size_t(put ? slot : 0) * kv_row_bytes(p.kv_layout);
   if (p.kv_layout == QSFM_KV_FP8_FP32_SCALES) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float m = max8(y[h]);
+      float m = 0.f, rest = 0.f;  // the largest |y + z|
+      auto larger = [&](float a, float az) {
+        if (a > m || (a == m && az > rest)) m = a, rest = az;
+      };
 #pragma unroll
-      for (int o = 1; o <= 4; o <<= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, o));
-      const float scale = __fdiv_rn(fmaxf(m, 1e-12f), 448.f);
+      for (int i = 0; i < 8; ++i) larger(fabsf(y[h][i]), y[h][i] < 0.f ? -z[h][i] : z[h][i]);
+#pragma unroll
+      for (int o = 1; o <= 4; o <<= 1) {
+        const float a = __shfl_xor_sync(kAll, m, o), az = __shfl_xor_sync(kAll, rest, o);
+        larger(a, az);
+      }
+      if (m <= 1e-12f) m = 1e-12f, rest = 0.f;
+      float scale = m * (1.f / 448.f);
+      const float off = fmaf(-scale, 448.f, m) + rest;
+      if (fabsf(off) <= 3.402823466e38f) scale = fmaf(off, 1.f / 448.f, scale);
+      const float reciprocal = __frcp_rn(scale);
       float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(y[h][i], scale);
+      for (int i = 0; i < 8; ++i) q[i] = sticky_quotient(y[h][i], z[h][i], scale, reciprocal);
       const uint2 code = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
       if (put) {
         *reinterpret_cast<uint2*>(row + 256 * h + 8 * lane) = code;
@@ -240,6 +394,7 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
     }
     return;
   }
+  sticky16(y, z);
   if (p.kv_layout == QSFM_KV_BF16) {
     if (put) {
 #pragma unroll
@@ -311,14 +466,13 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
     float m = max8(y[h]);
     m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
     ok &= __shfl_xor_sync(kAll, int(ok), 1) != 0;
-    const float want = __fdiv_rn(m, 6.f) * inv_power;
+    const float want = sticky_quotient(m, 0.f, 6.f, 1.f / 6.f) * inv_power;
     const uint32_t s8 = ok ? e4m3x4(want, 0.f, 0.f, 0.f) & 0xFFu : 0x7Fu;
     const float scale = of_e4m3(s8) * power;
-    // a division, not a product with the reciprocal: a quotient on a rounding
-    // border stays on it
+    const float reciprocal = scale > 0.f ? __frcp_rn(scale) : 0.f;
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = scale > 0.f ? __fdiv_rn(y[h][i], scale) : 0.f;
+    for (int i = 0; i < 8; ++i) q[i] = scale > 0.f ? sticky_quotient(y[h][i], 0.f, scale, reciprocal) : 0.f;
     const uint32_t code = e2m1x8(q);
     if (rope) {
       if (put) store8_bf16(reinterpret_cast<__nv_bfloat16*>(row) + el, y[h]);
@@ -357,18 +511,16 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
 // A warp streams them through a ring of its own in shared memory, kStages rows
 // in flight (asynchronous copies; each lane reads back only what it copied, so
 // no barrier), and keeps the token's cosines and sines from head to head.
-// Without queries (kQueries false) the key rows take fewer registers, so that
-// more of them are in flight: 8191 fp32 rows in 8.7 us instead of 10.4.
-template <typename T, bool kQueries>
-__global__ void __launch_bounds__(kRowThreads, kQueries ? kRowBlocks : 4) norm_rope_kernel(const qsfm_norm_rope_params p, const int kv_blocks,
-                                                                const int per, int* fault) {
+template <typename T>
+__global__ void __launch_bounds__(kRowThreads, kRowBlocks)
+    norm_rope_kernel(const qsfm_norm_rope_params p, const int kv_blocks, const int per, int* fault) {
   extern __shared__ __align__(16) uint8_t s_rows[];
   constexpr int kStages = stages<T>();
   constexpr int kVec = sizeof(T) / 2;  // 16-byte vectors of 8 elements
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float w[2][8], y[2][8];
   Turn turn;
-  if (!kQueries || int(blockIdx.x) < kv_blocks) {
+  if (int(blockIdx.x) < kv_blocks) {
     const int t = blockIdx.x * kRowWarps + warp;
     if (t >= p.tokens) return;
     const T* src = static_cast<const T*>(p.kv) + size_t(t) * p.kv_token_stride + 8 * lane;
@@ -382,12 +534,13 @@ __global__ void __launch_bounds__(kRowThreads, kQueries ? kRowBlocks : 4) norm_r
     if (p.rope_dim != 0) load_turn(p, pos, lane, turn);
     raw[0].get(y[0]);
     raw[1].get(y[1]);
-    norm_rope_row(p, p.norm_kv != 0, w, turn, lane, y);
+    float z[2][8];
+    norm_rope_row<sizeof(T) == 2>(p, p.norm_kv != 0, w, turn, lane, y, z);
     if (slot >= 0 && (slot >> 7) >= p.num_blocks) {
       if (lane == 0) atomicOr(fault, QSFM_FAULT_SLOT);
       slot = -1;
     }
-    store_row(p, slot, lane, y);
+    store_row(p, slot, lane, y, z);
     if (p.kv_out != nullptr) {
       __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.kv_out) + size_t(t) * kDim + 8 * lane;
       store8_bf16(out, y[0]);
@@ -406,7 +559,8 @@ __global__ void __launch_bounds__(kRowThreads, kQueries ? kRowBlocks : 4) norm_r
   const uint32_t ring = smem_u32(s_rows) + uint32_t(warp * kStages) * kDim * sizeof(T) + 16 * lane;
   auto request = [&](int r) {
     if (r < r1) {
-      const T* src = static_cast<const T*>(p.q) + size_t(t_in) * p.q_token_stride + size_t(head_in) * p.q_head_stride + 8 * lane;
+      const T* src = static_cast<const T*>(p.q) + size_t(t_in) * p.q_token_stride +
+                     size_t(head_in) * p.q_head_stride + 8 * lane;
       const uint32_t dst = ring + uint32_t((r - r0) / kRowWarps % kStages) * kDim * sizeof(T);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -461,11 +615,11 @@ template <typename T>
 cudaError_t launch_rows(const qsfm_norm_rope_params& p, int* fault, cudaStream_t s) {
   const int kv_blocks = p.kv != nullptr ? (p.tokens + kRowWarps - 1) / kRowWarps : 0;
   if (p.q == nullptr) {
-    norm_rope_kernel<T, false><<<kv_blocks, kRowThreads, 0, s>>>(p, kv_blocks, 0, fault);
+    norm_rope_kernel<T><<<kv_blocks, kRowThreads, 0, s>>>(p, kv_blocks, 0, fault);
     return cudaGetLastError();
   }
   constexpr int kSmem = kRowWarps * stages<T>() * kDim * int(sizeof(T));
-  cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  cudaError_t e = cudaFuncSetAttribute(norm_rope_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   int dev = 0, sms = 0;
   if (e == cudaSuccess) e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -476,7 +630,7 @@ cudaError_t launch_rows(const qsfm_norm_rope_params& p, int* fault, cudaStream_t
   int per = (rows + blocks - 1) / blocks;
   per = (per + kRowWarps - 1) / kRowWarps * kRowWarps;
   const int q_blocks = (rows + per - 1) / per;
-  norm_rope_kernel<T, true><<<kv_blocks + q_blocks, kRowThreads, kSmem, s>>>(p, kv_blocks, per, fault);
+  norm_rope_kernel<T><<<kv_blocks + q_blocks, kRowThreads, kSmem, s>>>(p, kv_blocks, per, fault);
   return cudaGetLastError();
 }
 

@@ -465,8 +465,9 @@ qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* p, void* workspace
  *   positions[t]: (a, b) -> (a cos - b sin, b cos + a sin) with the pairs
  *   (2i, 2i + 1) when interleaved is set, (i, i + rope_dim / 2) otherwise,
  *   cos = cos_sin[pos][i], sin = cos_sin[pos][rope_dim / 2 + i]
- * in fp32 throughout, rounded once: q_out[t] in bf16; the kv row in the row
- * format kv_layout at row slot_map[t] of the cache (kv_cache is
+ * in fp32, rounded once: q_out[t] in bf16; the kv row, whose fp32 values are
+ * carried with what they leave over so that every code is the formula's, in
+ * the row format kv_layout at row slot_map[t] of the cache (kv_cache is
  * [num_blocks, 128, 1, row], row s its s-th row).
  *   packed384  exponent byte 127 + E, E = floor(log2 max|y|) - 10 over the
  *              whole row (clipped to -100 .. 100), scale = e4m3(max|y| of the
