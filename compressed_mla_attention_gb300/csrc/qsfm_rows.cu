@@ -16,8 +16,8 @@
 // first blocks of the grid, one warp each, bound by latency and by the
 // instructions of their last bits (below).
 // Measured: 4099 tokens of 128 + 1 bf16 rows 177 us, 6.1 TB/s of rows read and
-// written (90% of a copy's rate); 256 tokens 6.4 us; one token 3.5 us; 8191 fp32
-// key rows alone 12.2 us.
+// written (90% of a copy's rate); 256 tokens 6.4 us; one token 3.6 us; 8191 fp32
+// key rows alone 12.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -181,9 +181,9 @@ __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bo
 // rounding border a value lies: key rows are computed as y + z, z what fp32 y
 // leaves over. In 8191 rows of 512 that are stored as bf16 fp32 alone puts 50
 // elements on the wrong side, and 3 to 6 of the codes of the other formats; this
-// none (with fp32 scales 1: the codes go by the scale as it is stored). It costs
-// the key rows half of their time (8191 fp32 rows 7.9 -> 12.2 us, one token 3.1
-// -> 3.5 us); the query rows, whose results are not stored codes, go without.
+// none. It costs the key rows half of their time (8191 fp32 rows 7.9 -> 12.0 us,
+// one token 3.1 -> 3.6 us); the query rows, whose results are not stored codes, go
+// without.
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = a + b;
   const float t = s - a;
@@ -298,13 +298,13 @@ __device__ __forceinline__ void sticky16(float (&y)[2][8], const float (&z)[2][8
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[h][i] = sticky(y[h][i], z[h][i]);
 }
-// (y + z) / d, d > 0, in the same sense, for a rounding to at most 18 bits: the
+// (y + z) / (d + dz), d > 0, in the same sense, for a rounding to at most 18 bits: the
 // quotient by the reciprocal (two ulps off at most) goes to the next multiple of
 // 16 ulps, and the sign of what is left over says on which side of it y + z is.
-__device__ __forceinline__ float sticky_quotient(float y, float z, float d, float reciprocal) {
+__device__ __forceinline__ float sticky_quotient(float y, float z, float d, float dz, float reciprocal) {
   const float a = fabsf(y);
   uint32_t b = (__float_as_uint(a * reciprocal) + 8u) & ~15u;
-  const float left = fmaf(-__uint_as_float(b), d, a) + (y < 0.f ? -z : z);
+  const float q = __uint_as_float(b), left = fmaf(-q, d, a) + fmaf(-q, dz, y < 0.f ? -z : z);
   if (left < 0.f && b > 0) b -= 1;
   if (left < 0.f || left > 0.f) b |= 1u;
   return copysignf(__uint_as_float(b), y);
@@ -379,11 +379,15 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
       if (m <= 1e-12f) m = 1e-12f, rest = 0.f;
       float scale = m * (1.f / 448.f);
       const float off = fmaf(-scale, 448.f, m) + rest;
-      if (fabsf(off) <= 3.402823466e38f) scale = fmaf(off, 1.f / 448.f, scale);
+      float scale_rest = 0.f;  // codes go by max|y| / 448 itself, of which `scale` is the rounding
+      if (fabsf(off) <= 3.402823466e38f) {
+        scale = fmaf(off, 1.f / 448.f, scale);
+        scale_rest = (fmaf(-scale, 448.f, m) + rest) * (1.f / 448.f);
+      }
       const float reciprocal = __frcp_rn(scale);
       float q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = sticky_quotient(y[h][i], z[h][i], scale, reciprocal);
+      for (int i = 0; i < 8; ++i) q[i] = sticky_quotient(y[h][i], z[h][i], scale, scale_rest, reciprocal);
       const uint2 code = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
       if (put) {
         *reinterpret_cast<uint2*>(row + 256 * h + 8 * lane) = code;
@@ -466,13 +470,13 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
     float m = max8(y[h]);
     m = fmaxf(m, __shfl_xor_sync(kAll, m, 1));
     ok &= __shfl_xor_sync(kAll, int(ok), 1) != 0;
-    const float want = sticky_quotient(m, 0.f, 6.f, 1.f / 6.f) * inv_power;
+    const float want = sticky_quotient(m, 0.f, 6.f, 0.f, 1.f / 6.f) * inv_power;
     const uint32_t s8 = ok ? e4m3x4(want, 0.f, 0.f, 0.f) & 0xFFu : 0x7Fu;
     const float scale = of_e4m3(s8) * power;
     const float reciprocal = scale > 0.f ? __frcp_rn(scale) : 0.f;
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = scale > 0.f ? sticky_quotient(y[h][i], 0.f, scale, reciprocal) : 0.f;
+    for (int i = 0; i < 8; ++i) q[i] = scale > 0.f ? sticky_quotient(y[h][i], 0.f, scale, 0.f, reciprocal) : 0.f;
     const uint32_t code = e2m1x8(q);
     if (rope) {
       if (put) store8_bf16(reinterpret_cast<__nv_bfloat16*>(row) + el, y[h]);

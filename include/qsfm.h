@@ -476,7 +476,7 @@ qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* p, void* workspace
  *   packed640  exponent of each 64 nope elements the smallest with max|y| <=
  *              448 2^(e - 127) (e clipped to 27 .. 227), code = e4m3(y / 2^(e - 127))
  *   fp8        scale = max|y| of each 64 / 448 (at least 1e-12 / 448), code =
- *              e4m3(y / scale)
+ *              e4m3(y / scale), scale as it is before its rounding to fp32
  *   A scale group with an element that is not finite stores a scale of NaN
  *   (packed formats); the other groups are as without it.
  * A token whose position is negative is padding: nothing is written for it. A
