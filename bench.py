@@ -52,7 +52,7 @@ FLUSH_BYTES = 512 << 20  # > 129 MB L2
 KV_ROW_BYTES = {"fp8_fp32_scales": 512 + 8 * 4, "packed640": 640, "packed384": 384, "bf16": 1024}
 FLOPS_PER_ROW_HEAD = 4 * 512  # QK^T + PV per attended (token, row) and head
 KERNEL_SRCS = [os.path.join(ROOT, "compressed_mla_attention_gb300", "csrc", f)
-               for f in ("qsfm_attention.cu", "qsfm_device.cuh")]
+               for f in ("qsfm_attention.cu", "qsfm_attention_common.cuh", "qsfm_device.cuh")]
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "attention_traffic.txt")
 
 
@@ -90,7 +90,7 @@ def measured_peaks():
 
 
 def kernel_sha() -> str:
-    """Hash of the attention kernel's sources (its file and the device header
+    """Hash of the attention kernel's sources (its file and the device headers
     it inlines): a recorded traffic figure holds only for this hash."""
     h = hashlib.sha256()
     for path in KERNEL_SRCS:

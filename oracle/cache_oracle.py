@@ -54,8 +54,7 @@ def pack384(y, e2m1, e4m3):
     codes = np.zeros(448, dtype=np.int64)
     for g in range(28):
         t = y[64 + 16 * g:80 + 16 * g]
-        # fp32 quotient, as the definition's amax / 6 is one rounding away from it
-        want = np.float64(np.float32(np.abs(t).max()) / np.float32(6.0)) * 2.0 ** -e
+        want = np.abs(t).max() / 6.0 * 2.0 ** -e
         c = int(nearest(min(want, 448.0), e4m3))
         out[352 + g] = c
         s = e4m3[c] * 2.0 ** e
