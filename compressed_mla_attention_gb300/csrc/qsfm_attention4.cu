@@ -45,6 +45,8 @@
 // ran slower, whatever it saved); 128 requests of 2 tokens x 640 rows 50 us; 64 of 1 token on up
 // to 1024 rows 39 us, both with the plan (3 us) and most of it start and end: 2 to 4
 // tiles per CTA.
+#include <atomic>
+
 #include "qsfm_attention_common.cuh"
 
 namespace qsfm {
@@ -848,12 +850,14 @@ cudaError_t launch_attention4(const qsfm_params& p, int num_tokens, int num_ctas
                               cudaStream_t s) {
   // The register split takes from what the launch gives: with fewer registers per
   // thread than it counts on, the producers would wait for theirs forever.
-  static const cudaError_t split = [] {
+  static std::atomic<bool> enough{false};
+  if (!enough.load(std::memory_order_relaxed)) {
     cudaFuncAttributes a;
     const cudaError_t q = cudaFuncGetAttributes(&a, attention4_kernel);
-    return q != cudaSuccess ? q : a.numRegs >= kLaunchRegs ? cudaSuccess : cudaErrorInvalidConfiguration;
-  }();
-  if (split != cudaSuccess) return split;
+    if (q != cudaSuccess) return q;
+    if (a.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    enough.store(true, std::memory_order_relaxed);
+  }
   cudaError_t e = cudaFuncSetAttribute(attention4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemAlloc);
   if (e != cudaSuccess) return e;
   CUtensorMap qmap;

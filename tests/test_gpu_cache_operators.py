@@ -507,6 +507,38 @@ def test_four_bit_units_without_rows_in_a_row(cuda_device, ctas):
     four_bit_tolerance(out, lse, w, list(range(w.total_t)))
 
 
+def test_four_bit_rows_through_the_other_entry_points(cuda_device):
+    """The pass without a workspace gives the bits of the one with, and the
+    gather exports the rows' bytes."""
+    w = W.build("4-bit entries", layout="TND", q_lens=[5, 3], s2=[700, 9000], cmp_ratio=4, mode="CSA", k2=512,
+                kv_format="packed384", seed=13)
+    args = W.device_inputs(w, cuda_device)
+    args.pop("return_softmax_lse")
+    out, plan = torch.empty_like(args["q"]), torch.empty(Q.METADATA_INTS, dtype=torch.int32, device=cuda_device)
+    lse = torch.empty(w.total_t, 64, device=cuda_device)
+    p = Q.make_params(attn_out=out, softmax_lse=lse, metadata=plan, return_lse=True, num_ctas=24, **args)
+    Q.metadata(p, plan)
+    size = Q.workspace_size(p)
+    assert size > 0  # fewer tokens than CTAs: the scratch is used
+    Q.forward(p, torch.empty(size, dtype=torch.uint8, device=cuda_device))
+    want = out.clone(), lse.clone()
+    out.fill_(float("nan")), lse.fill_(float("nan"))
+    Q.forward_noalloc(p)
+    torch.cuda.synchronize()
+    assert Q.device_status() == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    tokens = [0, 4, 5, 7]
+    new = lambda *s, t=torch.int32: torch.empty(*s, dtype=t, device=cuda_device)  # noqa: E731
+    rows, ids, counts = new(4, 1280, 384, t=torch.uint8), new(4, 1280), new(4)
+    Q.debug_gather(p, i32(tokens, cuda_device), 1280, rows, None, ids, counts)
+    torch.cuda.synchronize()
+    assert Q.device_status() == 0
+    tb, tp = w.token_batch(), w.token_pos()
+    for j, t in enumerate(tokens):
+        k = O.token_kv(w, t, int(tb[t]), int(tp[t]))
+        got = rows[j, :int(counts[j])][(ids[j, :int(counts[j])] >= 0).nonzero()[:, 0]].cpu().numpy()
+        assert np.array_equal(O.decode_rows(got, None), k)
+
+
 def test_four_bit_full_decode_batch(cuda_device):
     w = W.config(2, kv_format="packed384")
     out, lse = run_gpu(w, cuda_device, lse=True)
