@@ -778,7 +778,9 @@ def norm_rope_store(q=None, kv=None, *, stream=None, **kwargs):
     token, left alone) index cos_sin fp32 [P, rope_dim] (cosines, then sines);
     q_weight / kv_weight [512] fp32 or bf16; interleaved rotates elements
     (2i, 2i + 1) from rope_offset on, else (i, i + rope_dim / 2). norm_q /
-    norm_kv False leave the norm out. Returns q_out (None without q).
+    norm_kv False leave the norm out. With a stream of its own the call expects
+    its inputs to be there for that stream, and to live until it has run.
+    Returns q_out (None without q).
     """
     import torch
 
@@ -850,7 +852,9 @@ def update_block_tables(block_table, prev_lens, lens, free_list, free_count, *, 
     given, with positions) gets the pool row of every new row and positions
     its token position, -1 behind the last; cu_rows int32 [B + 1] the rows'
     prefix sums; residual int32 [B] the tokens behind the last row. num_blocks
-    bounds the block ids (default: P). Returns (slot_map, positions).
+    bounds the block ids (default: P). With a stream of its own the call expects
+    its inputs to be there for that stream, and to live until it has run.
+    Returns (slot_map, positions).
     """
     import torch
 

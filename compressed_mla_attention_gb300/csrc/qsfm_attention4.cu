@@ -31,20 +31,19 @@
 // is requested as soon as the last score product of the unit has completed.
 //
 // What bounds it, per tile of 128 rows x 64 heads: the 64 MMAs read 6 KB of shared
-// memory each, 48 cycles at 128 B / cycle (measured: 48.1 issued back to back, the
-// same at N = 32 and beside busy warps), 3072 in all, where the tensor pipe alone
-// would take 2048; K~ takes 1024 to store and the codes some 2000 issue cycles to
-// convert (28 elements / cycle / SM: the conversion to f16 pairs, to fp32, one packed
-// product, one to bf16). The chain above runs them partly in turn: about 7100
-// cycles per tile, 3.6 us. Measured on 152 SMs: prefill in chunks (128 heads,
-// 640 rows per token) 595 us, 677 TFLOP/s; windows of 128 rows for 8192 tokens 285 us,
-// 3.8 TB/s of q, output and cache (a unit's output takes the softmax warps some
-// 5000 of 9000 cycles: their issue slots and the shared memory are the MMAs' and
-// producers' as well, and all roles' loops together are more code than the
-// instruction caches next to the schedulers hold: every variant with more of it
-// ran slower, whatever it saved); 128 requests of 2 tokens x 640 rows 50 us; 64 of 1 token on up
-// to 1024 rows 39 us, both with the plan (3 us) and most of it start and end: 2 to 4
-// tiles per CTA.
+// memory each, 48 cycles at 128 B / cycle (48.8 measured, issued back to back, and the
+// same beside busy warps), where the tensor pipe alone would take 32; K~ takes 1024
+// cycles to store and the codes some 2000 issue cycles to convert (28 elements / cycle /
+// SM: the conversion to f16 pairs, to fp32, one packed product, one to bf16). The chain
+// above runs them partly in turn: about 7100 cycles per tile, 3.6 us. Measured on 152
+// SMs: prefill in chunks (128 heads, 640 rows per token) 590 us, 683 TFLOP/s; windows of
+// 128 rows for 8192 tokens 285 us, 3.8 TB/s of q, output and cache (a unit's output
+// takes the softmax warps some 5000 of 9000 cycles: their issue slots and the shared
+// memory are the MMAs' and producers' as well, and all roles' loops together are more
+// code than the instruction caches next to the schedulers hold: every variant with more
+// of it ran slower, whatever it saved); 128 requests of 2 tokens x 640 rows 47 us; 64 of
+// 1 token on up to 1152 rows 36 us, both with the plan (3 us), and 10 us of them start
+// and end.
 #include <atomic>
 
 #include "qsfm_attention_common.cuh"
