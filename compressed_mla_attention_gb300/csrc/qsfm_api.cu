@@ -581,8 +581,10 @@ qsfm_status qsfm_norm_rope_store(const qsfm_norm_rope_params* p, void* stream) {
   if (p->tokens == 0) return QSFM_OK;
   int* fault = fault_ptr();
   if (fault == nullptr) return QSFM_ERR_CUDA;
+  qsfm_norm_rope_params rows = *p;
+  if (rows.kv_cache == nullptr) rows.kv_layout = QSFM_KV_BF16;  // what kv_out alone holds
   const NvtxRange range("qsfm_norm_rope_store");
-  return cuda_status(qsfm::launch_norm_rope(*p, fault, static_cast<cudaStream_t>(stream)));
+  return cuda_status(qsfm::launch_norm_rope(rows, fault, static_cast<cudaStream_t>(stream)));
 }
 
 void qsfm_block_table_params_init(qsfm_block_table_params* p) {

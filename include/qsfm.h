@@ -477,6 +477,8 @@ qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* p, void* workspace
  *              448 2^(e - 127) (e clipped to 27 .. 227), code = e4m3(y / 2^(e - 127))
  *   fp8        scale = max|y| of each 64 / 448 (at least 1e-12 / 448), code =
  *              e4m3(y / scale), scale as it is before its rounding to fp32
+ *              (the root that both share is fp32's: stored scales are within
+ *              20 2^-24 of the formula's)
  *   A scale group with an element that is not finite stores a scale of NaN
  *   (packed formats); the other groups are as without it.
  * A token whose position is negative is padding: nothing is written for it. A

@@ -315,6 +315,79 @@ def test_norm_rope_store_matches_the_oracle(cuda_device, name, fmt):
         assert np.array_equal(values[stored], held)
 
 
+def half_even(x, bits, lowest=0.0):
+    """x to `bits` significant bits, none finer than `lowest`, ties to even."""
+    with np.errstate(divide="ignore"):
+        unit = np.maximum(np.exp2(np.floor(np.log2(np.abs(x))) + 1 - bits), lowest)
+    return np.where(x == 0, 0, np.round(x / np.where(x == 0, 1, unit)) * unit)
+
+
+def formula_rows(y, fmt):
+    """The values that rows y [n, 512] are held as, by the formats' definitions in 64 bits."""
+    if fmt == "bf16":
+        return half_even(y, 8)
+    n = len(y)
+    if fmt == "fp8_fp32_scales":
+        t = y.reshape(n, 8, 64)
+        scale = np.abs(t).max(2, keepdims=True) / 448
+        return (half_even(t / scale, 4, 2.0 ** -9) * scale).reshape(n, 512)
+    rope = half_even(y[:, :64], 8)
+    if fmt == "packed640":
+        t = y[:, 64:].reshape(n, 7, 64)
+        scale = np.exp2(np.ceil(np.log2(np.abs(t).max(2, keepdims=True) / 448)))
+        return np.concatenate((rope, (half_even(t / scale, 4, 2.0 ** -9) * scale).reshape(n, 448)), 1)
+    t = y[:, 64:].reshape(n, 28, 16)
+    power = np.exp2(np.floor(np.log2(np.abs(y).max(1))) - 10)[:, None, None]
+    scale = half_even(np.abs(t).max(2, keepdims=True) / 6 / power, 4, 2.0 ** -9) * power
+    return np.concatenate((rope, (np.clip(half_even(t / scale, 2, 0.5), -6, 6) * scale).reshape(n, 448)), 1)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_stored_rows_are_the_formulas(cuda_device, fmt, dtype):
+    """Every stored element is the rounding of the exact one. The kernel carries
+    y to about 2^-40 of the products it is made of, so of the 600,000 elements
+    one in 10^5 trials would be so near a rounding border; fp32 alone is off
+    in some ten (bf16)."""
+    dev, n = cuda_device, 1200
+    g = torch.Generator().manual_seed(21)
+    kv = (2 * torch.randn(n, 512, generator=g)).to(dtype).to(dev)
+    w = (1 + 0.3 * torch.randn(512, generator=g)).to(dev)
+    pos = torch.randint(0, 3000, (n,), generator=g).int()
+    slots = torch.randperm(1280, generator=g)[:n].int()
+    for inter, offset in ((True, 0), (False, 448)):
+        cache, scale = new_cache(fmt, 10, dev)
+        out = torch.empty(n, 512, dtype=torch.bfloat16, device=dev)
+        Q.norm_rope_store(None, kv, kv_cache=cache, kv_scale=scale, kv_out=out, slot_map=slots.to(dev), positions=pos.to(dev),
+                          cos_sin=table_of(3000, 64, dev), kv_weight=w, rope_offset=offset, interleaved=inter)
+        torch.cuda.synchronize()
+        y, _ = reference_rows(kv, w, pos.numpy(), table_of(3000, 64, dev), offset, inter, eps=float(np.float32(1e-6)))
+        want, got = formula_rows(y, fmt), cache_values(cache, scale, slots.numpy())
+        if fmt == "fp8_fp32_scales":
+            # the codes are the formula's; the root of fp8 rows, common to a group and its scale, is fp32's: 15 of the
+            # 20 units in Y_REL, and three roundings (two products, the scale's own)
+            exact = np.abs(y.reshape(n, 8, 64)).max(2) / 448
+            codes = cache_values(cache, torch.ones_like(scale), slots.numpy())
+            assert np.array_equal(codes, half_even(y / np.repeat(exact, 64, axis=1), 4, 2.0 ** -9))
+            held = scale.cpu().double().numpy().reshape(-1, 8)[slots.numpy()]
+            assert np.all(np.abs(held - exact) <= Y_REL * exact)
+        else:
+            assert np.array_equal(got, want)
+            assert np.array_equal(out.double().cpu().numpy(), want)
+
+
+def test_key_rows_without_a_cache(cuda_device):
+    """kv_out alone: the rows in bf16."""
+    g = torch.Generator().manual_seed(22)
+    kv = torch.randn(70, 512, generator=g).to(cuda_device)
+    out = torch.empty(70, 512, dtype=torch.bfloat16, device=cuda_device)
+    pos = torch.arange(70, dtype=torch.int32)
+    Q.norm_rope_store(None, kv, kv_out=out, positions=pos.to(cuda_device), cos_sin=table_of(70, 64, cuda_device))
+    torch.cuda.synchronize()
+    y, _ = reference_rows(kv, None, pos.numpy(), table_of(70, 64, cuda_device), 0, True, eps=float(np.float32(1e-6)))
+    assert np.array_equal(out.double().cpu().numpy(), half_even(y, 8))
+
+
 @pytest.mark.parametrize("fmt", ["packed384", "packed640"])
 def test_rows_as_they_are_are_stored_bit_for_bit(cuda_device, fmt):
     """Without norm and rotation the quantisation of bf16 rows is exact,
