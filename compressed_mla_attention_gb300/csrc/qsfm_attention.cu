@@ -73,6 +73,8 @@ constexpr int kMmaWarp = kWorkWarps;
 constexpr int kResolverWarp = kMmaWarp + 1;
 constexpr int kThreads = (kResolverWarp + 1) * 32;
 constexpr int kRing = 8;     // tiles of resolved rows in flight
+constexpr int kResolveTiles = 1;  // tiles per resolver pass (more keeps more loads in flight, at a
+                                  // larger instruction footprint; the ring already runs 8 tiles ahead)
 constexpr int kBarWork = 1;  // named barrier id of the worker warps
 
 // shared memory map (byte offsets from a 1024-aligned base)
@@ -124,11 +126,8 @@ constexpr uint32_t kIdescPV = make_idesc_bf16(128, 64, /*a_mn=*/1, /*b_mn=*/1, k
 constexpr int kMaxRowShift = 7;
 
 struct Smem {
-  static constexpr int kRing = qsfm::kRing, kBarRowsFull = qsfm::kBarRowsFull, kBarRowsEmpty = qsfm::kBarRowsEmpty;
   uint32_t base;
   uint8_t* ptr;
-  __device__ int* ring_rows() const { return reinterpret_cast<int*>(ptr + kSRows); }
-  __device__ int* ring_kind() const { return reinterpret_cast<int*>(ptr + kSRowKind); }
   __device__ float* f(uint32_t off) const { return reinterpret_cast<float*>(ptr + off); }
   __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(ptr + kSBar) + i; }
   __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + kSBar + 224); }
@@ -136,6 +135,70 @@ struct Smem {
     return reinterpret_cast<volatile int*>(ptr + kSBar + 232);
   }
 };
+
+// ------------------------------------------------------------- resolver
+// Tile n's rows go to ring slot n % kRing: 128 physical rows (block * 128 +
+// offset, -1 = masked) and the pool they come from. After the CTA's last tile
+// the resolver writes an end mark (-1) in the next slot. Up to kResolveTiles
+// tiles of one unit per pass: all their index loads are in flight together,
+// then all their block-table loads, so a pass costs two memory round trips
+// whatever its tile count.
+__device__ void resolver_role(const qsfm_params& p, const Smem& sm, Range rg, int T, int* fault) {
+  constexpr int kN = kResolveTiles;
+  const int lane = threadIdx.x & 31;
+  int* rows = reinterpret_cast<int*>(sm.ptr + kSRows);
+  int* kind = reinterpret_cast<int*>(sm.ptr + kSRowKind);
+  const uint8_t* q8 = static_cast<const uint8_t*>(p.q);
+  PieceIter pieces(&p, rg, T);
+  uint32_t n = 0;  // next ring position
+  int unit, lo, hi;
+  TokenGeom g;
+  while (pieces.next(unit, g, lo, hi)) {
+    if (lo >= hi) continue;
+    // the unit's Q goes to L2 a few tiles before its first product; the next
+    // token's index list while this one is resolved
+    if (lane == 0) bulk_prefetch_l2(q8 + size_t(unit) * kHeads * kDim * 2, kHeads * kDim * 2);
+    if (p.cmp_sparse_indices != nullptr && g.tok + 1 < (T >> unit_shift(p))) {
+      const uint8_t* ix = reinterpret_cast<const uint8_t*>(p.cmp_sparse_indices + (size_t)(g.tok + 1) * p.k2);
+      for (int off = 128 * lane; off < 4 * p.k2; off += 32 * 128) prefetch_l2(ix + off);
+    }
+    // passes of up to kN tiles of this unit
+    for (int k0 = lo; k0 < hi; k0 += kN) {
+      int k[kN];
+      bool live[kN];
+#pragma unroll
+      for (int t = 0; t < kN; ++t) {
+        k[t] = k0 + t;
+        live[t] = k0 + t < hi;
+      }
+#pragma unroll
+      for (int t = 0; t < kN; ++t) {
+        const uint32_t m = n + t;
+        if (live[t] && !warp_wait_or_abort(sm, kBarRowsEmpty + m % kRing, ((m / kRing) & 1) ^ 1, fault)) return;
+      }
+      int lg[kN][4], pr[kN][4];
+      bool cmp[kN];
+      resolve_tile_rows<kN>(p, g, k, live, lane, fault, lg, pr, cmp);
+#pragma unroll
+      for (int t = 0; t < kN; ++t) {
+        if (!live[t]) continue;
+        const uint32_t slot = (n + t) % kRing;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) rows[slot * kTileRows + lane + 32 * u] = pr[t][u];
+        if (lane == 0) kind[slot] = cmp[t] ? 1 : 0;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.bar(kBarRowsFull + slot));
+      }
+      n += min(kN, hi - k0);
+    }
+  }
+  // end mark after the CTA's last tile
+  const uint32_t slot = n % kRing;
+  if (!warp_wait_or_abort(sm, kBarRowsEmpty + slot, ((n / kRing) & 1) ^ 1, fault)) return;
+  if (lane == 0) kind[slot] = -1;
+  __syncwarp();
+  if (lane == 0) mbar_arrive(sm.bar(kBarRowsFull + slot));
+}
 
 // ------------------------------------------------------------- MMA issue
 // QK^T of chunk c (d-blocks 2c, 2c + 1), k-step s of d-block db: A (K~,

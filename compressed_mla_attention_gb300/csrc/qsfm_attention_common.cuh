@@ -1,10 +1,8 @@
 // Parts the attention kernels share: the walk over a CTA's planned pieces,
-// bounded waits, lane reductions, the resolver warp, the tensor map of q.
+// bounded waits, lane reductions, the tensor map of q.
 //
-// A kernel's shared-memory view (the template argument Smem) offers bar(i),
-// abort_flag(), ring_rows(), ring_kind() and the constants kRing (tiles of
-// resolved rows in flight), kBarRowsFull and kBarRowsEmpty (the first of the
-// ring's mbarriers).
+// A kernel's shared-memory view (the template argument Smem) offers bar(i) and
+// abort_flag().
 #pragma once
 
 #include <cuda.h>
@@ -19,8 +17,6 @@
 namespace qsfm {
 namespace {
 
-constexpr int kResolveTiles = 1;  // tiles per resolver pass (more keeps more loads in flight, at a
-                                  // larger instruction footprint; the ring already runs 8 tiles ahead)
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -114,72 +110,6 @@ __device__ __forceinline__ bool warp_wait_or_abort(const Smem& sm, int bar, uint
   if ((threadIdx.x & 31) == 0) ok = wait_or_abort(sm, bar, parity, fault);
   __syncwarp();  // the other lanes wait here (and are ordered after lane 0's acquire)
   return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-}
-
-// ------------------------------------------------------------- resolver
-// Tile n's rows go to ring slot n % kRing: 128 physical rows (block * 128 +
-// offset, -1 = masked) and the pool they come from. After the CTA's last tile
-// the resolver writes an end mark (-1) in the next slot. Up to kResolveTiles
-// tiles of one unit per pass: all their index loads are in flight together,
-// then all their block-table loads, so a pass costs two memory round trips
-// whatever its tile count.
-template <typename Smem>
-__device__ void resolver_role(const qsfm_params& p, const Smem& sm, Range rg, int T, int* fault) {
-  constexpr int kN = kResolveTiles, kRing = Smem::kRing;
-  constexpr int kBarRowsFull = Smem::kBarRowsFull, kBarRowsEmpty = Smem::kBarRowsEmpty;
-  const int lane = threadIdx.x & 31;
-  int* rows = sm.ring_rows();
-  int* kind = sm.ring_kind();
-  const uint8_t* q8 = static_cast<const uint8_t*>(p.q);
-  PieceIter pieces(&p, rg, T);
-  uint32_t n = 0;  // next ring position
-  int unit, lo, hi;
-  TokenGeom g;
-  while (pieces.next(unit, g, lo, hi)) {
-    if (lo >= hi) continue;
-    // the unit's Q goes to L2 a few tiles before its first product; the next
-    // token's index list while this one is resolved
-    if (lane == 0) bulk_prefetch_l2(q8 + size_t(unit) * kHeads * kDim * 2, kHeads * kDim * 2);
-    if (p.cmp_sparse_indices != nullptr && g.tok + 1 < (T >> unit_shift(p))) {
-      const uint8_t* ix = reinterpret_cast<const uint8_t*>(p.cmp_sparse_indices + (size_t)(g.tok + 1) * p.k2);
-      for (int off = 128 * lane; off < 4 * p.k2; off += 32 * 128) prefetch_l2(ix + off);
-    }
-    // passes of up to kN tiles of this unit
-    for (int k0 = lo; k0 < hi; k0 += kN) {
-      int k[kN];
-      bool live[kN];
-#pragma unroll
-      for (int t = 0; t < kN; ++t) {
-        k[t] = k0 + t;
-        live[t] = k0 + t < hi;
-      }
-#pragma unroll
-      for (int t = 0; t < kN; ++t) {
-        const uint32_t m = n + t;
-        if (live[t] && !warp_wait_or_abort(sm, kBarRowsEmpty + m % kRing, ((m / kRing) & 1) ^ 1, fault)) return;
-      }
-      int lg[kN][4], pr[kN][4];
-      bool cmp[kN];
-      resolve_tile_rows<kN>(p, g, k, live, lane, fault, lg, pr, cmp);
-#pragma unroll
-      for (int t = 0; t < kN; ++t) {
-        if (!live[t]) continue;
-        const uint32_t slot = (n + t) % kRing;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) rows[slot * kTileRows + lane + 32 * u] = pr[t][u];
-        if (lane == 0) kind[slot] = cmp[t] ? 1 : 0;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm.bar(kBarRowsFull + slot));
-      }
-      n += min(kN, hi - k0);
-    }
-  }
-  // end mark after the CTA's last tile
-  const uint32_t slot = n % kRing;
-  if (!warp_wait_or_abort(sm, kBarRowsEmpty + slot, ((n / kRing) & 1) ^ 1, fault)) return;
-  if (lane == 0) kind[slot] = -1;
-  __syncwarp();
-  if (lane == 0) mbar_arrive(sm.bar(kBarRowsFull + slot));
 }
 
 __device__ __forceinline__ float e8m0_value(uint32_t e) {
