@@ -230,8 +230,10 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
 
 cudaError_t launch_block_tables(const qsfm_block_table_params& p, int* fault, cudaStream_t s) {
   const size_t smem = 5 * size_t(p.batch) * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       5 * 8192 * int(sizeof(int)));
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024 - sizeof(Sums) * kTabThreads / 32)  // beyond what every kernel may use
+    e = cudaFuncSetAttribute(block_table_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             5 * 8192 * int(sizeof(int)));
   if (e != cudaSuccess) return e;
   int ctas = 1;
   if (p.max_rows > kTabAlone) {
