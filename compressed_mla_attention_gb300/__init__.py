@@ -846,7 +846,8 @@ def update_block_tables(block_table, prev_lens, lens, free_list, free_count, *, 
     block_table int32 [B, W], free_list int32 [P] (block ids, a stack of which
     the first free_count int32 [1] entries are free) are updated in place:
     requests that shrink from prev_lens[b] to lens[b] tokens (0: ended) give
-    blocks back, then requests that grow take them, in order. With cmp_ratio
+    blocks back (none for a column of -1), then requests that grow take them,
+    in order. With cmp_ratio
     r, floor(len / r) rows count (compressed rows). free_count_out: the new
     count goes there instead. slot_map int32 [max_rows] (allocated when not
     given, with positions) gets the pool row of every new row and positions

@@ -4,12 +4,15 @@
 // requests give back and take, and the pool row of every new cache row. With
 // the cache rows of request b before and after the step, p_b and r_b, its
 // blocks before and after, h_b = ceil(p_b / 128) and n_b = ceil(r_b / 128),
-//   G_b = sum_{i<b} max(0, h_i - n_i)   blocks given back before request b,
+//   G_b = sum_{i<b} g_i                 blocks given back before request b, g_i of
+//                                       the columns n_i .. h_i - 1 that hold one,
 //   T_b = sum_{i<b} max(0, n_i - h_i)   blocks taken before it,
 //   N_b = sum_{i<b} max(0, r_i - p_i)   new rows before it,
 // the i-th block taken is the i-th from the top of the stack "free list, then
 // the blocks given back in order", so each output element follows from the
-// three prefix sums alone and no thread waits for another's write.
+// three prefix sums alone and no thread waits for another's write. A column may
+// hold no block: -1 where the pool was short or the block lies behind a window and
+// is somebody else's by now. So g_i is counted, a warp per request that shrinks.
 //
 // Every CTA computes the prefix sums over the batch for itself (up to 160 KB of
 // shared memory; the lengths come from L2) and takes a share of the output
@@ -21,8 +24,10 @@
 // in place is a launch of its own (one CTA, the sums again).
 // Bound by latency up to some ten thousand rows (the launch, one round trip for
 // the lengths, the scan, the search and one or two round trips for a block id),
-// then by the stores. 2 requests with one new row each 3.1 us, 128 requests 5.2
-// us, 500 requests with half a million new rows 7.7 us (4 MB of slots and positions).
+// then by the stores. Times inside a graph: 2 requests with one new row each 3.2 us,
+// 128 requests 6.1 us, 500 requests with half a million new rows 11.3 us (4 MB of
+// slots and positions). Counting what is given back takes 1.1 and 3.8 us of the last
+// two (25 of the 500 requests end, 13 thousand columns, read by every CTA).
 #include <cuda_runtime.h>
 
 #include "qsfm_device.cuh"
@@ -92,7 +97,7 @@ __device__ __forceinline__ int find_request(const int* at, int n, int i) {
 
 // update: 0 leaves free_count alone, 1 updates it (and free_count_out), 2 does
 // nothing else.
-__global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_block_table_params p, const int update,
+__global__ void __launch_bounds__(kTabThreads, 2) block_table_kernel(const qsfm_block_table_params p, const int update,
                                                                   int* fault) {
   __shared__ Sums s_warps[kTabThreads / 32];
   extern __shared__ int s_dyn[];
@@ -107,8 +112,7 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
   const int per = (p.batch + kTabThreads - 1) / kTabThreads;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   const int stack = *p.free_count;  // in flight with the lengths
-  Sums mine{0, 0, 0};
-  bool wide = false;
+  bool wide = false, shrinks = false;
   for (int b = b0; b < b1; ++b) {
     const int n0 = max(0, __ldg(p.prev_lens + b)), n1 = max(0, __ldg(p.lens + b));
     int prev = n0 / p.cmp_ratio, rows = n1 / p.cmp_ratio;
@@ -119,14 +123,52 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
     const int held = (min(prev, cap_rows) + kBlock - 1) / kBlock, need = (min(rows, cap_rows) + kBlock - 1) / kBlock;
     s_prev[b] = prev;
     s_need[b] = need;
+    s_rows[b] = max(0, rows - prev);
+    s_taken[b] = max(0, need - held);
+    s_given[b] = 0;
+    shrinks |= held > need;
+  }
+  if (wide && cta == 0 && update < 2) atomicOr(fault, QSFM_FAULT_ORI_TABLE_COL);
+  auto held_of = [&](int b) { return (min(s_prev[b], cap_rows) + kBlock - 1) / kBlock; };
+  auto in_pool = [&](int block) { return block >= 0 && block < p.num_blocks; };
+  if (__syncthreads_or(shrinks)) {
+    constexpr int kWarps = kTabThreads / 32;
+    const int lane = tid & 31;
+    // neighbouring requests go to different warps
+    for (int base = tid >> 5; base < p.batch; base += 32 * kWarps) {
+      const int mine = base + lane * kWarps;
+      uint32_t todo = __ballot_sync(0xffffffffu, mine < p.batch && held_of(mine) > s_need[mine]);
+      for (; todo != 0; todo &= todo - 1) {
+        const int b = base + (__ffs(todo) - 1) * kWarps, end = held_of(b);
+        const int32_t* columns = p.block_table + size_t(b) * p.max_blocks;
+        int blocks = 0;
+        bool foreign = false;
+        constexpr int kAtOnce = 16;  // columns that a lane has in flight
+        for (int c = s_need[b] + lane; c < end; c += 32 * kAtOnce) {
+          int block[kAtOnce];
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) block[k] = c + 32 * k < end ? columns[c + 32 * k] : -1;
+#pragma unroll
+          for (int k = 0; k < kAtOnce; ++k) {
+            blocks += in_pool(block[k]) ? 1 : 0;
+            foreign |= block[k] < -1 || block[k] >= p.num_blocks;
+          }
+        }
+        blocks = __reduce_add_sync(0xffffffffu, blocks);
+        if (lane == 0) s_given[b] = blocks;
+        if (foreign && cta == 0 && update < 2) atomicOr(fault, QSFM_FAULT_ORI_BLOCK_ID);
+      }
+    }
+    __syncthreads();
+  }
+  Sums mine{0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    const Sums own{s_rows[b], s_taken[b], s_given[b]};
     s_rows[b] = mine.rows;
     s_taken[b] = mine.taken;
     s_given[b] = mine.given;
-    mine.rows = add_rows(mine.rows, max(0, rows - prev));
-    mine.taken += max(0, need - held);
-    mine.given += max(0, held - need);
+    mine = add(mine, own);
   }
-  if (wide && cta == 0 && update < 2) atomicOr(fault, QSFM_FAULT_ORI_TABLE_COL);
   Sums total;
   const Sums before = scan_before(mine, s_warps, total);
   for (int b = b0; b < b1; ++b) {
@@ -151,22 +193,36 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
   }
   if (update == 2) return;
 
+  // a block id of the list or of a held column: -1 where it is none
+  auto checked = [&](int block) {
+    if (in_pool(block)) return block;
+    atomicOr(fault, QSFM_FAULT_ORI_BLOCK_ID);
+    return -1;
+  };
   // the i-th block given back, and the i-th taken (-1: none left)
   auto given_block = [&](int i) {
     const int b = find_request(s_given, p.batch, i);
-    return p.block_table[size_t(b) * p.max_blocks + s_need[b] + (i - s_given[b])];
+    const int blocks = (b + 1 < p.batch ? s_given[b + 1] : total.given) - s_given[b];
+    int c = held_of(b);
+    const int first = s_need[b], after = s_given[b] + blocks - 1 - i;  // columns with a block behind it
+    const int32_t* columns = p.block_table + size_t(b) * p.max_blocks;
+    if (blocks == c - first) return columns[c - 1 - after];
+    // some columns hold none: from the last one down (the front ones are those behind a window)
+    for (int left = after; c > first;) {
+      constexpr int kAtOnce = 8;
+      int block[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) block[k] = c - 1 - k >= first ? columns[c - 1 - k] : -1;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (in_pool(block[k]) && left-- == 0) return block[k];
+      c -= kAtOnce;
+    }
+    return -1;
   };
   auto taken_block = [&](int i) {
     const int from_top = total.given - 1 - i;  // of the blocks given back; then the free list
-    return from_top >= 0 ? given_block(from_top) : count + from_top >= 0 ? p.free_list[count + from_top] : -1;
-  };
-  auto held_of = [&](int b) { return (min(s_prev[b], cap_rows) + kBlock - 1) / kBlock; };
-  auto checked = [&](int block) {
-    if (block >= p.num_blocks || block < -1) {
-      atomicOr(fault, QSFM_FAULT_ORI_BLOCK_ID);
-      return -1;
-    }
-    return block;
+    return from_top >= 0 ? given_block(from_top) : count + from_top >= 0 ? checked(p.free_list[count + from_top]) : -1;
   };
 
   // Rows, taken and returned blocks start at different warps, so that their
@@ -198,8 +254,8 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
       if (col >= p.max_blocks) continue;
       if (col != col_of) {
         const int held = held_of(b);
-        block = checked(col < held ? p.block_table[size_t(b) * p.max_blocks + col]
-                                   : taken_block(s_taken[b] + col - held));
+        block = col < held ? checked(p.block_table[size_t(b) * p.max_blocks + col])
+                           : taken_block(s_taken[b] + col - held);
         col_of = col;
       }
       if (block >= 0) slot[k] = block * kBlock + row % kBlock;
@@ -219,7 +275,7 @@ __global__ void __launch_bounds__(kTabThreads) block_table_kernel(const qsfm_blo
   }
   for (int i = me_taken; i < total.taken; i += step) {
     const int b = find_request(s_taken, p.batch, i);
-    p.block_table[size_t(b) * p.max_blocks + held_of(b) + (i - s_taken[b])] = checked(taken_block(i));
+    p.block_table[size_t(b) * p.max_blocks + held_of(b) + (i - s_taken[b])] = taken_block(i);
   }
   // blocks given back and not taken again go onto the free list
   const int pushed = min(max(0, total.given - total.taken), p.free_capacity - count);

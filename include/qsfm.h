@@ -552,9 +552,10 @@ qsfm_status qsfm_norm_rope_store(const qsfm_norm_rope_params* p, void* stream);
  * need_b = ceil(rows(lens[b]) / 128), for the B requests in order:
  *   a request that shrinks gives the blocks of its table columns need_b ..
  *   held_b - 1 back to the end of the free list (a request that has ended has
- *   lens[b] = 0), then a request that grows takes the blocks of columns
- *   held_b .. need_b - 1 from the end of the list, in the order (request,
- *   column). So a block given back in a call may be taken in the same call.
+ *   lens[b] = 0; a column of -1 holds no block and gives none back), then a
+ *   request that grows takes the blocks of columns held_b .. need_b - 1 from the
+ *   end of the list, in the order (request, column). So a block given back in a
+ *   call may be taken in the same call.
  * The table columns behind need_b are left as they were.
  * The new rows rows(prev_lens[b]) .. rows(lens[b]) - 1 of all requests, end to
  * end, are described by
@@ -569,8 +570,10 @@ qsfm_status qsfm_norm_rope_store(const qsfm_norm_rope_params* p, void* stream);
  * free_count int32 [1] are the state, updated in place; free_count_out, when
  * not NULL, takes the new count instead of free_count (the call can then be
  * repeated on the same inputs). Bad data is reported in the fault word and
- * skipped: no free block left (QSFM_FAULT_BLOCK_POOL: -1 in the table), a
- * block id outside [0, num_blocks) (QSFM_FAULT_ORI_BLOCK_ID: slots -1), more
+ * skipped: no free block left (QSFM_FAULT_BLOCK_POOL: -1 in the table); a
+ * block id outside [0, num_blocks) on the free list or in a held column that a
+ * new row falls into, and one outside [-1, num_blocks) in a column given back
+ * (QSFM_FAULT_ORI_BLOCK_ID: -1 in the table, slots -1, not given back); more
  * than max_blocks blocks in a request (QSFM_FAULT_ORI_TABLE_COL), more new
  * rows than max_rows (QSFM_FAULT_SLOT). Negative lengths count as 0. The
  * buffers do not overlap.

@@ -73,26 +73,31 @@ def bf16_bits(x):
     return ((b + 0x7FFF + ((b >> 16) & 1)) >> 16).astype(np.uint16)
 
 
-def block_tables(table, prev_lens, lens, free_list, free_count, ratio, max_rows):
+def block_tables(table, prev_lens, lens, free_list, free_count, ratio, max_rows, num_blocks=None):
     """The state and the outputs after one step, request by request:
-    (table, free_list, free_count, slot_map, positions, cu_rows, residual)."""
+    (table, free_list, free_count, slot_map, positions, cu_rows, residual).
+    What is not in [0, num_blocks) (default: the list's length) is no block: a
+    column that holds such a thing gives nothing back, and what is taken from
+    the list is then -1."""
     table, free_list = table.copy(), free_list.copy()
+    blocks = len(free_list) if num_blocks is None else num_blocks
     before = [int(n) // ratio for n in prev_lens]
     after = [int(n) // ratio for n in lens]
     held = [-(-n // BLOCK) for n in before]
     need = [-(-n // BLOCK) for n in after]
     stack = [int(b) for b in free_list[:free_count]]
     for b in range(len(lens)):
-        stack += [int(table[b, c]) for c in range(need[b], held[b])]
+        stack += [int(v) for v in table[b, need[b]:held[b]] if 0 <= v < blocks]
     for b in range(len(lens)):
         for c in range(held[b], need[b]):
-            table[b, c] = stack.pop() if stack else -1
+            block = stack.pop() if stack else -1
+            table[b, c] = block if 0 <= block < blocks else -1
     free_list[free_count:len(stack)] = stack[free_count:]
     slots, positions, cu = [], [], [0]
     for b in range(len(lens)):
         for row in range(before[b], after[b]):
             block = int(table[b, row // BLOCK])
-            slots.append(block * BLOCK + row % BLOCK if block >= 0 else -1)
+            slots.append(block * BLOCK + row % BLOCK if 0 <= block < blocks else -1)
             positions.append(row * ratio)
         cu.append(len(slots))
     pad = max_rows - len(slots)

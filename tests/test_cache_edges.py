@@ -1,0 +1,46 @@
+"""The operators around the cache where a table, a batch or a script is not the
+ordinary one (CPU): the oracle of block tables over columns and lists that hold
+no block, calls without tokens, the entry script."""
+
+import ast
+import ctypes
+import os
+
+import numpy as np
+import pytest
+
+import compressed_mla_attention_gb300 as Q
+from oracle import cache_oracle as C
+from tests.test_abi import lib  # noqa: F401
+from tests.test_cache_operators import CACHE_AT, TAB_AT, W_AT, norm_rope_valid
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+# ------------------------------------------------------------------ block tables
+def test_oracle_gives_back_blocks_alone():
+    """A short pool leaves -1 in the table; the request's end gives back the
+    blocks that it has, and the next request takes one of them."""
+    table, free = np.full((3, 2), -1, dtype=np.int32), np.array([5, -7, -7, -7, -7, -7], dtype=np.int32)
+    table, free, n, slots, *_ = C.block_tables(table, [0, 0, 0], [128, 128, 0], free, 1, 1, 256)
+    assert table[:2, 0].tolist() == [5, -1] and n == 0 and set(slots[128:].tolist()) == {-1}
+    table, free, n, slots, *_ = C.block_tables(table, [128, 128, 0], [128, 0, 128], free, n, 1, 128)
+    assert table[2, 0] == -1 and n == 0 and set(slots.tolist()) == {-1}  # request 1 had none to give
+    table, free, n, slots, *_ = C.block_tables(table, [128, 0, 128], [0, 0, 0], free, n, 1, 0)
+    assert n == 1 and free[0] == 5
+    table, free, n, slots, *_ = C.block_tables(table, [0, 0, 0], [0, 3, 0], free, n, 1, 3)
+    assert n == 0 and slots.tolist() == [640, 641, 642]
+
+
+def test_oracle_gives_back_what_a_window_left():
+    table, free = np.array([[-1, -1, -1, 7]], dtype=np.int32), np.array([0, 1, -7, -7, -7, -7, -7, -7], dtype=np.int32)
+    _, f, n, *_ = C.block_tables(table, [500], [0], free, 2, 1, 0)
+    assert n == 3 and f.tolist() == [0, 1, 7, -7, -7, -7, -7, -7]
+
+
+def test_oracle_passes_no_foreign_id_on():
+    """Ids outside the pool, in a column given back or on the list, are not blocks."""
+    table, free = np.array([[3, 99], [-1, -1]], dtype=np.int32), np.array([1, 44, 0, 0], dtype=np.int32)
+    t, f, n, slots, *_ = C.block_tables(table, [256, 0], [0, 256], free, 2, 1, 256)
+    assert t[1].tolist() == [3, -1] and n == 1 and f[0] == 1
+    assert slots[:128].tolist() == [3 * 128 + i for i in range(128)] and set(slots[128:].tolist()) == {-1}

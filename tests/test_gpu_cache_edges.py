@@ -1,0 +1,130 @@
+"""GPU tests of the operators around the cache where a call is not the ordinary
+one: tables with columns that hold no block, rows and queries that are not
+finite, calls without tokens."""
+
+import numpy as np
+import pytest
+import torch
+
+import compressed_mla_attention_gb300 as Q
+from oracle import cache_oracle as C
+from tests.test_gpu_cache_operators import i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from compressed_mla_attention_gb300 import build
+
+    build.build()
+    Q.lib()
+
+
+# ------------------------------------------------------------------ block tables
+def table_step(dev, state, prev, lens, rows, ratio=1, num_blocks=None, inplace=True):
+    """One call and the oracle's from the same state; returns the fault word and the slots."""
+    table, free, count = state
+    nb = len(free) if num_blocks is None else num_blocks
+    ref = C.block_tables(table, prev, lens, free, count, ratio, rows, num_blocks=nb)
+    t, f, n = i32(table, dev), i32(free, dev), i32([count], dev)
+    out = None if inplace else i32([-99], dev)
+    cu, res = i32(np.zeros(len(lens) + 1), dev), i32(np.zeros(len(lens)), dev)
+    slots, pos = Q.update_block_tables(t, i32(prev, dev), i32(lens, dev), f, n, max_rows=rows, cu_rows=cu, residual=res,
+                                       free_count_out=out, cmp_ratio=ratio, num_blocks=nb)
+    torch.cuda.synchronize()
+    fault = Q.device_status()
+    assert np.array_equal(t.cpu().numpy(), ref[0])
+    assert int((n if inplace else out)[0]) == ref[2]
+    assert np.array_equal(f.cpu().numpy(), ref[1])
+    for got, want in ((slots, ref[3]), (pos, ref[4]), (cu, ref[5]), (res, ref[6])):
+        assert np.array_equal(got.cpu().numpy(), want)
+    state[:] = ref[:3]
+    return fault, ref[3]
+
+
+def test_a_short_pool_recovers_every_block(cuda_device):
+    """Two blocks for four wanted; both requests end; a new one takes a block."""
+    state = [np.full((2, 4), -1, dtype=np.int32), np.array([5, 6, -7, -7], dtype=np.int32), 2]
+    fault, _ = table_step(cuda_device, state, [0, 0], [300, 128], 428, num_blocks=16)
+    assert fault == Q.FAULT_BLOCK_POOL and state[0].tolist() == [[6, 5, -1, -1], [-1] * 4]
+    fault, _ = table_step(cuda_device, state, [300, 128], [0, 0], 1, num_blocks=16)
+    assert fault == 0 and state[2] == 2 and state[1][:2].tolist() == [6, 5]
+    fault, slots = table_step(cuda_device, state, [0, 0], [0, 100], 100, num_blocks=16)
+    assert fault == 0 and slots.tolist() == [5 * 128 + i for i in range(100)]
+    # a request that goes on in a column without a block is reported, and its rows are not stored
+    state = [np.array([[6, -1]], dtype=np.int32), np.array([1, 2], dtype=np.int32), 2]
+    fault, slots = table_step(cuda_device, state, [200], [201], 1, num_blocks=16)
+    assert fault == Q.FAULT_ORI_BLOCK_ID and slots.tolist() == [-1]
+
+
+def test_columns_behind_a_window_hold_no_block(cuda_device):
+    state = [np.array([[-1, -1, -1, 7], [-1, 3, -1, -1]], dtype=np.int32), np.array([0, 1] + [-7] * 6, dtype=np.int32), 2]
+    fault, slots = table_step(cuda_device, state, [500, 256], [0, 257], 1)
+    assert fault == 0 and state[2] == 2 and slots.tolist() == [7 * 128]
+    # one table row of 1000 columns, the last two blocks of it live; and a request that takes both
+    table = np.full((2, 1000), -1, dtype=np.int32)
+    table[0, 998:] = 4, 2
+    state = [table, np.array([0, -7, -7, -7, -7], dtype=np.int32), 1]
+    fault, _ = table_step(cuda_device, state, [128000, 0], [0, 300], 300)
+    assert fault == 0 and state[0][1, :3].tolist() == [2, 4, 0] and state[2] == 0
+
+
+def test_foreign_ids_are_reported_and_not_passed_on(cuda_device):
+    for bad in (99, -2, 2 ** 31 - 1):
+        state = [np.array([[3, bad], [-1, -1]], dtype=np.int32), np.array([1, 0, 0, 0], dtype=np.int32), 1]
+        fault, _ = table_step(cuda_device, state, [256, 0], [0, 0], 1, num_blocks=16)
+        assert fault == Q.FAULT_ORI_BLOCK_ID and state[2] == 2 and state[1][:2].tolist() == [1, 3]
+    for bad in (99, -1):  # on the free list
+        state = [np.full((1, 2), -1, dtype=np.int32), np.array([1, bad], dtype=np.int32), 2]
+        fault, _ = table_step(cuda_device, state, [0], [256], 256, num_blocks=16)
+        assert fault == Q.FAULT_ORI_BLOCK_ID and state[0].tolist() == [[-1, 1]] and state[2] == 0
+
+
+@pytest.mark.parametrize("inplace", [True, False])
+@pytest.mark.parametrize("name,batch,width,ratio,new_hi", [
+    ("few", 3, 9, 1, 400), ("one CTA", 40, 30, 4, 700), ("wide rows", 12, 700, 1, 3000), ("many CTAs", 300, 40, 1, 2500),
+    ("many requests", 3000, 5, 1, 150)])
+def test_tables_with_holes_match_the_oracle(cuda_device, name, batch, width, ratio, new_hi, inplace):
+    """Held columns of which some hold no block, or an id outside the pool."""
+    r = np.random.RandomState(len(name))
+    cap = width * 128 * ratio
+    prev = r.randint(0, cap + 1, batch)
+    lens = np.minimum(prev + r.randint(0, new_hi + 1, batch), cap)
+    shrink = r.rand(batch) < 0.4
+    lens[shrink] = (prev[shrink] * r.rand(shrink.sum())).astype(int) * r.randint(0, 2, shrink.sum())
+    held = -(-(prev // ratio) // 128)
+    pool = int(held.sum()) + batch
+    perm, at = r.permutation(pool), 0
+    table = r.randint(-5, pool, (batch, width)).astype(np.int32)
+    for b in range(batch):
+        table[b, :held[b]] = perm[at:at + held[b]]
+        at += held[b]
+        kind = r.randint(4)
+        if kind == 1:  # behind a window
+            table[b, :max(0, held[b] - 2)] = -1
+        elif kind == 2:  # a short pool's, here and there
+            table[b, :held[b]][r.rand(held[b]) < 0.5] = -1
+        elif kind == 3 and held[b] and batch < 300:
+            table[b, r.randint(held[b])] = r.choice([pool, -3])
+    free = np.concatenate([perm[at:], np.full(at, -7)]).astype(np.int32)
+    rows = int(np.maximum(lens // ratio - prev // ratio, 0).sum()) + 5
+    table_step(cuda_device, [table, free, pool - at], prev, lens, rows, ratio=ratio, inplace=inplace)
+
+
+def test_a_history_of_short_pools_loses_no_block(cuda_device):
+    """Forty steps of a pool too small for its requests: after each, every
+    block is in one table or on the list, once."""
+    r = np.random.RandomState(7)
+    batch, width, pool = 6, 8, 17
+    state = [np.full((batch, width), -1, dtype=np.int32), r.permutation(pool).astype(np.int32), pool]
+    prev, short = np.zeros(batch, dtype=int), 0
+    for _ in range(40):
+        lens = np.minimum(prev + r.randint(0, 300, batch), width * 128)
+        lens[r.rand(batch) < 0.25] = 0
+        fault, _ = table_step(cuda_device, state, prev, lens, int(np.maximum(lens - prev, 0).sum()) + 1)
+        short += fault & Q.FAULT_BLOCK_POOL != 0
+        used = [v for b, n in enumerate(lens) for v in state[0][b, :-(-n // 128)].tolist() if v >= 0]
+        assert sorted(used + state[1][:state[2]].tolist()) == list(range(pool))
+        prev = lens
+    assert short > 5
