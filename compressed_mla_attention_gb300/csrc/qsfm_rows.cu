@@ -15,9 +15,9 @@
 // its rows through a ring in shared memory. The key rows are few; they are the
 // first blocks of the grid, one warp each, bound by latency and by the
 // instructions of their last bits (below).
-// Measured: 4099 tokens of 128 + 1 bf16 rows 177 us, 6.1 TB/s of rows read and
-// written (90% of a copy's rate); 256 tokens 6.4 us; one token 3.6 us; 8191 fp32
-// key rows alone 12.0 us.
+// Measured inside a graph: 4099 tokens of 128 + 1 bf16 rows 177 us, 6.1 TB/s of rows
+// read and written (90% of a copy's rate); 256 tokens 6.5 us; one token 3.9 us; 8191
+// fp32 key rows alone, fp8 rows stored, 12.9 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -298,7 +298,7 @@ __device__ __forceinline__ void sticky16(float (&y)[2][8], const float (&z)[2][8
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[h][i] = sticky(y[h][i], z[h][i]);
 }
-// (y + z) / (d + dz), d > 0, in the same sense, for a rounding to at most 18 bits: the
+// (y + z) / (d + dz), d > 0, all finite, in the same sense, for a rounding to at most 18 bits: the
 // quotient by the reciprocal (two ulps off at most) goes to the next multiple of
 // 16 ulps, and the sign of what is left over says on which side of it y + z is.
 __device__ __forceinline__ float sticky_quotient(float y, float z, float d, float dz, float reciprocal) {
@@ -365,6 +365,9 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
   if (p.kv_layout == QSFM_KV_FP8_FP32_SCALES) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      bool ok = finite8(y[h]);
+#pragma unroll
+      for (int o = 1; o <= 4; o <<= 1) ok &= __shfl_xor_sync(kAll, int(ok), o) != 0;
       float m = 0.f, rest = 0.f;  // the largest |y + z|
       auto larger = [&](float a, float az) {
         if (a > m || (a == m && az > rest)) m = a, rest = az;
@@ -388,7 +391,11 @@ __device__ __forceinline__ void store_row(const qsfm_norm_rope_params& p, int sl
       float q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) q[i] = sticky_quotient(y[h][i], z[h][i], scale, scale_rest, reciprocal);
-      const uint2 code = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+      uint2 code = make_uint2(e4m3x4(q[0], q[1], q[2], q[3]), e4m3x4(q[4], q[5], q[6], q[7]));
+      if (!ok) {  // NaN codes as well as a NaN scale: a reader may limit the scale
+        code = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+        scale = __uint_as_float(0x7FC00000u);
+      }
       if (put) {
         *reinterpret_cast<uint2*>(row + 256 * h + 8 * lane) = code;
         if ((lane & 7) == 0) p.kv_scale[size_t(slot) * kScales + 4 * h + (lane >> 3)] = scale;

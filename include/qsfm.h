@@ -479,8 +479,9 @@ qsfm_status qsfm_lightning_indexer(const qsfm_indexer_params* p, void* workspace
  *              e4m3(y / scale), scale as it is before its rounding to fp32
  *              (the root that both share is fp32's: stored scales are within
  *              20 2^-24 of the formula's)
- *   A scale group with an element that is not finite stores a scale of NaN
- *   (packed formats); the other groups are as without it.
+ *   A scale group with an element that is not finite stores a scale of NaN (fp8
+ *   rows: and codes of NaN); the other groups are as without it. Elements that are
+ *   stored as bf16 are stored as they are.
  * A token whose position is negative is padding: nothing is written for it. A
  * slot that is negative stores no row (q_out and kv_out are
  * written); each slot is named by at most one token (of two, the row's bytes

@@ -8,7 +8,8 @@ import torch
 
 import compressed_mla_attention_gb300 as Q
 from oracle import cache_oracle as C
-from tests.test_gpu_cache_operators import i32
+from oracle import qsfm_oracle as O
+from tests.test_gpu_cache_operators import FORMATS, cache_values, i32, new_cache
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,51 @@ def test_a_history_of_short_pools_loses_no_block(cuda_device):
         assert sorted(used + state[1][:state[2]].tolist()) == list(range(pool))
         prev = lens
     assert short > 5
+
+
+# ------------------------------------------------------------------ rows that are not finite
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_broken_row_is_stored_as_one(cuda_device, fmt, dtype, norm):
+    """NaN and infinities in key rows of every format: without the norm the
+    element's scale group holds NaN, codes and scale (a bf16 element is as it is); with it a
+    NaN breaks its whole row, and of a row with an infinity, whose norm divides by
+    infinity, its group is NaN and the others are zeros. The rows beside are as
+    without it."""
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(7, 512, generator=g)
+    bad = [(1, 70, "nan"), (1, 300, "-inf"), (2, 511, "inf"), (4, 64, "nan"), (4, 500, "nan"), (5, 130, "-inf")]
+    for row, at, v in bad:
+        x[row, at] = float(v)
+    dev, slots = cuda_device, torch.arange(7, dtype=torch.int32, device=cuda_device)
+    stored = []
+    for rows in (x, torch.where(torch.isfinite(x), x, 0.0)):
+        cache, scale = new_cache(fmt, 1, dev)
+        out = torch.empty(7, 512, dtype=torch.bfloat16, device=dev)
+        Q.norm_rope_store(None, rows.to(dtype).to(dev), kv_cache=cache, kv_scale=scale, kv_out=out, slot_map=slots, norm_kv=norm)
+        torch.cuda.synchronize()
+        assert Q.device_status() == 0
+        stored.append((cache_values(cache, scale, range(7)), out.double().cpu().numpy(),
+                       O.pool_bytes(cache.cpu()).reshape(128, -1)[:7]))
+    (held, out, raw), (clean, clean_out, _) = stored
+    size = {"packed384": 16, "packed640": 64, "fp8_fp32_scales": 64, "bf16": 1}[fmt]
+    broken = np.zeros((7, 512), dtype=bool)
+    for row, at, v in bad:
+        # the first 64 elements of a packed row are bf16 of their own
+        broken[row, at // size * size:at // size * size + size] = True
+    whole = [1, 4] if norm else []  # a NaN in the sum
+    broken[whole] = True
+    if fmt == "bf16" and not norm:
+        assert np.array_equal(held, x.to(torch.bfloat16).double().numpy(), equal_nan=True)
+        assert np.array_equal(out, held, equal_nan=True)
+        return
+    assert np.isnan(held[broken]).all() and np.isnan(out[broken]).all()
+    zero = np.zeros_like(broken)
+    if norm:
+        zero[[2, 5]] = ~broken[[2, 5]]
+    assert (held[zero] == 0).all() and (out[zero] == 0).all()
+    rest = ~broken & ~zero
+    assert np.array_equal(held[rest], clean[rest]) and np.array_equal(out[rest], clean_out[rest])
+    if fmt == "fp8_fp32_scales":  # the attention must not read a number there, whatever it makes of the scale
+        assert (raw[broken] & 0x7F == 0x7F).all()
