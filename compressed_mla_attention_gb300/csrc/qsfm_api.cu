@@ -300,6 +300,13 @@ qsfm_status check_norm_rope(const qsfm_norm_rope_params* pp) {
   if (p.in_type != QSFM_BF16 && p.in_type != QSFM_F16 && p.in_type != QSFM_F32) return QSFM_ERR_INVALID_ARG;
   if (!(p.eps >= 0.f) || !std::isfinite(p.eps)) return QSFM_ERR_INVALID_ARG;
   if ((long long)p.tokens * (p.heads + 1ll) > kMaxNormRows) return QSFM_ERR_UNSUPPORTED;
+  if (p.rope_dim < 0 || p.rope_offset < 0 || p.rope_dim + (long long)p.rope_offset > QSFM_HEAD_DIM)
+    return QSFM_ERR_INVALID_ARG;
+  if (p.rope_dim != 0) {
+    if (p.rope_dim != 32 && p.rope_dim != 64 && p.rope_dim != 128 && p.rope_dim != 256) return QSFM_ERR_UNSUPPORTED;
+    if (p.rope_offset % p.rope_dim != 0) return QSFM_ERR_UNSUPPORTED;
+  }
+  if (p.tokens == 0) return QSFM_OK;  // of empty tensors, whose pointers are null, nothing is asked
   if (p.q == nullptr && p.kv == nullptr) return QSFM_ERR_INVALID_ARG;
   if ((p.q != nullptr) != (p.heads > 0) || (p.q != nullptr) != (p.q_out != nullptr)) return QSFM_ERR_INVALID_ARG;
   if (p.q == nullptr && p.q_weight != nullptr) return QSFM_ERR_INVALID_ARG;
@@ -307,11 +314,7 @@ qsfm_status check_norm_rope(const qsfm_norm_rope_params* pp) {
     return QSFM_ERR_INVALID_ARG;
   if (p.kv != nullptr && p.kv_cache == nullptr && p.kv_out == nullptr) return QSFM_ERR_INVALID_ARG;
   // the rotation
-  if (p.rope_dim < 0 || p.rope_offset < 0 || p.rope_dim + (long long)p.rope_offset > QSFM_HEAD_DIM)
-    return QSFM_ERR_INVALID_ARG;
   if (p.rope_dim != 0) {
-    if (p.rope_dim != 32 && p.rope_dim != 64 && p.rope_dim != 128 && p.rope_dim != 256) return QSFM_ERR_UNSUPPORTED;
-    if (p.rope_offset % p.rope_dim != 0) return QSFM_ERR_UNSUPPORTED;
     if (p.cos_sin == nullptr || p.positions == nullptr || p.max_positions < 1) return QSFM_ERR_INVALID_ARG;
   } else if (p.cos_sin != nullptr) {
     return QSFM_ERR_INVALID_ARG;
@@ -337,7 +340,6 @@ qsfm_status check_norm_rope(const qsfm_norm_rope_params* pp) {
   for (const void* v : vectors)
     if (!aligned(v, 16)) return QSFM_ERR_INVALID_ARG;
   if (!aligned(p.positions, 4) || !aligned(p.slot_map, 4) || !aligned(p.kv_scale, 4)) return QSFM_ERR_INVALID_ARG;
-  if (p.tokens == 0) return QSFM_OK;
   // rows are written while others are still read: no output overlaps an input
   const long long T = p.tokens;
   const long long q_bytes = ((T - 1) * p.q_token_stride + (p.heads - 1ll) * p.q_head_stride + QSFM_HEAD_DIM) * size;

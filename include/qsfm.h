@@ -541,7 +541,8 @@ typedef struct qsfm_norm_rope_params {
 /* Defaults: dim 512, both norms, eps 1e-6, kv_layout fp8, pointers NULL. */
 void qsfm_norm_rope_params_init(qsfm_norm_rope_params* p);
 
-/* One launch on `stream`; no workspace, nothing read back. Errors:
+/* One launch on `stream` (none for T = 0, whose pointers are not looked at); no
+ * workspace, nothing read back. Errors:
  * QSFM_ERR_INVALID_ARG, QSFM_ERR_UNSUPPORTED (dim other than 512, rope_dim
  * not built, T (heads + 1) above 2^30, a cache of 2^31 rows or more). */
 qsfm_status qsfm_norm_rope_store(const qsfm_norm_rope_params* p, void* stream);

@@ -12,7 +12,7 @@ import pytest
 import compressed_mla_attention_gb300 as Q
 from oracle import cache_oracle as C
 from tests.test_abi import lib  # noqa: F401
-from tests.test_cache_operators import CACHE_AT, TAB_AT, W_AT, norm_rope_valid
+from tests.test_cache_operators import norm_rope_valid
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -44,3 +44,30 @@ def test_oracle_passes_no_foreign_id_on():
     t, f, n, slots, *_ = C.block_tables(table, [256, 0], [0, 256], free, 2, 1, 256)
     assert t[1].tolist() == [3, -1] and n == 1 and f[0] == 1
     assert slots[:128].tolist() == [3 * 128 + i for i in range(128)] and set(slots[128:].tolist()) == {-1}
+
+
+# ------------------------------------------------------------------ calls without tokens
+TOKEN_POINTERS = ("q", "q_out", "kv", "kv_out", "positions", "slot_map")
+
+
+@pytest.mark.parametrize("change", [{}, dict(heads=0, q_weight=None), dict(kv_cache=None, kv_weight=None),
+                                    dict(rope_dim=0, cos_sin=None)], ids=["all", "kv only", "q only", "norm only"])
+def test_no_tokens_with_null_pointers(lib, change):  # noqa: F811
+    """Empty tensors have null pointers: with no tokens nothing is asked of them."""
+    p = norm_rope_valid(lib)
+    for k, v in change.items():
+        setattr(p, k, v)
+    for f in TOKEN_POINTERS:
+        setattr(p, f, None)
+    p.tokens = 0
+    assert lib.qsfm_norm_rope_store(ctypes.byref(p), None) == 0
+
+
+@pytest.mark.parametrize("change,code", [(dict(dim=256), 2), (dict(in_type=3), 1), (dict(eps=-1.0), 1), (dict(heads=-1), 1),
+                                         (dict(rope_dim=48), 2), (dict(rope_offset=480), 1)])
+def test_no_tokens_with_bad_attributes(lib, change, code):  # noqa: F811
+    p = norm_rope_valid(lib)
+    p.tokens = 0
+    for k, v in change.items():
+        setattr(p, k, v)
+    assert lib.qsfm_norm_rope_store(ctypes.byref(p), None) == code

@@ -9,7 +9,7 @@ import torch
 import compressed_mla_attention_gb300 as Q
 from oracle import cache_oracle as C
 from oracle import qsfm_oracle as O
-from tests.test_gpu_cache_operators import FORMATS, cache_values, i32, new_cache
+from tests.test_gpu_cache_operators import FORMATS, cache_values, i32, new_cache, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -177,3 +177,24 @@ def test_a_broken_row_is_stored_as_one(cuda_device, fmt, dtype, norm):
     assert np.array_equal(held[rest], clean[rest]) and np.array_equal(out[rest], clean_out[rest])
     if fmt == "fp8_fp32_scales":  # the attention must not read a number there, whatever it makes of the scale
         assert (raw[broken] & 0x7F == 0x7F).all()
+
+
+# ------------------------------------------------------------------ calls without tokens
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_step_without_tokens(cuda_device, fmt):
+    """Empty tensors, whose pointers are null: nothing is launched, nothing written."""
+    dev = cuda_device
+    none = torch.empty(0, dtype=torch.int32, device=dev)
+    q, kv = (torch.empty(0, *s, dtype=torch.bfloat16, device=dev) for s in ((64, 512), (512,)))
+    w = torch.ones(512, device=dev)
+    at = dict(positions=none, cos_sin=table_of(10, 64, dev))
+    cache, scale = new_cache(fmt, 1, dev)
+    before = cache.clone()
+    store = dict(kv_cache=cache, kv_scale=scale, slot_map=none, kv_weight=w)
+    for got in (Q.norm_rope_store(q, kv, q_weight=w, kv_out=torch.empty(0, 512, dtype=torch.bfloat16, device=dev), **store, **at),
+                Q.norm_rope_store(q, q_weight=w, **at), Q.norm_rope_store(q, q_out=torch.empty_like(q))):
+        assert got.shape == (0, 64, 512)
+    assert Q.norm_rope_store(None, kv, **store, **at) is None
+    assert Q.norm_rope_store(None, kv[:, None], **store) is None
+    torch.cuda.synchronize()
+    assert Q.device_status() == 0 and torch.equal(cache, before)
