@@ -71,3 +71,12 @@ def test_no_tokens_with_bad_attributes(lib, change, code):  # noqa: F811
     for k, v in change.items():
         setattr(p, k, v)
     assert lib.qsfm_norm_rope_store(ctypes.byref(p), None) == code
+
+
+# ------------------------------------------------------------------ the entry script
+def test_the_entry_script_defines_all_before_it_runs():
+    """Run as a script, the file calls smoke() in its last statement: what that
+    calls has been defined by then."""
+    body = ast.parse(open(os.path.join(ROOT, "__graft_entry__.py")).read()).body
+    runs = [i for i, node in enumerate(body) if isinstance(node, ast.If)]
+    assert runs == [len(body) - 1]
