@@ -727,16 +727,17 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
       const int h = tid - (kSmThreads - 64);
       const float lt = any ? (red[h] + red[64 + h]) + (red[128 + h] + red[192 + h]) : 0.f;
       const float mu = m_used[h];
-      const float lse2 = lt > 0.f ? mu + log2f(lt) : -INFINITY;
+      const bool none = lt == 0.f;  // no row (a sum of NaN is not none: it shows in the output and lse)
+      const float lse2 = none ? -INFINITY : mu + log2f(lt);
       float den = lt;
       if (whole) {
         const float sink2 = sinks[unit_head0(p, t) + h];  // -inf without sinks
-        if (lt > 0.f) den += exp2f(sink2 - mu);
+        if (!none) den += exp2f(sink2 - mu);
         if (p.return_lse) p.softmax_lse[size_t(t) * 64 + h] = lse2 * kLn2;
       } else {
         ws.lse[size_t(slot) * 64 + h] = lse2 * kLn2;
       }
-      inv[64 * (live & 1) + h] = lt > 0.f ? 1.f / den : 0.f;
+      inv[64 * (live & 1) + h] = none ? 0.f : 1.f / den;
     }
     if (any) {
       pending = Out{t, whole, writable ? slot : -1, live, n - 1};

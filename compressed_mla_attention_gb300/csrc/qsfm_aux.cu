@@ -161,12 +161,15 @@ __global__ void __launch_bounds__(kCombineThreads)
       li = ov ? ws.lse[size_t(sl) * 64 + h] : -INFINITY;
     };
     float L = -INFINITY;
+    bool nan = false;  // a part whose sum is NaN makes the whole NaN (a maximum passes it over)
     for (int i0 = 0; i0 < m; i0 += 32) {
       int sl;
       float li = -INFINITY;
       if (i0 + lane < m) part(i0 + lane, sl, li);
       L = fmaxf(L, li);
+      nan |= isnan(li);
     }
+    nan = __any_sync(0xffffffffu, nan);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L = fmaxf(L, __shfl_xor_sync(0xffffffffu, L, o));
     float sum = 0.f;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const float lse_all = L > -INFINITY ? L + logf(sum) : -INFINITY;
+    const float lse_all = nan ? NAN : L > -INFINITY ? L + logf(sum) : -INFINITY;
     float denom_log = lse_all;
     if (p.sinks != nullptr && lse_all > -INFINITY) {
       const float mx = fmaxf(lse_all, sk);
@@ -187,7 +190,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (p.return_lse && lane == 0) p.softmax_lse[size_t(t) * 64 + h] = lse_all;
     float4 acc[4];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int q = 0; q < 4; ++q) acc[q] = nan ? make_float4(NAN, NAN, NAN, NAN) : make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < m && lse_all > -INFINITY; i0 += 32) {
       // weights of this group of parts, one per lane, then broadcast
       int sl = 0;

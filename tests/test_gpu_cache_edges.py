@@ -2,13 +2,17 @@
 one: tables with columns that hold no block, rows and queries that are not
 finite, calls without tokens."""
 
+import dataclasses
+
 import numpy as np
 import pytest
 import torch
 
 import compressed_mla_attention_gb300 as Q
+import workloads as W
 from oracle import cache_oracle as C
 from oracle import qsfm_oracle as O
+from tests.harness import assert_parity, run_gpu
 from tests.test_gpu_cache_operators import FORMATS, cache_values, i32, new_cache, table_of
 
 pytestmark = pytest.mark.gpu
@@ -198,3 +202,42 @@ def test_a_step_without_tokens(cuda_device, fmt):
     assert Q.norm_rope_store(None, kv[:, None], **store) is None
     torch.cuda.synchronize()
     assert Q.device_status() == 0 and torch.equal(cache, before)
+
+
+# ------------------------------------------------------------------ attention over what is not finite
+def nan_row(w, fmt, row):
+    """w with a NaN in cmp row `row` of request 0."""
+    kv = w.cmp_kv.clone()
+    at = kv.view(-1, kv.shape[-1])[int(w.cmp_block_table[0, row // 128]) * 128 + row % 128]
+    if fmt == "packed384":
+        at[352 + 9] = 0x7F  # one scale
+    elif fmt == "packed640":
+        at[576 + 2] = 0xFF
+    elif fmt == "fp8_fp32_scales":
+        at[130] = 0x7F
+    else:
+        at[130] = float("nan")
+    return dataclasses.replace(w, cmp_kv=kv)
+
+
+# CTAs: units split over them (more than one part holds the row's unit), and not
+@pytest.mark.parametrize("ctas", [16, 7, 1])
+@pytest.mark.parametrize("fmt", ["packed384"])
+def test_nan_rows_and_queries_show_in_every_plan(cuda_device, fmt, ctas):
+    """A NaN in one row of one part makes its token's output and lse NaN, and a
+    NaN in one head's query those of its head, however the tiles are cut; the
+    rest is what it is without them."""
+    w = W.build(f"nan {fmt}", layout="BSND", q_lens=[1, 1], s2=[70000, 50000], cmp_ratio=128, mode="HCA", kv_format=fmt, seed=5)
+    o_ref, l_ref = O.reference(w, [0, 1])
+    for row in (0, 200, 545):
+        out, lse = run_gpu(nan_row(w, fmt, row), cuda_device, num_ctas=ctas, lse=True)
+        assert np.isnan(out[0]).all() and np.isnan(lse[0]).all()
+        out[0], lse[0] = o_ref[0], l_ref[0]
+        assert_parity(out, lse, w, [0, 1], o_ref, l_ref)
+    q = w.q.clone()
+    q[0, 5, 17], q[1, 63, 511] = float("nan"), float("nan")
+    out, lse = run_gpu(dataclasses.replace(w, q=q), cuda_device, num_ctas=ctas, lse=True)
+    for t, h in ((0, 5), (1, 63)):
+        assert np.isnan(out[t, h]).all() and np.isnan(lse[t, h])
+        out[t, h], lse[t, h] = o_ref[t, h], l_ref[t, h]
+    assert_parity(out, lse, w, [0, 1], o_ref, l_ref)
