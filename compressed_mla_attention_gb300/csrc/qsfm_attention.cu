@@ -762,14 +762,15 @@ __device__ void worker_role(const qsfm_params& p, const Smem& sm, Range rg, int 
     if (tid < 64 && writable) {
       const float lt = any ? (red[tid] + red[64 + tid]) + (red[128 + tid] + red[192 + tid]) : 0.f;
       const float mu = m_used[tid];
-      const float lse2 = lt > 0.f ? mu + log2f(lt) : -INFINITY;
+      // not lt > 0: a sum of NaN is no piece without rows, it shows in the output and lse
+      const float lse2 = !(lt <= 0.f) ? mu + log2f(lt) : -INFINITY;
       if (whole) {
         float den = lt;
-        if (p.sinks != nullptr && lt > 0.f) den += exp2f(sink2 - mu);
-        inv[tid] = lt > 0.f ? 1.f / den : 0.f;
+        if (p.sinks != nullptr && !(lt <= 0.f)) den += exp2f(sink2 - mu);
+        inv[tid] = !(lt <= 0.f) ? 1.f / den : 0.f;
         if (p.return_lse) p.softmax_lse[size_t(t) * 64 + tid] = lse2 * kLn2;
       } else {
-        inv[tid] = lt > 0.f ? 1.f / lt : 0.f;
+        inv[tid] = !(lt <= 0.f) ? 1.f / lt : 0.f;
         ws.lse[size_t(slot) * 64 + tid] = lse2 * kLn2;
       }
     }

@@ -15,7 +15,10 @@
  *     x_j      = softmax_scale * sum_d Q[t, h, d] K~[j, d]
  *     O[t, h]  = sum_j e^{x_j} K~[j, :] / (sum_j e^{x_j} + e^{sink_h})
  *     lse[t,h] = log sum_j e^{x_j}          (the sink is not included)
- *   A token with no attended row gets O = 0 and lse = -inf.
+ *   A token with no attended row gets O = 0 and lse = -inf. A NaN in an attended
+ *   row makes the token's O and lse NaN, one in a head's query those of the head
+ *   (fp8 rows: a query that is not finite takes the scale that the 64 heads of its
+ *   group share in f16, so that the other heads' O and lse are not to be used).
  *
  * Modes (QuantSparseFlashMla, "约束说明" (constraints), third bullet):
  *   SWA  cmp_kv == NULL                        ori window only

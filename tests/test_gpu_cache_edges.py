@@ -222,7 +222,7 @@ def nan_row(w, fmt, row):
 
 # CTAs: units split over them (more than one part holds the row's unit), and not
 @pytest.mark.parametrize("ctas", [16, 7, 1])
-@pytest.mark.parametrize("fmt", ["packed384"])
+@pytest.mark.parametrize("fmt", FORMATS)
 def test_nan_rows_and_queries_show_in_every_plan(cuda_device, fmt, ctas):
     """A NaN in one row of one part makes its token's output and lse NaN, and a
     NaN in one head's query those of its head, however the tiles are cut; the
@@ -235,9 +235,12 @@ def test_nan_rows_and_queries_show_in_every_plan(cuda_device, fmt, ctas):
         out[0], lse[0] = o_ref[0], l_ref[0]
         assert_parity(out, lse, w, [0, 1], o_ref, l_ref)
     q = w.q.clone()
-    q[0, 5, 17], q[1, 63, 511] = float("nan"), float("nan")
+    q[0, 5, 17] = float("nan")
+    if fmt != "fp8_fp32_scales":  # there one scale serves the 64 heads of a token: the other token alone is compared
+        q[1, 63, 511] = float("nan")
     out, lse = run_gpu(dataclasses.replace(w, q=q), cuda_device, num_ctas=ctas, lse=True)
-    for t, h in ((0, 5), (1, 63)):
+    for t, h in torch.isnan(q).any(2).nonzero().tolist():
         assert np.isnan(out[t, h]).all() and np.isnan(lse[t, h])
         out[t, h], lse[t, h] = o_ref[t, h], l_ref[t, h]
-    assert_parity(out, lse, w, [0, 1], o_ref, l_ref)
+    tokens = [1] if fmt == "fp8_fp32_scales" else [0, 1]
+    assert_parity(out, lse, w, tokens, o_ref[tokens], l_ref[tokens])
