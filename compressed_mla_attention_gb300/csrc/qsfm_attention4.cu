@@ -646,8 +646,10 @@ __device__ void softmax_role(const qsfm_params& p, const Smem& sm, int first_uni
           const float mt = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
           const float mu = m_used[tid];
           float a = 1.f;
-          if (!seen) {  // nothing is accumulated yet
-            if (mt > -INFINITY) m_used[tid] = mt;
+          if (!seen) {
+            // Nothing is accumulated yet. Of scores that are all -inf the guess must not
+            // stay: a later score far below it would be lost. Any other is far above this.
+            m_used[tid] = mt > -INFINITY ? mt : -3e38f;
           } else if (mt > -INFINITY && (mu == -INFINITY || mt > mu + kRescaleLog2)) {
             a = (mu == -INFINITY) ? 0.f : exp2f(mu - mt);
             m_used[tid] = mt;

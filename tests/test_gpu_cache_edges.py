@@ -244,3 +244,31 @@ def test_nan_rows_and_queries_show_in_every_plan(cuda_device, fmt, ctas):
         out[t, h], lse[t, h] = o_ref[t, h], l_ref[t, h]
     tokens = [1] if fmt == "fp8_fp32_scales" else [0, 1]
     assert_parity(out, lse, w, tokens, o_ref[tokens], l_ref[tokens])
+
+
+@pytest.mark.parametrize("ctas", [1, 5])
+def test_a_first_tile_of_minus_infinities(cuda_device, ctas):
+    """The window of each token is its own row, whose first element is -inf and
+    meets a positive query: weight 0. The other rows' scores are all far below
+    zero, some -350 against the first tile's, and count as they are."""
+    w = W.build("4-bit minus inf", layout="TND", q_lens=[1, 1, 1], s2=[900, 700, 800], cmp_ratio=4, mode="CSA", k2=150,
+                kv_format="packed384", seed=21, sinks=False, ori_win_left=0)
+    q, ori, cmp = w.q.clone(), w.ori_kv.clone(), w.cmp_kv.clone()
+    q[:, :, 0], q[:, :, 1] = 1.0, -8000.0
+    first = torch.tensor([float("-inf"), 1.0], dtype=torch.bfloat16).view(torch.uint8)
+    ori.view(-1, 384)[:, :4] = first
+    cmp.view(-1, 384)[:, :4] = torch.tensor([0.5, 1.0], dtype=torch.bfloat16).view(torch.uint8)
+    w = dataclasses.replace(w, q=q, ori_kv=ori, cmp_kv=cmp)
+    out, lse = run_gpu(w, cuda_device, num_ctas=ctas, lse=True)
+    for t in range(3):
+        k = O.token_kv(w, t, t, 0)[1:]  # without the first row
+        x = w.softmax_scale * (O.q_fp64(w, t) @ k.T)
+        top = x.max(1, keepdims=True)
+        p = np.exp(x - top)
+        want = (p / p.sum(1, keepdims=True)) @ k
+        # fp32 accumulation of 512 products of up to 8000: 512 roundings of 2^-24 of sum |q k|
+        dx = 512 * 2.0 ** -24 * w.softmax_scale * (np.abs(O.q_fp64(w, t)) @ np.abs(k).T).max(1) + 2.0 ** -20
+        bound = (2 * dx[:, None] + 2.0 ** -8 + len(k) * 2.0 ** -24) * ((p / p.sum(1, keepdims=True)) @ np.abs(k)) + 2.0 ** -8 * np.abs(want)
+        assert (np.abs(out[t] - want) <= 1.01 * bound)[:, 1:].all()  # of element 0 the formula has 0 * -inf
+        l = np.log(p.sum(1)) + top[:, 0]
+        assert (np.abs(lse[t] - l) <= dx + len(k) * 2.0 ** -24 + 2.0 ** -20 * np.abs(l)).all()
