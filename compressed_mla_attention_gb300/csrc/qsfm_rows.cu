@@ -183,7 +183,8 @@ __device__ __forceinline__ void norm_rope_row(const qsfm_norm_rope_params& p, bo
 // elements on the wrong side, and 3 to 6 of the codes of the other formats; this
 // none. It costs the key rows half of their time (8191 fp32 rows 7.9 -> 12.0 us,
 // one token 3.1 -> 3.6 us); the query rows, whose results are not stored codes, go
-// without.
+// without. The sum and the product with what they leave over are Knuth's and Dekker's
+// error-free transformations (the product's rest by a fused multiply-add).
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   s = a + b;
   const float t = s - a;
@@ -346,14 +347,13 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-__device__ __forceinline__ uint2 dequant8(uint32_t codes, float scale, float (&v)[8]) {
+__device__ __forceinline__ void dequant8(uint32_t codes, float scale, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint2 d = dequant4_e2m1(codes >> (16 * i), scale);
     const float2 a = of_bf16x2(d.x), b = of_bf16x2(d.y);
     v[4 * i] = a.x; v[4 * i + 1] = a.y; v[4 * i + 2] = b.x; v[4 * i + 3] = b.y;
   }
-  return make_uint2(0, 0);
 }
 
 // The warp's row y + z into row `slot` of the cache (slot < 0: nowhere); y becomes

@@ -276,7 +276,10 @@ qsfm_status qsfm_forward_workspace_size(const qsfm_params* p, size_t* bytes);
  * token across CTAs) the log-sum-exp combine kernel. Writes attn_out and,
  * when return_lse is set, softmax_lse. p->metadata must come from
  * qsfm_metadata() with the same shapes and lengths (QuantSparseFlashMla,
- * "约束说明": metadata is required, shape [1024]).
+ * "约束说明": metadata is required, shape [1024]). A call gives the same bits
+ * every time. In another batch a token may differ in its last bits: where it is
+ * split otherwise, and over 4-bit rows also by the tokens worked on before it,
+ * whose maxima are the first reference of its softmax.
  * workspace: device memory of at least qsfm_forward_workspace_size() bytes.
  */
 qsfm_status qsfm_forward(const qsfm_params* p, void* workspace,
@@ -606,7 +609,8 @@ typedef struct qsfm_block_table_params {
 /* Defaults: cmp_ratio 1, block size 128, all pointers NULL. */
 void qsfm_block_table_params_init(qsfm_block_table_params* p);
 
-/* One launch on `stream`; no workspace, nothing read back. Errors:
+/* One launch on `stream`, two where max_rows is above 8192 and the count is
+ * updated in place; no workspace, nothing read back. Errors:
  * QSFM_ERR_INVALID_ARG, QSFM_ERR_UNSUPPORTED (more than 8192 requests, a
  * block size other than 128, a pool of 2^31 rows or more, max_blocks * 128 or
  * max_rows or B * max_blocks above 2^30). */

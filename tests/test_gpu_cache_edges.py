@@ -272,3 +272,45 @@ def test_a_first_tile_of_minus_infinities(cuda_device, ctas):
         assert (np.abs(out[t] - want) <= 1.01 * bound)[:, 1:].all()  # of element 0 the formula has 0 * -inf
         l = np.log(p.sum(1)) + top[:, 0]
         assert (np.abs(lse[t] - l) <= dx + len(k) * 2.0 ** -24 + 2.0 ** -20 * np.abs(l)).all()
+
+
+@pytest.mark.parametrize("ctas", [64, 3])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_a_broken_row_shows_in_the_tokens_that_attend_it(cuda_device, fmt, ctas):
+    """Stored by one call, read by the next: a NaN in a key row reaches the
+    tokens whose window holds the row and no others."""
+    dev, n, window, at = cuda_device, 40, 8, 20
+    g = torch.Generator().manual_seed(9)
+    x, q = torch.randn(n, 512, generator=g), torch.randn(n, 64, 512, generator=g).to(torch.bfloat16).to(dev)
+    order = torch.arange(n, dtype=torch.int32, device=dev)
+    runs = []
+    for value in (0.5, float("nan")):
+        x[at, 100] = value
+        cache, scale = new_cache(fmt, 1, dev)
+        Q.norm_rope_store(None, x.to(dev), kv_cache=cache, kv_scale=scale, slot_map=order, positions=order,
+                          cos_sin=table_of(n, 64, dev))
+        out, lse = Q.quant_sparse_flash_mla(q, cache, scale, i32([[0]], dev), i32([n], dev), layout="TND",
+                                            cu_seqlens_q=i32([0, n], dev), ori_win_left=window - 1, num_ctas=ctas,
+                                            return_softmax_lse=True)
+        torch.cuda.synchronize()
+        assert Q.device_status() == 0
+        runs.append((out.float().cpu().numpy(), lse.cpu().numpy(), np.abs(cache_values(cache, scale, range(n)))))
+    (clean, clean_lse, rows), (out, lse, _) = runs
+    hit = np.zeros(n, dtype=bool)
+    hit[at:at + window] = True
+    assert np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
+    # the others: the same rows, the weights rounded to 8 bits against another reference, the output to 8 bits
+    assert np.abs(out[~hit] - clean[~hit]).max() <= 4 * 2.0 ** -8 * rows.max()
+    # 512 products in fp32, twice: less than 2^-13 of sum |q k| / sqrt(512) (below 40 for these rows)
+    assert np.abs(lse[~hit] - clean_lse[~hit]).max() <= 40 * 2.0 ** -13
+
+
+@pytest.mark.parametrize("ctas", [0, 1, 7])
+def test_a_call_repeats_its_bits(cuda_device, ctas):
+    """The same call gives the same bits, split units among them."""
+    w = W.build("4-bit repeat", layout="TND", q_lens=[3, 1, 6], s2=[5000, 129, 20000], cmp_ratio=4, mode="CSA", k2=512,
+                kv_format="packed384", seed=31)
+    out, lse = run_gpu(w, cuda_device, num_ctas=ctas, lse=True)
+    for _ in range(20):
+        again, again_lse = run_gpu(w, cuda_device, num_ctas=ctas, lse=True)
+        assert np.array_equal(out, again) and np.array_equal(lse, again_lse)
