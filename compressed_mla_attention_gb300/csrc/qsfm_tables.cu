@@ -207,7 +207,8 @@ __global__ void __launch_bounds__(kTabThreads, 2) block_table_kernel(const qsfm_
     const int first = s_need[b], after = s_given[b] + blocks - 1 - i;  // columns with a block behind it
     const int32_t* columns = p.block_table + size_t(b) * p.max_blocks;
     if (blocks == c - first) return columns[c - 1 - after];
-    // some columns hold none: from the last one down (the front ones are those behind a window)
+    // some columns hold none: from the last one down (the front ones are those behind a window),
+    // at most the request's columns, some 0.3 us per eight
     for (int left = after; c > first;) {
       constexpr int kAtOnce = 8;
       int block[kAtOnce];
