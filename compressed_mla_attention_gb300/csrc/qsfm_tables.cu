@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kTabThreads, 2) block_table_kernel(const qsfm_
     const int32_t* columns = p.block_table + size_t(b) * p.max_blocks;
     if (blocks == c - first) return columns[c - 1 - after];
     // some columns hold none: from the last one down (the front ones are those behind a window),
-    // at most the request's columns, some 0.3 us per eight
+    // 0.16 us per eight columns: a request of 1024 that ends with holes takes 20 us more at most
     for (int left = after; c > first;) {
       constexpr int kAtOnce = 8;
       int block[kAtOnce];
