@@ -55,6 +55,9 @@ FAULT_KV_ROW = 0x80
 FAULT_BLOCK_POOL = 0x100
 FAULT_SLOT = 0x200
 FAULT_POSITION = 0x400
+FAULT_ROW_INDEX = 0x800
+FAULT_GROUP_ROWS = 0x1000
+SCALE_GROUP = 128
 LAYOUT_KV = {"PA_BBND": 0, "BSND": 1, "TND": 2}
 
 _i32 = ctypes.c_int32
@@ -125,6 +128,29 @@ class BlockTableParams(ctypes.Structure):
     ]
 
 
+class QuantizeParams(ctypes.Structure):
+    """Mirror of ``qsfm_quantize_params`` (include/qsfm.h); field order must match."""
+
+    _fields_ = [
+        ("rows", _i32), ("source_rows", _i32), ("heads", _i32), ("dim", _i32), ("in_type", _i32), ("pow2_scale", _i32),
+        ("rope_dim", _i32), ("rope_offset", _i32), ("interleaved", _i32), ("inverse", _i32), ("max_positions", _i32),
+        ("x_row_stride", _i64), ("x_head_stride", _i64), ("gate_row_stride", _i64), ("gate_head_stride", _i64),
+        ("x", _ptr), ("gate", _ptr), ("row_index", _ptr), ("positions", _ptr), ("cos_sin", _ptr), ("codes", _ptr),
+        ("scale", _ptr),
+    ]
+
+
+class MatmulParams(ctypes.Structure):
+    """Mirror of ``qsfm_matmul_params`` (include/qsfm.h); field order must match."""
+
+    _fields_ = [
+        ("rows", _i32), ("n", _i32), ("k", _i32), ("groups", _i32), ("out_type", _i32),
+        ("a_row_stride", _i64), ("w_row_stride", _i64), ("w_group_stride", _i64), ("a_scale_row_stride", _i64),
+        ("a_scale_col_stride", _i64), ("out_row_stride", _i64),
+        ("a", _ptr), ("a_scale", _ptr), ("w", _ptr), ("w_scale", _ptr), ("cu_rows", _ptr), ("out", _ptr),
+    ]
+
+
 class QsfmError(RuntimeError):
     def __init__(self, fn: str, code: int, cuda_error: str = ""):
         detail = f" ({cuda_error})" if cuda_error else ""
@@ -157,6 +183,10 @@ EXPORTS = {
     "qsfm_norm_rope_store": (_i32, [ctypes.POINTER(NormRopeParams), _ptr]),
     "qsfm_block_table_params_init": (None, [ctypes.POINTER(BlockTableParams)]),
     "qsfm_update_block_tables": (_i32, [ctypes.POINTER(BlockTableParams), _ptr]),
+    "qsfm_quantize_params_init": (None, [ctypes.POINTER(QuantizeParams)]),
+    "qsfm_quantize_rows": (_i32, [ctypes.POINTER(QuantizeParams), _ptr]),
+    "qsfm_matmul_params_init": (None, [ctypes.POINTER(MatmulParams)]),
+    "qsfm_scaled_matmul": (_i32, [ctypes.POINTER(MatmulParams), _ptr]),
 }
 
 
@@ -869,3 +899,175 @@ def update_block_tables(block_table, prev_lens, lens, free_list, free_count, *, 
     block_tables(make_block_table_params(block_table=block_table, prev_lens=prev_lens, lens=lens, free_list=free_list,
                                          free_count=free_count, slot_map=slot_map, **kwargs), stream)
     return slot_map, kwargs.get("positions")
+
+
+_E4M3 = ("torch.uint8", "torch.float8_e4m3fn")
+
+
+def _head_rows(name: str, t, shape=None):
+    """[T, K] or [T, N, D] as (T, N, D, row stride, head stride), elements contiguous."""
+    if t.dim() not in (2, 3) or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}; expected " + (str(tuple(shape)) if shape else "[T, K] or [T, N, D]"))
+    if int(t.shape[-1]) > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    heads = int(t.shape[1]) if t.dim() == 3 else 1
+    return int(t.shape[0]), heads, int(t.shape[-1]), t.stride(0), t.stride(1) if heads > 1 else 0
+
+
+def make_quantize_params(
+    *,
+    x,
+    codes,
+    scale,
+    gate=None,
+    row_index=None,
+    positions=None,
+    cos_sin=None,
+    rope_offset: int = 0,
+    interleaved: bool = True,
+    inverse: bool = False,
+    pow2_scale: bool = False,
+) -> _Launch:
+    """A parameter block for quantize() (arguments as quantize_rows()), to be
+    made once for fixed buffers and launched every step."""
+    tensors = dict(x=x, gate=gate, row_index=row_index, positions=positions, cos_sin=cos_sin, codes=codes, scale=scale)
+    src, heads, dim, row_stride, head_stride = _head_rows("x", x)
+    if str(x.dtype) not in ELEM_TYPE or (gate is not None and gate.dtype != x.dtype):
+        raise ValueError("x and gate must have one type: bfloat16, float16 or float32")
+    _expect("row_index", row_index, _I32, (None,))
+    T, K = src if row_index is None else int(row_index.shape[0]), heads * dim
+    groups = -(-K // SCALE_GROUP)
+    _expect("positions", positions, _I32, (T,))
+    _expect("cos_sin", cos_sin, _F32, (None, None))
+    _expect("codes", codes, _E4M3, (T, K) if codes.dim() == 2 else (T,) + tuple(x.shape[1:]))
+    _expect("scale", scale, _F32, (T, groups))
+    dev = _one_device(tensors)
+    p = QuantizeParams()
+    lib().qsfm_quantize_params_init(ctypes.byref(p))
+    p.rows, p.source_rows, p.heads, p.dim = T, src, heads, dim
+    p.in_type, p.pow2_scale = ELEM_TYPE[str(x.dtype)], int(bool(pow2_scale))
+    p.rope_offset, p.interleaved, p.inverse = int(rope_offset), int(bool(interleaved)), int(bool(inverse))
+    if cos_sin is not None:
+        p.max_positions, p.rope_dim = int(cos_sin.shape[0]), int(cos_sin.shape[1])
+    p.x, p.x_row_stride, p.x_head_stride = x.data_ptr(), row_stride, head_stride
+    if gate is not None:
+        _, _, _, p.gate_row_stride, p.gate_head_stride = _head_rows("gate", gate, x.shape)
+        p.gate = gate.data_ptr()
+    p.row_index, p.positions, p.cos_sin = _dptr(row_index), _dptr(positions), _dptr(cos_sin)
+    p.codes, p.scale = _dptr(codes), _dptr(scale)
+    return _Launch(p, dev, tensors)
+
+
+def quantize(launch: _Launch, stream=None) -> None:
+    """qsfm_quantize_rows() with a block of make_quantize_params()."""
+    launch.call("qsfm_quantize_rows", stream)
+
+
+def quantize_rows(x, *, codes=None, scale=None, stream=None, **kwargs):
+    """Rows as e4m3 codes with one fp32 scale per 128 elements
+    (qsfm_quantize_rows): what lightning_indexer() takes as queries (a head of
+    128 elements has one scale) and scaled_matmul() as rows.
+
+    x [T, K] or [T, N, D] bf16, fp16 or fp32 with contiguous last axis, its
+    other strides multiples of 16 bytes; K (N * D) a multiple of 16, D of 128
+    with more than one head. gate (x's shape and type): the rows are silu(gate)
+    * x. positions int32 [T] and cos_sin fp32 [P, rope_dim]: rope_dim elements
+    of each head from rope_offset on are turned as norm_rope_store() turns
+    them, or back (inverse). row_index int32 [T]: row t is made of x's row
+    row_index[t]. pow2_scale: scales are powers of two. Rows of a negative
+    index or position are padding: nothing is written for them. codes uint8 or
+    float8_e4m3fn ([T, K] or x's shape) and scale fp32 [T, ceil(K / 128)] are
+    allocated (zeros) when not given. With a stream of its own the call expects
+    its inputs to be there for that stream, and to live until it has run.
+    Returns (codes, scale).
+    """
+    import torch
+
+    index = kwargs.get("row_index")
+    T = int(x.shape[0]) if index is None else int(index.shape[0])
+    with _on(stream, x.device):
+        if codes is None:
+            codes = torch.zeros((T,) + tuple(x.shape[1:]), dtype=torch.uint8, device=x.device)
+        if scale is None:
+            k = int(x[0].numel()) if x.shape[0] else int(x.shape[1:].numel())
+            scale = torch.zeros(T, -(-k // SCALE_GROUP), device=x.device)
+    quantize(make_quantize_params(x=x, codes=codes, scale=scale, **kwargs), stream)
+    return codes, scale
+
+
+def make_matmul_params(*, a, a_scale, w, w_scale, out, cu_rows=None) -> _Launch:
+    """A parameter block for matmul() (arguments as scaled_matmul() or, with
+    cu_rows, grouped_scaled_matmul()), to be made once for fixed buffers."""
+    tensors = dict(a=a, a_scale=a_scale, w=w, w_scale=w_scale, cu_rows=cu_rows, out=out)
+    for name, t in (("a", a), ("w", w)):
+        if str(t.dtype) not in _E4M3:
+            raise ValueError(f"{name} has type {t.dtype}; expected {' or '.join(_E4M3)}")
+    if a.dim() != 2:
+        raise ValueError("a must be [M, K]")
+    M, K = int(a.shape[0]), int(a.shape[1])
+    if w.dim() != (2 if cu_rows is None else 3) or int(w.shape[-1]) != K:
+        raise ValueError(f"w must be {'[N, K]' if cu_rows is None else '[groups, N, K]'} with K = {K}")
+    groups, N = 1 if cu_rows is None else int(w.shape[0]), int(w.shape[-2])
+    for name, t in (("a", a), ("w", w), ("out", out)):
+        if int(t.shape[-1]) > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+    kb, nb = -(-K // SCALE_GROUP), -(-N // SCALE_GROUP)
+    if str(a_scale.dtype) not in _F32 or tuple(a_scale.shape) != (M, kb):
+        raise ValueError(f"a_scale must be float32 [{M}, {kb}]")
+    _expect("w_scale", w_scale, _F32, (nb, kb) if cu_rows is None else (groups, nb, kb))
+    _expect("cu_rows", cu_rows, _I32, (groups + 1,))
+    if str(out.dtype) not in ELEM_TYPE or tuple(out.shape) != (M, N):
+        raise ValueError(f"out must be bfloat16, float16 or float32 [{M}, {N}]")
+    dev = _one_device(tensors)
+    p = MatmulParams()
+    lib().qsfm_matmul_params_init(ctypes.byref(p))
+    p.rows, p.n, p.k, p.groups, p.out_type = M, N, K, groups, ELEM_TYPE[str(out.dtype)]
+    p.a, p.a_row_stride = a.data_ptr(), a.stride(0)
+    p.a_scale, p.a_scale_row_stride, p.a_scale_col_stride = a_scale.data_ptr(), a_scale.stride(0), a_scale.stride(1)
+    p.w, p.w_row_stride, p.w_group_stride = w.data_ptr(), w.stride(-2), w.stride(0) if cu_rows is not None else 0
+    p.out, p.out_row_stride = out.data_ptr(), out.stride(0)
+    p.w_scale, p.cu_rows = _dptr(w_scale), _dptr(cu_rows)
+    return _Launch(p, dev, tensors)
+
+
+def matmul(launch: _Launch, stream=None) -> None:
+    """qsfm_scaled_matmul() with a block of make_matmul_params()."""
+    launch.call("qsfm_scaled_matmul", stream)
+
+
+def scaled_matmul(a, a_scale, w, w_scale, *, out=None, out_dtype=None, stream=None):
+    """a w^T of quantised rows and a quantised matrix (qsfm_scaled_matmul).
+
+    a e4m3 codes [M, K] (uint8 or float8_e4m3fn) with a_scale fp32 [M, ceil(K /
+    128)] (any strides), as quantize_rows() makes them; w codes [N, K] with
+    w_scale fp32 [ceil(N / 128), ceil(K / 128)], one scale per 128 x 128
+    elements. K a multiple of 16; rows of a and w may be strided by multiples of
+    16 bytes. out [M, N] bf16, fp16 or fp32 (rows may be strided) is allocated
+    when not given, in out_dtype (default bf16). With a stream of its own the
+    call expects its inputs to be there for that stream, and to live until it
+    has run. Returns out.
+    """
+    return _matmul(a, a_scale, w, w_scale, None, out, out_dtype, stream)
+
+
+def grouped_scaled_matmul(a, a_scale, w, w_scale, cu_rows, *, out=None, out_dtype=None, stream=None):
+    """scaled_matmul() with one matrix per group of rows: rows cu_rows[g] ..
+    cu_rows[g + 1] - 1 of a (cu_rows int32 [groups + 1], on the device) times
+    w[g]^T, w [groups, N, K], w_scale [groups, ceil(N / 128), ceil(K / 128)].
+    Groups may be empty. Rows outside all groups are left as they are: zeros
+    where out is not given. Returns out [M, N].
+    """
+    return _matmul(a, a_scale, w, w_scale, cu_rows, out, out_dtype, stream)
+
+
+def _matmul(a, a_scale, w, w_scale, cu_rows, out, out_dtype, stream):
+    import torch
+
+    if out is None:
+        with _on(stream, a.device):
+            make = torch.empty if cu_rows is None else torch.zeros
+            out = make(int(a.shape[0]), int(w.shape[-2]), dtype=out_dtype or torch.bfloat16, device=a.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError(f"out has type {out.dtype}, not {out_dtype}")
+    matmul(make_matmul_params(a=a, a_scale=a_scale, w=w, w_scale=w_scale, out=out, cu_rows=cu_rows), stream)
+    return out

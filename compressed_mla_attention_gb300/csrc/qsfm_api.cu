@@ -402,6 +402,111 @@ qsfm_status check_block_tables(const qsfm_block_table_params* pp) {
   return QSFM_OK;
 }
 
+// A tensor's bytes, for the overlap checks.
+struct Bytes {
+  const void* at;
+  long long n;
+};
+
+// Limits of the quantiser's 32-bit group arithmetic (a warp's last group among it).
+constexpr long long kMaxQuantGroups = (1ll << 31) - (1ll << 16);
+constexpr long long kMaxQuantStride = 1ll << 31;
+
+qsfm_status check_quantize(const qsfm_quantize_params* pp) {
+  if (pp == nullptr) return QSFM_ERR_INVALID_ARG;
+  const qsfm_quantize_params& p = *pp;
+  if (p.rows < 0 || p.source_rows < 0 || p.heads < 1 || p.dim < 1) return QSFM_ERR_INVALID_ARG;
+  if (p.in_type != QSFM_BF16 && p.in_type != QSFM_F16 && p.in_type != QSFM_F32) return QSFM_ERR_INVALID_ARG;
+  const long long k = (long long)p.heads * p.dim;
+  if (k % 16 != 0 || (p.heads > 1 && p.dim % 128 != 0)) return QSFM_ERR_UNSUPPORTED;
+  if (k > 1 << 30 || p.rows * ((k + 127) / 128) >= kMaxQuantGroups) return QSFM_ERR_UNSUPPORTED;
+  if (p.rope_dim < 0 || p.rope_offset < 0 || p.rope_dim + (long long)p.rope_offset > p.dim) return QSFM_ERR_INVALID_ARG;
+  if (p.rope_dim != 0) {
+    if (p.rope_dim != 32 && p.rope_dim != 64 && p.rope_dim != 128) return QSFM_ERR_UNSUPPORTED;
+    if (p.rope_offset % p.rope_dim != 0) return QSFM_ERR_UNSUPPORTED;
+  }
+  if (p.rows == 0) return QSFM_OK;  // of empty tensors, whose pointers are null, nothing is asked
+  if (p.codes == nullptr || p.scale == nullptr || (p.x == nullptr && p.source_rows > 0)) return QSFM_ERR_INVALID_ARG;
+  if (p.row_index == nullptr && p.source_rows != p.rows) return QSFM_ERR_INVALID_ARG;
+  if (p.rope_dim != 0) {
+    if (p.cos_sin == nullptr || p.positions == nullptr || p.max_positions < 1 || p.gate != nullptr)
+      return QSFM_ERR_INVALID_ARG;
+  } else if (p.cos_sin != nullptr) {
+    return QSFM_ERR_INVALID_ARG;
+  }
+  for (const long long stride : {p.x_row_stride, p.x_head_stride, p.gate_row_stride, p.gate_head_stride})
+    if (stride >= kMaxQuantStride) return QSFM_ERR_UNSUPPORTED;
+  // 16-byte vector accesses to the rows and the table
+  const long long size = p.in_type == QSFM_F32 ? 4 : 2;
+  if (p.x_row_stride < 0 || p.x_head_stride < 0 || (p.x_row_stride * size) % 16 != 0 || (p.x_head_stride * size) % 16 != 0)
+    return QSFM_ERR_INVALID_ARG;
+  if (p.gate != nullptr && (p.gate_row_stride < 0 || p.gate_head_stride < 0 || (p.gate_row_stride * size) % 16 != 0 ||
+                            (p.gate_head_stride * size) % 16 != 0))
+    return QSFM_ERR_INVALID_ARG;
+  if (!aligned(p.x, 16) || !aligned(p.gate, 16) || !aligned(p.cos_sin, 16) || !aligned(p.codes, 16))
+    return QSFM_ERR_INVALID_ARG;
+  if (!aligned(p.row_index, 4) || !aligned(p.positions, 4) || !aligned(p.scale, 4)) return QSFM_ERR_INVALID_ARG;
+  const long long T = p.rows, S = p.source_rows;
+  const auto extent = [&](long long row, long long head) {
+    return S == 0 ? 0 : ((S - 1) * row + (p.heads - 1) * head + p.dim) * size;
+  };
+  const Bytes outs[] = {{p.codes, T * k}, {p.scale, T * ((k + 127) / 128) * 4}};
+  const Bytes ins[] = {{p.x, extent(p.x_row_stride, p.x_head_stride)},
+                       {p.gate, extent(p.gate_row_stride, p.gate_head_stride)},
+                       {p.row_index, T * 4},
+                       {p.positions, T * 4},
+                       {p.cos_sin, (long long)p.max_positions * p.rope_dim * 4}};
+  for (const Bytes& o : outs)
+    for (const Bytes& i : ins)
+      if (overlap(o.at, o.n, i.at, i.n)) return QSFM_ERR_INVALID_ARG;
+  return overlap(outs[0].at, outs[0].n, outs[1].at, outs[1].n) ? QSFM_ERR_INVALID_ARG : QSFM_OK;
+}
+
+constexpr long long kMaxStride = 1ll << 37;  // elements; times a number of rows it stays within 64 bits
+constexpr int kMaxMatmulGroups = 1024;
+constexpr int kMaxMatmulSize = 1 << 24;
+constexpr long long kMaxMatmulTiles = 1 << 30;  // of 128 x 16 outputs, the smallest
+
+qsfm_status check_matmul(const qsfm_matmul_params* pp) {
+  if (pp == nullptr) return QSFM_ERR_INVALID_ARG;
+  const qsfm_matmul_params& p = *pp;
+  if (p.rows < 0 || p.n < 1 || p.k < 1 || p.groups < 1) return QSFM_ERR_INVALID_ARG;
+  if (p.out_type != QSFM_BF16 && p.out_type != QSFM_F16 && p.out_type != QSFM_F32) return QSFM_ERR_INVALID_ARG;
+  if (p.groups > 1 && p.cu_rows == nullptr && p.rows > 0) return QSFM_ERR_INVALID_ARG;
+  if (p.k % 16 != 0 || p.groups > kMaxMatmulGroups) return QSFM_ERR_UNSUPPORTED;
+  if (p.rows >= kMaxMatmulSize || p.n >= kMaxMatmulSize || p.k >= kMaxMatmulSize) return QSFM_ERR_UNSUPPORTED;
+  if (((p.rows + 15ll) / 16 + p.groups) * ((p.n + 127ll) / 128) > kMaxMatmulTiles) return QSFM_ERR_UNSUPPORTED;
+  if (p.rows == 0) return QSFM_OK;  // of empty tensors, whose pointers are null, nothing is asked
+  if (p.a == nullptr || p.a_scale == nullptr || p.w == nullptr || p.w_scale == nullptr || p.out == nullptr)
+    return QSFM_ERR_INVALID_ARG;
+  if (!aligned(p.a, 16) || !aligned(p.w, 16)) return QSFM_ERR_INVALID_ARG;
+  // a dimension of length 1 may have any stride: it is not stepped along
+  const auto bad = [](long long stride, long long least, long long count) {
+    return count > 1 && (stride < least || stride % 16 != 0);
+  };
+  for (const long long stride : {p.a_row_stride, p.w_row_stride, p.w_group_stride, p.a_scale_row_stride,
+                                 p.a_scale_col_stride, p.out_row_stride})
+    if (stride >= kMaxStride) return QSFM_ERR_UNSUPPORTED;
+  if (bad(p.a_row_stride, p.k, p.rows) || bad(p.w_row_stride, p.k, p.n) ||
+      bad(p.w_group_stride, (p.n - 1) * (p.n > 1 ? p.w_row_stride : 0) + p.k, p.groups))
+    return QSFM_ERR_INVALID_ARG;
+  if (p.a_row_stride < 0 || p.w_row_stride < 0 || p.w_group_stride < 0 || p.a_scale_row_stride < 0 ||
+      p.a_scale_col_stride < 0 || p.out_row_stride < 0 || (p.rows > 1 && p.out_row_stride < p.n))
+    return QSFM_ERR_INVALID_ARG;
+  const long long size = p.out_type == QSFM_F32 ? 4 : 2, M = p.rows, kb = (p.k + 127ll) / 128;
+  if (!aligned(p.out, size) || !aligned(p.a_scale, 4) || !aligned(p.w_scale, 4) || !aligned(p.cu_rows, 4))
+    return QSFM_ERR_INVALID_ARG;
+  const Bytes out = {p.out, ((M - 1) * p.out_row_stride + p.n) * size};
+  const Bytes ins[] = {{p.a, (M - 1) * p.a_row_stride + p.k},
+                       {p.a_scale, ((M - 1) * p.a_scale_row_stride + (kb - 1) * p.a_scale_col_stride + 1) * 4},
+                       {p.w, (p.groups - 1) * p.w_group_stride + (p.n - 1) * p.w_row_stride + p.k},
+                       {p.w_scale, p.groups * ((p.n + 127ll) / 128) * kb * 4},
+                       {p.cu_rows, p.cu_rows != nullptr ? (p.groups + 1ll) * 4 : 0}};
+  for (const Bytes& i : ins)
+    if (overlap(out.at, out.n, i.at, i.n)) return QSFM_ERR_INVALID_ARG;
+  return QSFM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -603,6 +708,38 @@ qsfm_status qsfm_update_block_tables(const qsfm_block_table_params* p, void* str
   if (fault == nullptr) return QSFM_ERR_CUDA;
   const NvtxRange range("qsfm_update_block_tables");
   return cuda_status(qsfm::launch_block_tables(*p, fault, static_cast<cudaStream_t>(stream)));
+}
+
+void qsfm_quantize_params_init(qsfm_quantize_params* p) {
+  if (p == nullptr) return;
+  std::memset(p, 0, sizeof(*p));
+  p->heads = 1;
+}
+
+qsfm_status qsfm_quantize_rows(const qsfm_quantize_params* p, void* stream) {
+  const qsfm_status st = check_quantize(p);
+  if (st != QSFM_OK) return st;
+  if (p->rows == 0) return QSFM_OK;
+  int* fault = fault_ptr();
+  if (fault == nullptr) return QSFM_ERR_CUDA;
+  const NvtxRange range("qsfm_quantize_rows");
+  return cuda_status(qsfm::launch_quantize(*p, fault, static_cast<cudaStream_t>(stream)));
+}
+
+void qsfm_matmul_params_init(qsfm_matmul_params* p) {
+  if (p == nullptr) return;
+  std::memset(p, 0, sizeof(*p));
+  p->groups = 1;
+}
+
+qsfm_status qsfm_scaled_matmul(const qsfm_matmul_params* p, void* stream) {
+  const qsfm_status st = check_matmul(p);
+  if (st != QSFM_OK) return st;
+  if (p->rows == 0) return QSFM_OK;
+  int* fault = fault_ptr();
+  if (fault == nullptr) return QSFM_ERR_CUDA;
+  const NvtxRange range("qsfm_scaled_matmul");
+  return cuda_status(qsfm::launch_matmul(*p, fault, static_cast<cudaStream_t>(stream)));
 }
 
 qsfm_status qsfm_get_device_status(int32_t* fault_word) {

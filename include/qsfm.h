@@ -172,6 +172,9 @@ typedef enum {
 #define QSFM_FAULT_SLOT           0x200 /* a slot past the end of the cache, or
                                           more new rows than slot_map holds */
 #define QSFM_FAULT_POSITION       0x400 /* a position past the cos_sin table */
+#define QSFM_FAULT_ROW_INDEX      0x800 /* a row_index past the source rows  */
+#define QSFM_FAULT_GROUP_ROWS     0x1000 /* cu_rows that decreases or leaves
+                                           the rows of the product           */
 
 /*
  * All inputs, attributes and outputs of one forward call. Pointers are
@@ -615,6 +618,118 @@ void qsfm_block_table_params_init(qsfm_block_table_params* p);
  * block size other than 128, a pool of 2^31 rows or more, max_blocks * 128 or
  * max_rows or B * max_blocks above 2^30). */
 qsfm_status qsfm_update_block_tables(const qsfm_block_table_params* p, void* stream);
+
+/*
+ * Rows quantised to e4m3 with an fp32 scale per 128 elements. An addition of
+ * this library: the form that qsfm_lightning_indexer() takes queries and keys in
+ * (a head of 128 elements has one scale) and qsfm_scaled_matmul() its rows.
+ * Row t of the K = heads * dim elements y, with A = max|y| of each 128 elements
+ * (the last scale of a row may have fewer):
+ *   scale = A / 448 and code = e4m3(448 y / A), A at least 1e-12; with
+ *   pow2_scale, scale = 2^e, e the smallest with A <= 448 2^e (clipped to -100 ..
+ *   100), and code = e4m3(y / scale); to nearest even, saturating.
+ *   y = x, silu(gate) * x when gate is given, or x with the rope_dim elements of
+ *   each head row from rope_offset on turned by the angles of positions[t], as
+ *   qsfm_norm_rope_store() turns them, or turned back when inverse is set (the
+ *   attention's output, whose values carry the keys' rotation).
+ * Every code is that of the formula (a gate below -87 counts as silu = 0); the
+ * scales are within 16 2^-24 of the formula's, without gate and rotation its
+ * rounding to fp32. A group with an element y that is not finite has codes and a
+ * scale of NaN.
+ *   x, gate    bf16, fp16 or fp32 (in_type) [source_rows, heads, dim], element
+ *              strides *_row_stride and *_head_stride, elements contiguous
+ *   row_index  int32 [T] or NULL: row t is made of row row_index[t] of x and gate
+ *              (without it source_rows must be T)
+ *   positions  int32 [T]; cos_sin fp32 [max_positions, rope_dim], both NULL with
+ *              rope_dim 0 (positions may be given all the same)
+ *   codes      e4m3fn bytes [T, K];  scale fp32 [T, ceil(K / 128)]
+ * A row whose index or position is negative is padding: nothing is written for it.
+ * A row whose index is past the source rows (QSFM_FAULT_ROW_INDEX) or whose position
+ * is past the table (QSFM_FAULT_POSITION) is skipped.
+ * K is a multiple of 16, dim of 128 with more than one head; rope_dim is 0, 32, 64
+ * or 128 and rope_offset a multiple of it; gate and a rotation exclude each other.
+ * x, gate, cos_sin, codes 16-byte aligned, strides multiples of 16 bytes, the rest
+ * 4-byte aligned. Outputs overlap no input.
+ */
+typedef struct qsfm_quantize_params {
+  int32_t rows;            /* T                                             */
+  int32_t source_rows;     /* rows of x and gate                            */
+  int32_t heads;           /* default 1                                     */
+  int32_t dim;
+  int32_t in_type;         /* qsfm_elem_type of x and gate                  */
+  int32_t pow2_scale;
+  int32_t rope_dim;
+  int32_t rope_offset;
+  int32_t interleaved;     /* pairs (2i, 2i + 1); else (i, i + rope_dim / 2) */
+  int32_t inverse;
+  int32_t max_positions;   /* rows of cos_sin                               */
+  int64_t x_row_stride, x_head_stride, gate_row_stride, gate_head_stride; /* in elements */
+  const void* x;
+  const void* gate;
+  const int32_t* row_index;
+  const int32_t* positions;
+  const float* cos_sin;
+  void* codes;
+  float* scale;
+} qsfm_quantize_params;
+
+/* Defaults: one head, pointers NULL. */
+void qsfm_quantize_params_init(qsfm_quantize_params* p);
+
+/* One launch on `stream` (none for T = 0, whose pointers are not looked at); no
+ * workspace, nothing read back. Errors: QSFM_ERR_INVALID_ARG,
+ * QSFM_ERR_UNSUPPORTED (K not a multiple of 16, heads of a dim that is not one of
+ * 128, rope_dim not built, T ceil(K / 128) of 2^31 - 2^16 or more, a stride of 2^31 or more). */
+qsfm_status qsfm_quantize_rows(const qsfm_quantize_params* p, void* stream);
+
+/*
+ * Product of quantised rows with quantised matrices. An addition of this library:
+ * the projections around the attention, and the experts' products.
+ *   out[m][j] = sum over blocks b of 128 of  a_scale[m][b] w_scale[g][j / 128][b]
+ *                 * (sum over k in b of a[m][k] w[g][j][k])
+ * with e4m3fn a and w; g is 0, or with cu_rows the group of row m, the g with
+ * cu_rows[g] <= m < cu_rows[g + 1]. The sum over a block is the tensor cores' (fp32
+ * accumulators), blocks are added in fp32, and the result is rounded once to
+ * out_type. A call gives the same bits every time; for another number of rows the
+ * blocks may be added in another order.
+ *   a          e4m3fn bytes [M, K], rows a_row_stride apart
+ *   a_scale    fp32 [M, ceil(K / 128)], element strides a_scale_row_stride and
+ *              a_scale_col_stride
+ *   w          e4m3fn bytes [groups, N, K], strides w_group_stride, w_row_stride
+ *   w_scale    fp32 [groups, ceil(N / 128), ceil(K / 128)]
+ *   cu_rows    int32 [groups + 1] or NULL (one group, all rows): rows of group g;
+ *              groups may be empty. Rows before the first and behind the last group
+ *              are left as they were. Entries that decrease or lie outside 0 .. M are
+ *              cut to what is there (QSFM_FAULT_GROUP_ROWS)
+ *   out        [M, N] of out_type, rows out_row_stride apart (elements)
+ * K is a multiple of 16. a, w: 16-byte aligned, strides multiples of 16 bytes; out
+ * aligned to its elements, the rest 4-byte aligned. out overlaps no input.
+ */
+typedef struct qsfm_matmul_params {
+  int32_t rows;            /* M                                             */
+  int32_t n;
+  int32_t k;
+  int32_t groups;          /* default 1                                     */
+  int32_t out_type;        /* qsfm_elem_type                                */
+  int64_t a_row_stride, w_row_stride, w_group_stride;
+  int64_t a_scale_row_stride, a_scale_col_stride;
+  int64_t out_row_stride;
+  const void* a;
+  const float* a_scale;
+  const void* w;
+  const float* w_scale;
+  const int32_t* cu_rows;
+  void* out;
+} qsfm_matmul_params;
+
+/* Defaults: one group, bf16 output, pointers NULL. */
+void qsfm_matmul_params_init(qsfm_matmul_params* p);
+
+/* One launch on `stream` (none for M = 0, whose pointers are not looked at); no
+ * workspace, nothing read back. Errors: QSFM_ERR_INVALID_ARG,
+ * QSFM_ERR_UNSUPPORTED (K not a multiple of 16, more than 1024 groups, M, N or K of
+ * 2^24 or more, more than 2^30 tiles of 16 x 128 outputs, a stride of 2^37 or more). */
+qsfm_status qsfm_scaled_matmul(const qsfm_matmul_params* p, void* stream);
 
 /* Synchronously read and clear the device fault word of the current
  * device (QSFM_FAULT_* bits). Returns QSFM_ERR_DEVICE_FAULT when non-zero. */
