@@ -7,19 +7,24 @@
 // each head turned by its position's angles; a row may be taken from anywhere in
 // the input (row_index).
 //
-// Sixteen lanes hold a group, eight neighbouring elements each, so A is four
-// shuffles of a maximum over the elements' bits (which also carries an inf or NaN
-// through), a pair of the rotation is in the lane (adjacent) or rope_dim / 16 lanes
-// apart (halves), and a group's codes are one 128-byte line. The kernel is bound by
-// HBM: a warp has the loads of 2 kItems groups in flight.
+// Eight lanes hold a group, each two runs of eight elements (8 l and 64 + 8 l), so that
+// a load of a 16-bit input is whole lines, A is three shuffles, and a pair of a rotation
+// is in the lane (adjacent, or 64 elements apart) or rope_dim / 16 lanes away. The kernel
+// is bound by HBM as long as it takes few instructions: with sixteen elements a lane what
+// is done once a group weighs little.
 //
-// Every code is the formula's. The fast path rounds 448 y / A with an error e of a
-// few units of fp32, so it converts the quotient twice, times 1 - e and 1 + e: where
-// both give the same code, that is the code. Elsewhere (an element next to the border
-// of two codes) the quotient is made again: for 16-bit inputs by a division, whose
-// fp32 result cannot cross a border (x has 8 or 11 significant bits, A as many and a
-// border five, so that 448 x and border * A are either equal or 2^-17 apart); for
-// computed y, and fp32 inputs, in 64 bits.
+// Every code is the formula's, by one of two ways.
+//  * Where y and A are 16-bit inputs as they are, 448 y / A either lies on the border of
+//    two codes or is 2^-17 of itself away from it (y and A have at most 11 significant
+//    bits, a border five). These borders are met all the time: with bf16 inputs in a
+//    quarter of the groups. The quotient is made a little too large, by 2 to 10 units of
+//    2^-24, and its last four bits are cut: what lies on a border is then on it, what
+//    does not stays on its side.
+//  * Elsewhere (y computed, or fp32) an element is next to a border by chance. The
+//    quotient, within a few units (error()), is converted twice, times 1 - error and
+//    1 + error: where both give the same code, that is the code. Otherwise the sign of
+//    448 |y| - m A decides, m the border (0: the even code), with y and A as sums of two
+//    fp32 values and the products' roundings carried: about 46 bits.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -32,12 +37,18 @@
 namespace qsfm {
 namespace {
 
-constexpr int kQGroup = 128;                 // elements of a scale
+constexpr int kQGroup = 128;        // elements of a scale
+constexpr int kQLanes = 8;          // lanes of a group
+constexpr int kQElems = 16;         // elements of a lane
 constexpr int kQWarps = 8;
 constexpr uint32_t kAllLanes = 0xffffffffu;
-constexpr float kQMin = 1e-12f;              // A of an all-zero group
+constexpr float kQMin = 1e-12f;     // A of an all-zero group
 
-enum QuantizeMode { kPlain = 0, kRotate = 1, kGated = 2 };
+enum QuantizeMode { kPlain = 0, kAdjacent = 1, kHalves = 2, kGated = 3 };  // the middle two turn pairs
+
+// Blocks on an SM, from what was measured: 16384 bf16 rows of 8192 in 58 us with 6, 62 with
+// 4; gated 32 (5), 33 (4); turned 91 (4), 96 (5, an item a warp), 106 (3).
+constexpr int blocks_per_sm(int mode) { return mode == kPlain ? 6 : mode == kGated ? 5 : 4; }
 
 // Division of 31-bit numbers by an invariant d: q = (n * m) >> (32 + s) with
 // m = ceil(2^(32 + s) / d), s = ceil(log2 d) - 1 (exact for n < 2^31).
@@ -56,8 +67,9 @@ struct QuantizeShape {
   uint32_t groups;   // scales of a row
   uint32_t total;    // rows * groups
   int k;             // elements of a row
-  FastDiv per_row;   // by groups
-  FastDiv per_head;  // by the groups of a head row
+  uint32_t units;    // fours of groups that a warp takes at a time
+  FastDiv groups_of; // by the groups of a row (kTurns: of a head row)
+  FastDiv heads_of;  // kTurns: by the heads; else by the groups of a head row
 };
 
 // 8 consecutive elements as they are read, and in fp32.
@@ -72,7 +84,7 @@ struct Eight {
 #pragma unroll
     for (int i = 0; i < int(sizeof(T) / 2); ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
+  __device__ __forceinline__ void get(float* f) const {
     if constexpr (sizeof(T) == 4) {
       const uint32_t x[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
 #pragma unroll
@@ -94,22 +106,60 @@ struct Eight {
   }
 };
 
-// e4m3 codes of a (low byte) and b, to nearest even, saturating.
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+// max(|a|, |b|), NaN when one is.
+__device__ __forceinline__ float abs_max(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)));
   return r;
 }
-__device__ __forceinline__ uint2 codes8(const float (&q)[8], float r) {
-  return make_uint2(e4m3x2(q[0] * r, q[1] * r) | (e4m3x2(q[2] * r, q[3] * r) << 16),
-                    e4m3x2(q[4] * r, q[5] * r) | (e4m3x2(q[6] * r, q[7] * r) << 16));
+
+// (a, b) * r, both products in one instruction.
+__device__ __forceinline__ float2 mul2(float a, float b, float r) {
+  float2 o;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a), "f"(b), "f"(r));
+  return o;
 }
 
-// fp64 to fp32, a result that is not exact made odd: a rounding to fewer bits that
-// follows is then that of the fp64 value.
-__device__ __forceinline__ float round_odd(double x) {
-  const float f = __double2float_rz(x);
-  return double(f) == x ? f : __uint_as_float(__float_as_uint(f) | 1u);
+// e4m3 codes of a (low byte), b, c, d, to nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+// Codes of y r; kCut: of the products without their last four bits.
+template <bool kCut>
+__device__ __forceinline__ void codes16(const float (&y)[kQElems], float r, uint32_t (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 a = mul2(y[4 * i], y[4 * i + 1], r), b = mul2(y[4 * i + 2], y[4 * i + 3], r);
+    if constexpr (kCut) {
+      a.x = __uint_as_float(__float_as_uint(a.x) & ~15u);
+      a.y = __uint_as_float(__float_as_uint(a.y) & ~15u);
+      b.x = __uint_as_float(__float_as_uint(b.x) & ~15u);
+      b.y = __uint_as_float(__float_as_uint(b.y) & ~15u);
+    }
+    c[i] = e4m3x4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// 1 / a within 1 unit in the last place (a and the result normal).
+__device__ __forceinline__ float rcp_approx(float a) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+  return r;
+}
+// a / 448 to nearest: a quotient by the reciprocal, corrected by its remainder, is the
+// rounded one (Markstein's theorem, the reciprocal being rounded to nearest).
+__device__ __forceinline__ float over448(float a) {
+  constexpr float kInv = 1.0f / 448.0f;
+  const float q = a * kInv;
+  return __fmaf_rn(__fmaf_rn(-448.f, q, a), kInv, q);
 }
 
 // The smallest e with a <= 448 2^e = 1.75 2^(8 + e), within -100 .. 100.
@@ -117,69 +167,89 @@ __device__ __forceinline__ int pow2_exponent(float a) {
   const uint32_t u = __float_as_uint(a);
   return min(max(int(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0), -100), 100);
 }
-__device__ __forceinline__ int pow2_exponent(double a) {
-  const uint64_t u = uint64_t(__double_as_longlong(a));
-  return min(max(int(u >> 52) - 1023 - 8 + ((u & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull ? 1 : 0), -100), 100);
-}
 __device__ __forceinline__ float power2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
-// The lane's cosines and sines: adjacent pairs use four of each, halves eight.
-struct Angles {
-  float c[8], s[8];
+// A value as the sum of two fp32 numbers, the second at most half a unit of the first.
+struct Wide {
+  float hi, lo;
 };
 
-// y = x turned: lanes with `in` hold elements of the rotated range. The products'
-// difference with what its roundings leave over (each result within 1.5 units), so
-// that y is as good where its terms cancel.
-__device__ __forceinline__ float turned(float a, float c, float b, float s) {  // a c - b s
+// a c - b s: the products' difference with what its roundings leave over (each result
+// within 1.5 units), so that y is as good where its terms cancel.
+__device__ __forceinline__ float turned(float a, float c, float b, float s) {
   const float w = b * s;
   return __fmaf_rn(a, c, -w) + __fmaf_rn(-b, s, w);
 }
-template <typename V>
-__device__ __forceinline__ V turned(V a, V c, V b, V s) {
-  return a * c - b * s;
-}
-template <typename V>
-__device__ __forceinline__ void turn(const qsfm_quantize_params& p, bool in, int r, const Angles& t, V (&y)[8]) {
-  if (p.interleaved) {
-    if (in) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const V a = y[2 * i], b = y[2 * i + 1];
-        y[2 * i] = turned(a, V(t.c[i]), b, V(t.s[i]));
-        y[2 * i + 1] = turned(b, V(t.c[i]), a, V(-t.s[i]));
-      }
-    }
-  } else {
-    const int apart = p.rope_dim / 16;  // lanes between the elements of a pair
-    const bool second = r >= p.rope_dim / 2;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const V other = __shfl_xor_sync(kAllLanes, y[i], apart);
-      if (in) y[i] = turned(y[i], V(t.c[i]), other, V(second ? -t.s[i] : t.s[i]));
-    }
-  }
+// The same to about 2^-46 of the terms: both products and their difference exact, what
+// is left over added in fp32.
+__device__ __forceinline__ Wide turned_wide(float a, float c, float b, float s) {
+  const float v = a * c, w = b * s;
+  const float d = v - w, part = d - v;
+  const float left = (v - (d - part)) - (w + part);  // v - w - d
+  const float e = left + (__fmaf_rn(a, c, -v) - __fmaf_rn(b, s, -w));
+  const float h = d + e;
+  return {h, e - (h - d)};
 }
 
-__device__ __forceinline__ float silu(float g) { return g * __fdividef(1.f, 1.f + expf(-g)); }
-__device__ __forceinline__ double silu(double g) { return g / (1.0 + exp(-g)); }
+// (a, b) + 1.
+__device__ __forceinline__ float2 plus1(float2 v) {
+  float2 o;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %4};\n add.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(v.x), "f"(v.y), "f"(1.f));
+  return o;
+}
+// (a, b) * (c, d).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 o;
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 z, x, y;\n"
+      " mov.b64 {%0, %1}, z;\n}"
+      : "=f"(o.x), "=f"(o.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return o;
+}
+// x silu(g) of two elements. Units of 2^-24: the exponent 1.25 |g| (its product, log2 e),
+// ex2 4, 1 + e 1, the reciprocal 2, two products: 1.25 |g| + 9.
+__device__ __forceinline__ float2 gated(float2 x, float2 g) {
+  const float2 t = mul2(g.x, g.y, -1.4426950408889634f);
+  const float2 e = plus1(make_float2(ex2_approx(t.x), ex2_approx(t.y)));
+  return mul2(x, mul2(g, make_float2(rcp_approx(e.x), rcp_approx(e.y))));
+}
 
-// One item of a lane: eight elements of group f and what they are multiplied by.
+// Which code is that of y, `code` or the next one away from zero: that of the nearer
+// value, num |y| - m den deciding on their border m.
+__device__ __forceinline__ uint32_t nearer(uint32_t code, Wide y, float num, Wide den) {
+  const uint32_t sign = code & 0x80u, lower = code & 0x7Fu;
+  uint32_t two;  // the codes' values
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(uint16_t(lower | ((lower + 1) << 8))));
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
+  const float m = 0.5f * (f.x + f.y);
+  const float yh = fabsf(y.hi), yl = y.hi < 0.f ? -y.lo : y.lo;
+  const float v = num * yh, w = m * den.hi;
+  const float over = (v - w) + ((__fmaf_rn(num, yh, -v) - __fmaf_rn(m, den.hi, -w)) + (num * yl - m * den.lo));
+  return sign | (over > 0.f ? lower + 1 : over < 0.f ? lower : lower + (lower & 1));
+}
+
+// A lane's sixteen elements of a group, two runs of eight, and what is done to them.
 template <typename T, int kMode>
 struct Item {
-  Eight<T> x, gate;
-  int row;       // output row, -1: nothing is stored
-  int k0;        // the lane's first element in the row
-  int r, pos;    // kRotate: its place in the rotated range, the row's position
-  bool live, in;
+  static constexpr bool kTurns = kMode == kAdjacent || kMode == kHalves;
 
-  __device__ __forceinline__ void load(const qsfm_quantize_params& p, const QuantizeShape& s, uint32_t f, int sub,
-                                       int* fault) {
-    live = f < s.total;
-    const uint32_t out = s.per_row.div(f), g = f - out * s.groups;
-    row = live ? int(out) : -1;
-    k0 = int(g) * kQGroup + 8 * sub;
-    live = live && k0 < s.k;
+  Eight<T> x[2], gate[2];
+  int row;      // output row, -1: nothing is stored
+  int k0;       // the lane's first element in the row; the other run is 64 further
+  int r, pos;   // kTurns: the first element's place in the rotated range, the row's position
+  bool live[2];
+
+  // The lane's part of the group of row `out` (out >= p.rows: of none) that begins at
+  // element d of head row h, element k of the row.
+  __device__ __forceinline__ void load(const qsfm_quantize_params& p, const QuantizeShape& s, uint32_t out, uint32_t h,
+                                       int d, int k, int* fault) {
+    const int sub = threadIdx.x & (kQLanes - 1);
+    row = out < uint32_t(p.rows) ? int(out) : -1;
+    k0 = k + 8 * sub;
+    d += 8 * sub;
     int src = row;
     if (p.row_index != nullptr && row >= 0) {
       src = __ldg(p.row_index + row);
@@ -189,204 +259,372 @@ struct Item {
       }
     }
     pos = 0;
-    if (p.positions != nullptr && row >= 0) {
-      pos = __ldg(p.positions + row);
-      if (pos < 0 || (kMode == kRotate && pos >= p.max_positions)) {
-        if (pos >= 0 && sub == 0) atomicOr(fault, QSFM_FAULT_POSITION);
-        row = -1;
+    if (p.positions != nullptr && row >= 0) pos = __ldg(p.positions + row);  // looked at in check()
+    const T* from = static_cast<const T*>(p.x) + size_t(src) * p.x_row_stride + size_t(h) * p.x_head_stride + d;
+    const T* with = static_cast<const T*>(p.gate) + size_t(src) * p.gate_row_stride + size_t(h) * p.gate_head_stride + d;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      live[j] = row >= 0 && k0 + 64 * j < s.k;
+      if (live[j]) {
+        x[j].load(from + 64 * j);
+        if constexpr (kMode == kGated) gate[j].load(with + 64 * j);
+      } else {
+        x[j].zero();
+        if constexpr (kMode == kGated) gate[j].zero();
       }
     }
-    live = live && row >= 0;
-    const uint32_t h = p.heads > 1 ? s.per_head.div(g) : 0;
-    const int d = k0 - int(h) * p.dim;  // element of the head row
-    if (live) {
-      x.load(static_cast<const T*>(p.x) + size_t(src) * p.x_row_stride + size_t(h) * p.x_head_stride + d);
-      if constexpr (kMode == kGated)
-        gate.load(static_cast<const T*>(p.gate) + size_t(src) * p.gate_row_stride + size_t(h) * p.gate_head_stride + d);
-    } else {
-      x.zero();
-      if constexpr (kMode == kGated) gate.zero();
-    }
-    if constexpr (kMode == kRotate) {
-      r = d - p.rope_offset;
-      in = live && r >= 0 && r < p.rope_dim;
+    if constexpr (kTurns) r = d - p.rope_offset;
+  }
+
+  // Drops the row where its position says so (after all loads are on their way).
+  __device__ __forceinline__ void check(const qsfm_quantize_params& p, int* fault) {
+    if (pos < 0 || (kTurns && row >= 0 && pos >= p.max_positions)) {
+      if (pos >= 0 && (threadIdx.x & (kQLanes - 1)) == 0) atomicOr(fault, QSFM_FAULT_POSITION);
+      row = -1;
+      live[0] = live[1] = false;
     }
   }
 
-  // The angles of the lane's pairs (a position's row of the table serves all heads of
-  // its token, so it comes from the caches; held from the load on, the angles of four
-  // items would cost 64 registers).
-  __device__ __forceinline__ void load_angles(const qsfm_quantize_params& p, Angles& t) const {
-    if (!in) return;
-    const int half = p.rope_dim / 2, at = p.interleaved ? r / 2 : r >= half ? r - half : r;
-    const float* c = p.cos_sin + size_t(pos) * p.rope_dim + at;
-#pragma unroll
-    for (int i = 0; i < 8; i += 4) {
-      if (i > 0 && p.interleaved) break;
-      const float4 a = __ldg(reinterpret_cast<const float4*>(c + i));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(c + half + i));
-      t.c[i] = a.x; t.c[i + 1] = a.y; t.c[i + 2] = a.z; t.c[i + 3] = a.w;
-      t.s[i] = b.x; t.s[i + 1] = b.y; t.s[i + 2] = b.z; t.s[i + 3] = b.w;
-    }
-    if (p.inverse) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) t.s[i] = -t.s[i];
-    }
+  // Whether run j is turned.
+  __device__ __forceinline__ bool in(const qsfm_quantize_params& p, int j) const {
+    return kTurns && live[j] && r + 64 * j >= 0 && r + 64 * j < p.rope_dim;
   }
 
-  template <typename V>
-  __device__ __forceinline__ void values(const qsfm_quantize_params& p, const Angles& t, V (&y)[8]) const {
-    float f[8];
-    x.get(f);
+  // Cosines and sines of run j (a position's row of the table serves all heads of its
+  // token, so it comes from the caches), the sines with the sign that makes an element
+  // a c - b s; of adjacent pairs four of each.
+  __device__ __forceinline__ void load_angles(const qsfm_quantize_params& p, int j, float (&c)[8], float (&s)[8]) const {
+    const int half = p.rope_dim / 2, at = r + 64 * j;
+    const float* from = p.cos_sin + size_t(pos) * p.rope_dim + (kMode == kAdjacent ? at / 2 : at >= half ? at - half : at);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = V(f[i]);
+    for (int i = 0; i < (kMode == kAdjacent ? 4 : 8); i += 4) {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(from + i));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(from + half + i));
+      c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
+      s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
+    }
+    const bool flip = (p.inverse != 0) != (kMode == kHalves && at >= half);
+#pragma unroll
+    for (int i = 0; i < (kMode == kAdjacent ? 4 : 8); ++i) s[i] = flip ? -s[i] : s[i];
+  }
+
+  // The elements y. kGated: `large` becomes whether one of the warp's gates is above 12
+  // in magnitude.
+  template <int kAs>
+  __device__ __forceinline__ void values(const qsfm_quantize_params& p, float (&y)[kQElems], bool& large) const {
+    x[0].get(y);
+    x[1].get(y + 8);
     if constexpr (kMode == kGated) {
-      gate.get(f);
+      float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] *= silu(V(f[i]));
-    }
-    if constexpr (kMode == kRotate) turn(p, in, r, t, y);
-  }
-
-  // The codes of the lane's elements and the group's scale.
-  __device__ __forceinline__ uint2 codes(const qsfm_quantize_params& p, float& scale) const {
-    float y[8];
-    Angles t;
-    if constexpr (kMode == kRotate) load_angles(p, t);
-    values(p, t, y);
-    uint32_t m = 0;
+      for (int j = 0; j < 2; ++j) {
+        float g[8];
+        gate[j].get(g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kAllLanes, m, o));
-    const bool bad = m >= 0x7F800000u;  // an element is not finite
-    const float top32 = bad ? 1.f : __uint_as_float(m), a = fmaxf(top32, kQMin);
-    // at least the relative error of a quotient, in units of 2^-24: those of y (kRotate
-    // 3; kGated 9: expf 2, 1 + e 1, the division 4, two products), those of A (as
-    // many), r 1, the products r (1 +- kErr) and y r 2
-    constexpr float kErr = kMode == kGated ? 0x1p-19f : kMode == kRotate ? 0x1p-20f : 0x1p-21f;
-    float r;
-    bool near_power = false;
-    if (p.pow2_scale) {
-      const int e = pow2_exponent(top32);
-      scale = power2(e);
-      r = power2(-e);
-      if constexpr (kMode != kPlain) near_power = abs(int(__float_as_uint(top32) & 0x7FFFFFu) - 0x600000) < 64;
-    } else {
-      r = __fdiv_rn(448.f, a);
-      scale = __fdiv_rn(a, 448.f);
-    }
-    uint2 c = codes8(y, r * (1.f - kErr));
-    const uint2 d = codes8(y, r * (1.f + kErr));
-    const bool differ = c.x != d.x || c.y != d.y;
-    if constexpr (kMode == kPlain) {
-      if (differ) {
-        if constexpr (sizeof(T) == 2) {
-          if (p.pow2_scale) {
-            c = codes8(y, r);  // exact
-          } else {
-            float q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __fdiv_rn(y[i] * 0.4375f, a);  // 448 / 1024: no overflow
-            c = codes8(q, 1024.f);
-          }
-        } else {
-          float q[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = p.pow2_scale ? y[i] * r : round_odd(double(y[i]) * 448.0 / double(a));
-          c = codes8(q, 1.f);
+        for (int i = 0; i < 8; i += 2) {
+          top = abs_max(top, g[i]);
+          top = abs_max(top, g[i + 1]);
+          const float2 v = gated(make_float2(y[8 * j + i], y[8 * j + i + 1]), make_float2(g[i], g[i + 1]));
+          y[8 * j + i] = v.x;
+          y[8 * j + i + 1] = v.y;
         }
       }
-    } else {
-      // the warp's two groups again where one has such an element: the branch holds shuffles
-      if (__any_sync(kAllLanes, (differ || near_power) && !bad)) {
-        double z[8], top = 0.0;
-        values(p, t, z);
+      large = __any_sync(kAllLanes, !(top <= 12.f));
+    }
+    if constexpr (kTurns && kAs != kPlain) {
+      float z[kQElems];  // the inputs (both runs are turned from them)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = fmax(top, fabs(z[i]));
+      for (int i = 0; i < kQElems; ++i) z[i] = y[i];
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) top = fmax(top, __shfl_xor_sync(kAllLanes, top, o));
-        const int e = pow2_exponent(top);
-        top = fmax(top, double(kQMin));
-        float q[8];
-        if (p.pow2_scale) {
-          scale = power2(e);
-          const double step = double(power2(-e));
+      for (int j = 0; j < 2; ++j) {
+        if (!__any_sync(kAllLanes, in(p, j))) continue;
+        float other[8];  // what an element is turned with
 #pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = round_odd(z[i] * step);
-        } else {
-          scale = float(top / 448.0);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) q[i] = round_odd(z[i] * 448.0 / top);
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (kMode == kAdjacent) other[i] = z[8 * j + (i ^ 1)];
+          else if (p.rope_dim == 128) other[i] = z[8 * (j ^ 1) + i];
+          else other[i] = __shfl_xor_sync(kAllLanes, z[8 * j + i], p.rope_dim / 16);
         }
-        c = codes8(q, 1.f);
+        if (!in(p, j)) continue;
+        float c[8], s[8];
+        load_angles(p, j, c, s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = kMode == kAdjacent ? i / 2 : i;
+          y[8 * j + i] = turned(z[8 * j + i], c[k], other[i], kMode == kAdjacent && (i & 1) ? -s[k] : s[k]);
+        }
       }
     }
-    if (bad) {
-      scale = __uint_as_float(0x7FC00000u);
-      c = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-    }
-    return c;
   }
 };
 
-// kItems pairs of neighbouring groups per warp: half a warp a group.
+// The largest |y| of the lane's runs and of the group, NaN when one is.
+__device__ __forceinline__ float group_max(const float (&y)[kQElems], float (&run)[2]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    run[j] = abs_max(y[8 * j], y[8 * j + 1]);
+#pragma unroll
+    for (int i = 2; i < 8; ++i) run[j] = abs_max(run[j], y[8 * j + i]);
+  }
+  float m = abs_max(run[0], run[1]);
+#pragma unroll
+  for (int o = kQLanes / 2; o > 0; o >>= 1) m = abs_max(m, __shfl_xor_sync(kAllLanes, m, o));
+  return m;
+}
+
+// Element i (0 .. 15) of the lane whose first is k0 of output row `row`, from memory, as
+// a sum of two fp32 values.
+template <typename T, int kMode>
+__device__ __forceinline__ Wide wide_element(const qsfm_quantize_params& p, int row, int k0, int i) {
+  const int k = k0 + (i & 7) + (i >= 8 ? 64 : 0);
+  const int h = p.heads > 1 ? k / p.dim : 0, d = k - h * p.dim;
+  const size_t src = size_t(p.row_index != nullptr ? __ldg(p.row_index + row) : row);
+  const T* x = static_cast<const T*>(p.x) + src * p.x_row_stride + size_t(h) * p.x_head_stride;
+  const float v = float(x[d]);
+  if constexpr (kMode == kGated) {
+    const double g = float(static_cast<const T*>(p.gate)[src * p.gate_row_stride + size_t(h) * p.gate_head_stride + d]);
+    const double y = double(v) * (g / (1.0 + exp(-g)));
+    const float hi = float(y);
+    return {hi, float(y - double(hi))};
+  }
+  const int r = d - p.rope_offset;
+  if ((kMode == kAdjacent || kMode == kHalves) && r >= 0 && r < p.rope_dim) {
+    const int half = p.rope_dim / 2;
+    const bool second = kMode == kAdjacent ? (r & 1) != 0 : r >= half;
+    const int pair = kMode == kAdjacent ? r / 2 : second ? r - half : r;
+    const int apart = kMode == kAdjacent ? 1 : half;
+    const float* c = p.cos_sin + size_t(__ldg(p.positions + row)) * p.rope_dim + pair;
+    const float s = (p.inverse != 0) != second ? -c[half] : c[half];
+    return turned_wide(v, c[0], float(x[second ? d - apart : d + apart]), s);
+  }
+  return {v, 0.f};
+}
+
+// The elements of a lane that may hold the group's largest |y|, which is m in fp32.
+__device__ __forceinline__ uint32_t near_top(const float (&y)[kQElems], float m) {
+  uint32_t which = 0;
+#pragma unroll
+  for (int i = 0; i < kQElems; ++i)
+    which |= (__float_as_uint(y[i]) & 0x7FFFFFFFu) + 256u >= __float_as_uint(m) ? 1u << i : 0u;
+  return which;
+}
+
+// The largest |y| of the group among the elements that `which` has a bit for. The whole
+// warp calls it. (Out of line, as fix_borders(): a loop over single elements from memory,
+// so that a path that one warp in a hundred takes costs the others no registers and
+// little of the instruction cache.)
+template <typename T, int kMode>
+__device__ __noinline__ float2 wide_top(const qsfm_quantize_params& p, int row, int k0, uint32_t which) {
+  Wide top = {0.f, 0.f};
+  for (; which != 0; which &= which - 1) {
+    Wide v = wide_element<T, kMode>(p, row, k0, __ffs(which) - 1);
+    if (v.hi < 0.f) v = {-v.hi, -v.lo};
+    if (v.hi > top.hi || (v.hi == top.hi && v.lo > top.lo)) top = v;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int o = kQLanes / 2; o > 0; o >>= 1) {
+    const Wide v = {__shfl_xor_sync(kAllLanes, top.hi, o), __shfl_xor_sync(kAllLanes, top.lo, o)};
+    if (v.hi > top.hi || (v.hi == top.hi && v.lo > top.lo)) top = v;
+  }
+  return make_float2(top.hi, top.lo);
+}
+
+// Stores the codes of the lane's elements that `which` has a bit for, each one of two
+// neighbours, the lower of which (without its sign) is already stored.
+template <typename T, int kMode>
+__device__ __noinline__ void fix_borders(const qsfm_quantize_params& p, int row, int k0, uint32_t which, float num,
+                                         Wide den) {
+  uint8_t* codes = static_cast<uint8_t*>(p.codes) + size_t(row) * (size_t(p.heads) * p.dim) + k0;
+  for (; which != 0; which &= which - 1) {
+    const int i = __ffs(which) - 1;
+    uint8_t* at = codes + (i & 7) + (i >= 8 ? 64 : 0);
+    *at = uint8_t(nearer(*at, wide_element<T, kMode>(p, row, k0, i), num, den));
+  }
+}
+
+// A lane's codes of an item, and its group's scale. kMode is kPlain for items of which
+// nothing is turned, whatever they were loaded as.
+template <typename T, int kMode, typename I>
+__device__ __forceinline__ void finish(const qsfm_quantize_params& p, const QuantizeShape& s, const I& item,
+                                       size_t scale_at) {
+  constexpr bool kTurns = kMode == kAdjacent || kMode == kHalves;
+  float y[kQElems], run[2];
+  bool large = false;
+  item.template values<kMode>(p, y, large);
+  // At least the relative error of a quotient, in units of 2^-24: those of y (turned 3,
+  // gated 24 up to a gate of 12 and 118 up to 87), r (1 -+ error) 1; without powers of two
+  // also those of A (as many as of y), r 3, the product y r 1.
+  float error = kTurns ? 0x1p-20f : 0x1p-21f;
+  if constexpr (kMode == kGated) error = p.pow2_scale ? (large ? 0x1p-17f : 0x1p-19f) : (large ? 0x1p-16f : 0x1p-18f);
+  const uint32_t own = (item.live[0] ? 0xFFu : 0u) | (item.live[1] ? 0xFF00u : 0u);  // the lane's elements in the row
+  constexpr bool computed = kMode != kPlain;
+  const float m = group_max(y, run);
+  const bool bad = !(m < __uint_as_float(0x7F800000u));  // an element is not finite
+  const float a = fmaxf(bad ? 1.f : m, kQMin);
+  float scale, r;
+  uint32_t c[4];
+  if (p.pow2_scale) {
+    int e = pow2_exponent(m);
+    if (computed) {
+      // A next to 1.75 2^j, where e changes
+      const bool near = !bad && abs(int(__float_as_uint(m) & 0x7FFFFFu) - 0x600000) < 128;
+      if (__any_sync(kAllLanes, near)) {
+        const float2 top = wide_top<T, kMode>(p, item.row, item.k0, near ? near_top(y, m) & own : 0);
+        if (near) {
+          e = pow2_exponent(top.x);
+          if ((__float_as_uint(top.x) & 0x7FFFFFu) == 0x600000u && top.y > 0.f) e = min(max(e + 1, -100), 100);
+        }
+      }
+    }
+    scale = power2(e);
+    r = power2(-e);
+    if (!computed) codes16<false>(y, r, c);  // exact
+  } else {
+    scale = over448(a);
+    r = 0.875f * rcp_approx(a * 0x1p-9f);  // 448 / a; 512 / a is normal for every a
+    if constexpr (sizeof(T) == 2 && kMode != kGated) codes16<true>(y, r * (1.f + 0x1.8p-22f), c);
+  }
+  // the elements that lie next to a border by chance: those that are not an input over an input
+  uint32_t which = 0;
+  if (computed || (sizeof(T) == 4 && !p.pow2_scale)) {
+    uint32_t chance = 0xFFFFu;
+    if constexpr (kTurns) {
+      if (sizeof(T) == 2 || p.pow2_scale) {
+        // A is computed where a lane of the group holds it among its turned elements
+        const bool holds = (item.in(p, 0) && run[0] == m) || (item.in(p, 1) && run[1] == m);
+        const bool of_group = !p.pow2_scale && (__ballot_sync(kAllLanes, holds) >> (threadIdx.x & 24u) & 0xFFu) != 0;
+        chance = of_group ? 0xFFFFu : (item.in(p, 0) ? 0xFFu : 0u) | (item.in(p, 1) ? 0xFF00u : 0u);
+      }
+    }
+    uint32_t lo[4], hi[4];
+    codes16<false>(y, r * (1.f - error), lo);
+    codes16<false>(y, r * (1.f + error), hi);
+    const bool plain[2] = {(chance & 1) == 0, (chance & 0x100u) == 0};
+    if constexpr (kTurns) {
+      if (p.pow2_scale && (plain[0] || plain[1])) {
+        uint32_t exact[4];
+        codes16<false>(y, r, exact);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = exact[i];
+      }
+    }
+    bool differ = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (!plain[i / 2]) {
+        c[i] = lo[i];
+        differ = differ || lo[i] != hi[i];
+      }
+    if (__any_sync(kAllLanes, differ && !bad)) {
+#pragma unroll
+      for (int i = 0; i < kQElems; ++i)
+        which |= ((lo[i / 4] ^ hi[i / 4]) >> (8 * (i & 3)) & 0xFFu) != 0 ? chance & (1u << i) : 0u;
+      if (bad) which = 0;
+    }
+  }
+  if (bad) {
+    scale = __uint_as_float(0x7FC00000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = 0x7F7F7F7Fu;
+  }
+  uint8_t* to = static_cast<uint8_t*>(p.codes) + size_t(uint32_t(item.row)) * s.k + item.k0;
+  if (item.live[0]) *reinterpret_cast<uint2*>(to) = make_uint2(c[0], c[1]);
+  if (item.live[1]) *reinterpret_cast<uint2*>(to + 64) = make_uint2(c[2], c[3]);
+  if (item.row >= 0 && (threadIdx.x & (kQLanes - 1)) == 0) p.scale[scale_at] = scale;
+  if (kMode != kPlain || sizeof(T) == 4) {
+    which &= own;
+    if (__any_sync(kAllLanes, which != 0)) {
+      Wide den = {a, 0.f};
+      if (p.pow2_scale) {
+        den.hi = scale;
+      } else if (kMode != kPlain) {
+        const float2 top = wide_top<T, kMode>(p, item.row, item.k0, bad ? 0 : near_top(y, m) & own);
+        if (top.x >= kQMin) den = {top.x, top.y};
+      }
+      if (which != 0) fix_borders<T, kMode>(p, item.row, item.k0, which, p.pow2_scale ? 1.f : 448.f, den);
+      __syncwarp();
+    }
+  }
+}
+
+// kItems times four groups per warp: neighbours in a row or, where a part of each head is
+// turned, the same group of four heads in a row, so that what is turned is in warps of
+// its own.
 template <typename T, int kMode, int kItems>
-__global__ void __launch_bounds__(32 * kQWarps)
-    quantize_kernel(const qsfm_quantize_params p, const QuantizeShape s, int* fault) {
+__global__ void __launch_bounds__(32 * kQWarps, blocks_per_sm(kMode))
+    quantize_kernel(const __grid_constant__ qsfm_quantize_params p, const __grid_constant__ QuantizeShape s, int* fault) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, half = lane >> 4, sub = lane & 15;
-  const uint32_t warp = blockIdx.x * kQWarps + (threadIdx.x >> 5);
-  const uint32_t first = warp * (2 * kItems);
-  if (first >= s.total) return;  // the whole warp
+  const uint32_t quarter = (threadIdx.x & 31) >> 3;
+  const uint32_t first = (blockIdx.x * kQWarps + (threadIdx.x >> 5)) * kItems;
+  if (first >= s.units) return;  // the whole warp
   Item<T, kMode> item[kItems];
-#pragma unroll
-  for (int u = 0; u < kItems; ++u) item[u].load(p, s, first + 2 * u + half, sub, fault);
+  size_t scale_at[kItems];
 #pragma unroll
   for (int u = 0; u < kItems; ++u) {
-    float scale;
-    const uint2 c = item[u].codes(p, scale);
-    if (item[u].live)
-      *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.codes) + size_t(item[u].row) * s.k + item[u].k0) = c;
-    if (item[u].row >= 0 && sub == 0) p.scale[first + 2 * u + half] = scale;
+    if constexpr (Item<T, kMode>::kTurns) {
+      const uint32_t four = s.groups_of.div(first + u), g = first + u - four * s.groups_of.d;
+      const uint32_t head = 4 * four + quarter, row = s.heads_of.div(head), h = head - row * uint32_t(p.heads);
+      scale_at[u] = size_t(head) * s.groups_of.d + g;
+      item[u].load(p, s, first + u < s.units ? row : 0xffffffffu, h, int(g) * kQGroup, int(h) * p.dim + int(g) * kQGroup, fault);
+    } else {
+      const uint32_t f = 4 * (first + u) + quarter, row = s.groups_of.div(f), g = f - row * s.groups_of.d;
+      const uint32_t h = p.heads > 1 ? s.heads_of.div(g) : 0;
+      scale_at[u] = f;
+      item[u].load(p, s, row, h, int(g) * kQGroup - int(h) * p.dim, int(g) * kQGroup, fault);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kItems; ++u) {
+    item[u].check(p, fault);
+    if (Item<T, kMode>::kTurns && !__any_sync(kAllLanes, item[u].in(p, 0) || item[u].in(p, 1)))
+      finish<T, kPlain>(p, s, item[u], scale_at[u]);
+    else
+      finish<T, kMode>(p, s, item[u], scale_at[u]);
   }
 }
 
 template <typename T, int kMode>
-cudaError_t launch_mode(const qsfm_quantize_params& p, const QuantizeShape& s, int* fault, cudaStream_t stream) {
-  // few groups: one pair a warp, so that they spread over the SMs; many: four, for
-  // the bytes in flight
-  const uint32_t pairs = (s.total + 1) / 2;
-  if (pairs <= 152 * 32) {
-    return launch_after_predecessor(quantize_kernel<T, kMode, 1>, dim3((pairs + kQWarps - 1) / kQWarps),
-                                    dim3(32 * kQWarps), 0, stream, p, s, fault);
+cudaError_t launch_mode(const qsfm_quantize_params& p, int* fault, cudaStream_t stream) {
+  QuantizeShape s;
+  s.k = p.heads * p.dim;
+  const uint32_t groups = uint32_t((s.k + kQGroup - 1) / kQGroup), of_head = uint32_t((p.dim + kQGroup - 1) / kQGroup);
+  if (Item<T, kMode>::kTurns) {
+    s.groups_of.set(of_head);
+    s.heads_of.set(uint32_t(p.heads));
+    s.units = uint32_t((uint64_t(p.rows) * uint32_t(p.heads) + 3) / 4) * of_head;
+  } else {
+    s.groups_of.set(groups);
+    s.heads_of.set(of_head);
+    s.units = (uint32_t(p.rows) * groups + 3) / 4;
   }
-  const uint32_t warps = (pairs + 3) / 4;
-  return launch_after_predecessor(quantize_kernel<T, kMode, 4>, dim3((warps + kQWarps - 1) / kQWarps),
+  // few groups: four a warp, so that they spread over the SMs; many: 64 bytes of the
+  // inputs a lane, for the bytes in flight
+  constexpr int kItems = sizeof(T) == 4 || kMode == kGated ? 1 : 2;
+  if (kItems == 1 || s.units <= 152 * 32)
+    return launch_after_predecessor(quantize_kernel<T, kMode, 1>, dim3((s.units + kQWarps - 1) / kQWarps),
+                                    dim3(32 * kQWarps), 0, stream, p, s, fault);
+  const uint32_t warps = (s.units + kItems - 1) / kItems;
+  return launch_after_predecessor(quantize_kernel<T, kMode, kItems>, dim3((warps + kQWarps - 1) / kQWarps),
                                   dim3(32 * kQWarps), 0, stream, p, s, fault);
 }
 
 template <typename T>
-cudaError_t launch_type(const qsfm_quantize_params& p, const QuantizeShape& s, int* fault, cudaStream_t stream) {
-  if (p.gate != nullptr) return launch_mode<T, kGated>(p, s, fault, stream);
-  if (p.rope_dim > 0) return launch_mode<T, kRotate>(p, s, fault, stream);
-  return launch_mode<T, kPlain>(p, s, fault, stream);
+cudaError_t launch_type(const qsfm_quantize_params& p, int* fault, cudaStream_t stream) {
+  if (p.gate != nullptr) return launch_mode<T, kGated>(p, fault, stream);
+  if (p.rope_dim > 0 && p.interleaved) return launch_mode<T, kAdjacent>(p, fault, stream);
+  if (p.rope_dim > 0) return launch_mode<T, kHalves>(p, fault, stream);
+  return launch_mode<T, kPlain>(p, fault, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_quantize(const qsfm_quantize_params& p, int* fault, cudaStream_t stream) {
-  QuantizeShape s;
-  s.k = p.heads * p.dim;
-  s.groups = uint32_t((s.k + kQGroup - 1) / kQGroup);
-  s.total = uint32_t(p.rows) * s.groups;
-  s.per_row.set(s.groups);
-  s.per_head.set(p.heads > 1 ? uint32_t(p.dim / kQGroup) : 1);
   switch (p.in_type) {
-    case QSFM_BF16: return launch_type<__nv_bfloat16>(p, s, fault, stream);
-    case QSFM_F16: return launch_type<__half>(p, s, fault, stream);
-    default: return launch_type<float>(p, s, fault, stream);
+    case QSFM_BF16: return launch_type<__nv_bfloat16>(p, fault, stream);
+    case QSFM_F16: return launch_type<__half>(p, fault, stream);
+    default: return launch_type<float>(p, fault, stream);
   }
 }
 

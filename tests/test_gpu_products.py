@@ -13,9 +13,10 @@ from oracle import qsfm_oracle as O
 pytestmark = pytest.mark.gpu
 
 #: Scales against the formula's, relative: their own rounding (1 unit of 2^-24),
-#: and those of a computed A: rotated 3, gated 9 (expf 2, 1 + e 1, the division
-#: by it 4, two products).
-SCALE_REL = {"plain": 2.0 ** -24, "rotate": 4 * 2.0 ** -24, "gated": 10 * 2.0 ** -24}
+#: and those of a computed A: rotated 3, gated 9 + 1.25 |gate| (exp's argument
+#: 1.25 |gate|, its result 4, 1 + e 1, the reciprocal 2, two products), where
+#: the gates of the largest elements are below 12.
+SCALE_REL = {"plain": 2.0 ** -24, "rotate": 4 * 2.0 ** -24, "gated": 25 * 2.0 ** -24}
 
 
 @pytest.fixture(scope="module", autouse=True)
