@@ -5,47 +5,46 @@
 //
 // The scales differ from block to block of K, so a block's products (tcgen05.mma
 // kind::f8f6f4, fp32 accumulators in tensor memory) are read out, multiplied by their
-// two scales and added to sums in registers. The matrix is the MMA's M side (128 of its
-// rows, one scale), the rows of a are its N side (kCols of them at most): single tokens
-// waste none of the matrix's stream, and the N of an instruction is what the tile has.
-// The tile's matrix rows are tensor-memory lanes, a thread's sums those of one matrix
-// row with every row of a.
+// two scales and added to sums in registers. This file's kernel is that of few rows (of a
+// group, on average; qsfm_matmul_pair.cu has the other). The matrix is the MMA's M side
+// (128 of its rows, one scale), the rows of a are its N side (kCols of them at most):
+// single tokens waste none of the matrix's stream, and the N of an instruction is what
+// the tile has. Tensor-memory lanes are the tile's matrix rows, a thread's sums those of
+// one matrix row with rows of a.
 //
 // Roles: a warp that loads (TMA, 128-byte swizzle), one that issues MMAs, one that
-// copies the scales of the tile's rows (cp.async), 4 or 8 that add up and store. A
-// CTA walks tiles in turn; the rows of a group of rows fastest, then the matrix's.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
+// copies the scales of the tile's rows (cp.async), 4 or 8 that add up and store. A CTA
+// walks tiles in turn; the rows of a group fastest, then the matrix's. Where the tiles
+// leave SMs without work, a tile's blocks of K are split over a cluster, whose CTAs
+// exchange their sums through distributed shared memory.
+#include <atomic>
 
-#include <mutex>
-
-#include "qsfm_device.cuh"
-#include "qsfm_internal.h"
+#include "qsfm_matmul_common.cuh"
+#ifndef MM_PAIR
+#define MM_PAIR (rows > 128)
+#endif
 
 namespace qsfm {
 namespace {
 
 constexpr int kMmRows = 128;        // matrix rows of a tile
-constexpr int kMmK = 128;           // bytes of K per stage: one block of scales
-constexpr int kMmMaxGroups = 1024;
-constexpr long long kMmMaxTiles = (1ll << 30) + 1;  // counted at most
 constexpr int kMmScaleSlots = 8;
 constexpr int kMmMaxStages = 12;
-constexpr uint64_t kMmTimeoutNs = 1000000000ull;
-constexpr uint32_t kMmSmemMax = 227 * 1024;
 
 template <int kCols>
 struct MmConfig {
-  static constexpr int kEpiWarps = kCols > 128 ? 8 : 4;
-  static constexpr int kWarpCols = kCols > 128 ? kCols / 2 : kCols;  // columns of an adding warp
-  static constexpr int kThreads = 32 * (kEpiWarps + 3);
-  static constexpr int kBoxRows = kCols < 32 ? kCols : 32;           // rows of a per copy
+  static constexpr int kLogCols = kCols == 16 ? 4 : kCols == 32 ? 5 : kCols == 64 ? 6 : kCols == 128 ? 7 : 8;
+  static constexpr int kEpiWarps = kCols >= 64 ? 8 : 4;
+  static constexpr int kWarpCols = kCols >= 64 ? kCols / 2 : kCols;  // columns of an adding warp
+  static constexpr int kThreads = 32 * (kEpiWarps + 4);
+  // 128 sums a thread and 64 products on their way: registers that the other warps give
+  static constexpr bool kShareRegs = kCols == 256;
+  static constexpr int kAddRegs = 216, kOtherRegs = 72, kLaunchRegs = 168;
+  static_assert(256 * kAddRegs + 128 * kOtherRegs <= 384 * kLaunchRegs, "registers");
+  static constexpr int kBoxRows = kCols < 32 ? kCols : 32;  // rows of a per copy
   static constexpr uint32_t kStage = kMmRows * kMmK + kCols * kMmK;
   static constexpr uint32_t kScaleSlot = kCols * 4;
-  // after the stages: scale slots, group prefix, barriers, the rest
+  // after the stages: scale slots, group prefix, barriers
   static constexpr uint32_t kTail = kMmScaleSlots * kScaleSlot + (kMmMaxGroups + 4) * 4 + 512;
   static constexpr int kFit = int((kMmSmemMax - 1024 - kTail) / kStage);
   static constexpr int kStages = kFit < kMmMaxStages ? kFit : kMmMaxStages;
@@ -54,108 +53,23 @@ struct MmConfig {
   static constexpr uint32_t kBarAt = (kPrefixAt + (kMmMaxGroups + 4) * 4 + 7) & ~7u;
   static constexpr uint32_t kSmem = kBarAt + 512 + 1024;
   static constexpr uint32_t kTmemCols = 2 * kCols < 32 ? 32 : 2 * kCols;
-  static_assert(kSmem <= kMmSmemMax, "shared memory");
+  static_assert(kSmem <= kMmSmemMax && kCols * kMmRows * 4 <= kScaleAt, "shared memory");
 };
 
 // barriers
 constexpr int kMbFull = 0, kMbEmpty = kMmMaxStages, kMbSFull = 2 * kMmMaxStages, kMbSEmpty = kMbSFull + kMmScaleSlots,
               kMbTFull = kMbSEmpty + kMmScaleSlots, kMbTEmpty = kMbTFull + 2, kMbDrain = kMbTEmpty + 2,
               kMbCount = kMbDrain + 1;
-static_assert(kMbCount * 8 + 16 <= 512, "barriers");
+static_assert(kMbCount * 8 + 8 <= 512, "barriers");
 
 struct MmShape {
-  int kb;        // blocks of K
-  int col_tiles; // tiles of the matrix's rows
+  int kb;         // blocks of K
+  int col_tiles;  // tiles of the matrix's rows
+  int split;      // log2 of the CTAs of a cluster, which share a tile's blocks of K
 };
 
-struct MmSmem {
-  uint32_t base;
-  uint8_t* ptr;
-  uint32_t bars;  // offset of the barriers
-  __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(ptr + bars) + i; }
-  __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + bars + kMbCount * 8); }
-  __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(ptr + bars + kMbCount * 8 + 4); }
-};
-
-__device__ __forceinline__ bool mm_wait(const MmSmem& sm, int bar, uint32_t parity, int* fault) {
-  if (mbar_wait_bounded(sm.bar(bar), parity, sm.abort_flag(), kMmTimeoutNs)) return true;
-  if (!*sm.abort_flag()) {
-    *sm.abort_flag() = 1;
-    atomicOr(fault, QSFM_FAULT_TIMEOUT);
-  }
-  return false;
-}
-
-// Every lane waits (on an open barrier one test), the warp goes on together.
-__device__ __forceinline__ bool mm_warp_wait(const MmSmem& sm, int bar, uint32_t parity, int* fault) {
-  const bool ok = mm_wait(sm, bar, parity, fault);
-  return __all_sync(0xffffffffu, ok) != 0;
-}
-
-__device__ __forceinline__ void mm_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
-// 4 bytes to shared memory without a register, zeros where `bytes` is 0.
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-// One of the barrier's arrivals, once the thread's copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// D (+)= A B^T of 32 e4m3 of K, operands K-major with the 128-byte swizzle (8-row groups
-// of 1 KB). The whole warp runs the loop around it and one elected lane issues, so the
-// descriptors stay in uniform registers.
-constexpr uint32_t kMmDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // group stride, version, swizzle
-template <uint32_t kOff>
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 a, b;\n add.u32 x, %1, %6;\n add.u32 y, %2, %6;\n"
-      " mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
-      " setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kMmDescHigh), "n"(kOff)
-      : "memory");
-}
-__device__ __forceinline__ void mm_commit(uint64_t* bar) {
-  asm volatile(
-      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
-      : "memory");
-}
-__device__ __forceinline__ uint32_t mm_desc(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | ((16u >> 4) << 16); }
-
-// (s0, s1) += (c0, c1) * (f0, f1), each as fmaf rounds.
-__device__ __forceinline__ void mm_fma2(float& s0, float& s1, float c0, float c1, float f0, float f1) {
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 d, {%0, %1};\n"
-      " fma.rn.f32x2 d, a, b, d;\n mov.b64 {%0, %1}, d;\n}"
-      : "+f"(s0), "+f"(s1)
-      : "f"(c0), "f"(c1), "f"(f0), "f"(f1));
-}
-
-// One tile: rows row0 .. row0 + cols - 1 of a, matrix rows n0 .. of group g.
-struct MmTile {
-  int g, n0, row0, cols;
-};
-
-// Rows of group g, cut to what there is.
-__device__ __forceinline__ void group_rows(const qsfm_matmul_params& p, int g, int& lo, int& hi, bool& bad) {
-  if (p.cu_rows == nullptr) {
-    lo = 0;
-    hi = p.rows;
-    bad = false;
-    return;
-  }
-  const int a = __ldg(p.cu_rows + g), b = __ldg(p.cu_rows + g + 1);
-  bad = a < 0 || b < a || b > p.rows;
-  lo = min(max(a, 0), p.rows);
-  hi = max(lo, min(b, p.rows));
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // The CTA's walk over the tiles: prefix[g] tiles lie before group g's.
@@ -268,10 +182,73 @@ __device__ void mm_scales(const qsfm_matmul_params& p, const MmShape& s, const M
 }
 
 // ------------------------------------------------------------- sums and output
-__device__ __forceinline__ void mm_store(const qsfm_matmul_params& p, size_t at, float v) {
-  if (p.out_type == QSFM_BF16) static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16(v);
-  else if (p.out_type == QSFM_F16) static_cast<__half*>(p.out)[at] = __float2half(v);
-  else static_cast<float*>(p.out)[at] = v;
+// Adds up the blocks b0 .. b1 - 1 of a tile in registers; false after a timeout. A round
+// takes up to 64 columns out of tensor memory at once (a load and its wait take 200 cycles
+// and more, whatever its size).
+template <int kCols>
+__device__ __forceinline__ bool mm_add(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, const MmTile& t,
+                                       int b0, int b1, uint32_t tmem, uint32_t& buf, uint32_t& tpar, uint32_t& slot,
+                                       uint32_t& spar, float (&acc)[MmConfig<kCols>::kWarpCols], int* fault) {
+  using C = MmConfig<kCols>;
+  constexpr int kN = C::kWarpCols, kRound = kN < 64 ? kN : 64, kPart = kN < 32 ? kN : 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int quarter = warp & 3, c0 = (warp >> 2) * kN;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) acc[i] = 0.f;
+  const int live = t.cols - c0;  // columns of this warp
+  const float* wsp = p.w_scale + (size_t(t.g) * s.col_tiles + t.n0 / kMmRows) * s.kb;
+  // two blocks ahead, into the register that the block of the same parity is done with
+  // (a copy from register to register would wait for the load)
+  float wsr[2] = {b0 < b1 ? __ldg(wsp + b0) : 0.f, b0 + 1 < b1 ? __ldg(wsp + b0 + 1) : 0.f};
+  for (int bb = b0; bb < b1; bb += 2) {
+#pragma unroll
+   for (int par2 = 0; par2 < 2; ++par2) {
+    const int b = bb + par2;
+    if (b >= b1) break;
+    const float ws = wsr[par2];
+    if (b + 2 < b1) wsr[par2] = __ldg(wsp + b + 2);
+    if (!mm_warp_wait(sm, kMbSFull + slot, spar, fault)) return false;
+    if (!mm_warp_wait(sm, kMbTFull + buf, tpar, fault)) return false;
+    tc_fence_after();
+    const float4* sc = reinterpret_cast<const float4*>(sm.ptr + C::kScaleAt + slot * C::kScaleSlot) + c0 / 4;
+    const uint32_t at = tmem + buf * kCols + c0 + (uint32_t(32 * quarter) << 16);
+#pragma unroll
+    for (int c = 0; c < kN; c += kRound) {
+      float v[kRound];
+#pragma unroll
+      for (int h = 0; h < kRound; h += kPart)
+        if (c + h < live) {
+          if constexpr (kPart == 32) tmem_ld32(at + c + h, v + h);
+          else tmem_ld16(at + c + h, v + h);
+        }
+      tmem_ld_wait();
+      if (c + kRound >= kN) {  // the accumulator is free as soon as the last round has it
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sm.bar(kMbTEmpty + buf));
+      }
+#pragma unroll
+      for (int h = 0; h < kRound; h += kPart)
+        if (c + h < live) {
+#pragma unroll
+          for (int i = h; i < h + kPart; i += 4) {
+            const float4 f = sc[(c + i) / 4];
+            mm_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f.x * ws, f.y * ws);
+            mm_fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f.z * ws, f.w * ws);
+          }
+        }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(sm.bar(kMbSEmpty + slot));
+    buf ^= 1;
+    tpar ^= buf == 0;
+    if (++slot == kMmScaleSlots) {
+      slot = 0;
+      spar ^= 1;
+    }
+   }
+  }
+  return true;
 }
 
 template <int kCols>
@@ -280,57 +257,46 @@ __device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSm
   using C = MmConfig<kCols>;
   constexpr int kN = C::kWarpCols;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, c0 = (warp >> 2) * kN;
+  const int row = 32 * (warp & 3) + lane, c0 = (warp >> 2) * kN;
   uint32_t buf = 0, tpar = 0, slot = 0, spar = 0;
   MmTile t;
-  while (walk.next(p, s, t)) {
-    float acc[kN];
+  float acc[kN];
+  if (s.split == 0) {
+    while (walk.next(p, s, t)) {
+      if (!mm_add<kCols>(p, s, sm, t, b0, b1, tmem, buf, tpar, slot, spar, acc, fault)) return;
+      if (t.n0 + row < p.n) {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) acc[i] = 0.f;
-    const int live = t.cols - c0;  // columns of this warp
-    const float* wsp = p.w_scale + (size_t(t.g) * s.col_tiles + t.n0 / kMmRows) * s.kb;
-    float ws = b0 < b1 ? __ldg(wsp + b0) : 0.f;
-    for (int b = b0; b < b1; ++b) {
-      const float wnext = b + 1 < b1 ? __ldg(wsp + b + 1) : 0.f;
-      if (!mm_warp_wait(sm, kMbSFull + slot, spar, fault)) return;
-      if (!mm_warp_wait(sm, kMbTFull + buf, tpar, fault)) return;
-      tc_fence_after();
-      const float4* sc = reinterpret_cast<const float4*>(sm.ptr + C::kScaleAt + slot * C::kScaleSlot) + c0 / 4;
-      const uint32_t at = tmem + buf * kCols + c0 + (uint32_t(32 * quarter) << 16);
-#pragma unroll
-      for (int c = 0; c < kN; c += 16) {
-        if (c < live) {
-          float v[16];
-          tmem_ld16(at + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 f = sc[(c + i) / 4];
-            mm_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f.x * ws, f.y * ws);
-            mm_fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f.z * ws, f.w * ws);
-          }
-        }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(sm.bar(kMbTEmpty + buf));
-        mbar_arrive(sm.bar(kMbSEmpty + slot));
-      }
-      ws = wnext;
-      buf ^= 1;
-      tpar ^= buf == 0;
-      if (++slot == kMmScaleSlots) {
-        slot = 0;
-        spar ^= 1;
+        for (int c = 0; c < kN; ++c)
+          if (c0 + c < t.cols) mm_store(p, size_t(t.row0 + c0 + c) * p.out_row_stride + t.n0 + row, acc[c]);
       }
     }
-    const int n = t.n0 + 32 * quarter + lane;
-    if (n < p.n) {
+    return;
+  }
+  // The cluster's one tile: CTA r adds up the columns r w .. r w + w - 1 of all, w = kCols /
+  // CTAs, in the order of the CTAs. Their sums take the place of the operands, which every
+  // CTA of the cluster is through with at the first barrier.
+  bool ok = walk.next(p, s, t);
+  if (ok) ok = mm_add<kCols>(p, s, sm, t, b0, b1, tmem, buf, tpar, slot, spar, acc, fault);
+  const uint32_t rank = cluster_rank();
+  const int shift = C::kLogCols - s.split, w = 1 << shift;
+  cluster_sync();
+  if (ok) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c)
-        if (c < live) mm_store(p, size_t(t.row0 + c0 + c) * p.out_row_stride + n, acc[c]);
+    for (int c = 0; c < kN; ++c) {
+      const int col = c0 + c;
+      if (col < t.cols)
+        st_cluster(in_cta(sm.base + 4 * (((rank << shift) + (col & (w - 1))) * kMmRows + row), uint32_t(col >> shift)), acc[c]);
     }
+  }
+  cluster_sync();
+  if (!ok || t.n0 + row >= p.n) return;
+  const float* sums = reinterpret_cast<const float*>(sm.ptr) + row;
+  for (int c = warp >> 2; c < w; c += C::kEpiWarps / 4) {
+    const int col = int(rank << shift) + c;
+    if (col >= t.cols) break;
+    float v = sums[c * kMmRows];
+    for (int r = 1; r < 1 << s.split; ++r) v += sums[((r << shift) + c) * kMmRows];
+    mm_store(p, size_t(t.row0 + col) * p.out_row_stride + t.n0 + row, v);
   }
 }
 
@@ -345,7 +311,7 @@ __global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
   sm.base = (raw + 1023u) & ~1023u;
   sm.ptr = mm_smem + (sm.base - raw);
   sm.bars = C::kBarAt;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = tid >> 5;
   int* prefix = reinterpret_cast<int*>(sm.ptr + C::kPrefixAt);
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
@@ -367,29 +333,7 @@ __global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
   if (warp == C::kEpiWarps + 1) tmem_alloc(sm.tmem_slot(), C::kTmemCols);
   grid_dependency_wait();
   grid_launch_dependents();
-  if (warp == 0) {  // tiles before each group
-    long long run = 0;  // overlapping groups of a bad cu_rows may count more than there can be
-    const auto cut = [](long long v) { return int(v < kMmMaxTiles ? v : kMmMaxTiles); };
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
-      long long n = 0;
-      if (g0 + lane < p.groups) {
-        int lo, hi;
-        bool bad;
-        group_rows(p, g0 + lane, lo, hi, bad);
-        if (bad && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_GROUP_ROWS);
-        n = (long long)((hi - lo + kCols - 1) / kCols) * s.col_tiles;
-      }
-      long long sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += up;
-      }
-      if (g0 + lane < p.groups) prefix[g0 + lane] = cut(run + sum - n);
-      run += __shfl_sync(0xffffffffu, sum, 31);
-    }
-    if (lane == 0) prefix[p.groups] = cut(run);
-  }
+  if (warp == 0) count_tiles(p, kCols, s.col_tiles, prefix, fault);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -397,10 +341,15 @@ __global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
   MmWalk<kCols> walk;
   walk.prefix = prefix;
   walk.g = 0;
-  walk.at = int(blockIdx.x);
-  walk.step = int(gridDim.x);
+  walk.at = int(blockIdx.x >> s.split);
+  walk.step = int(gridDim.x >> s.split);
   walk.total = prefix[p.groups];
-  const int b0 = 0, b1 = s.kb;
+  const int part = int(blockIdx.x) & ((1 << s.split) - 1);
+  const int b0 = int(int64_t(s.kb) * part >> s.split), b1 = int(int64_t(s.kb) * (part + 1) >> s.split);
+  if constexpr (C::kShareRegs) {
+    if (warp < C::kEpiWarps) mm_more_registers<C::kAddRegs>();
+    else mm_fewer_registers<C::kOtherRegs>();
+  }
   if (warp < C::kEpiWarps) {
     mm_sum<kCols>(p, s, sm, walk, b0, b1, tmem, fault);
   } else if (warp == C::kEpiWarps) {
@@ -411,12 +360,16 @@ __global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
     mm_commit(sm.bar(kMbDrain));
     volatile int never = 0;
     if (!mbar_wait_poll(smem_u32(sm.bar(kMbDrain)), 0, &never, kMmTimeoutNs)) atomicOr(fault, QSFM_FAULT_TIMEOUT);
-  } else {
+  } else if (warp == C::kEpiWarps + 2) {
     mm_scales<kCols>(p, s, sm, walk, b0, b1, fault);
+  }
+  __syncwarp();
+  if (s.split > 0 && warp >= C::kEpiWarps) {  // (the adding warps' are in mm_sum)
+    cluster_sync();
+    cluster_sync();
   }
   // after an abort copies may still be on their way into this CTA's shared memory:
   // a millisecond is far more than they take
-  __syncwarp();
   if (warp == C::kEpiWarps && *sm.abort_flag())
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   __syncwarp();
@@ -429,53 +382,43 @@ __global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
 }
 
 // ------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    cudaDriverEntryPointQueryResult qres;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qres) ==
-            cudaSuccess &&
-        qres == cudaDriverEntryPointSuccess)
-      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return encode;
-}
-
-// Bytes [planes, rows, k] in boxes of box_rows x 128, what lies outside read as zero.
-// (A stride of a dimension of length 1 is not used: the encoder still wants it to be a
-// multiple of 16 that is not below the extent within.)
-cudaError_t make_map(const void* base, int k, int rows, int planes, long long row_stride, long long plane_stride,
-                     int box_rows, bool is3d, CUtensorMap* map) {
-  const auto encode = tensor_map_encoder();
-  if (encode == nullptr) return cudaErrorNotSupported;
-  if (rows <= 1) row_stride = (k + 15) & ~15;
-  if (planes <= 1) plane_stride = row_stride * rows;
-  const cuuint64_t dims[3] = {cuuint64_t(k), cuuint64_t(rows), cuuint64_t(planes)};
-  const cuuint64_t strides[2] = {cuuint64_t(row_stride), cuuint64_t(plane_stride)};
-  const cuuint32_t box[3] = {kMmK, cuuint32_t(box_rows), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, is3d ? 3 : 2, const_cast<void*>(base), dims, strides,
-                            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int kCols>
 cudaError_t launch_cols(const qsfm_matmul_params& p, const MmShape& s, int sms, int* fault, cudaStream_t stream) {
   using C = MmConfig<kCols>;
   cudaError_t e = cudaFuncSetAttribute(matmul_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
   if (e != cudaSuccess) return e;
+  if constexpr (C::kShareRegs) {
+    // with fewer registers than the split counts on, the adding warps would wait forever
+    static std::atomic<bool> enough{false};
+    if (!enough.load(std::memory_order_relaxed)) {
+      cudaFuncAttributes attr;
+      if ((e = cudaFuncGetAttributes(&attr, matmul_kernel<kCols>)) != cudaSuccess) return e;
+      if (attr.numRegs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
+      enough.store(true, std::memory_order_relaxed);
+    }
+  }
   CUtensorMap amap, wmap;
   if ((e = make_map(p.a, p.k, p.rows, 1, p.a_row_stride, 0, C::kBoxRows, false, &amap)) != cudaSuccess) return e;
   if ((e = make_map(p.w, p.k, p.n, p.groups, p.w_row_stride, p.w_group_stride, kMmRows, true, &wmap)) != cudaSuccess)
     return e;
   // at most this many tiles: every group but one may add a tile that is not full
-  const long long most = ((long long)p.rows / kCols + (p.groups < p.rows ? p.groups : p.rows)) * s.col_tiles;
-  const int grid = int(most < sms ? most : sms);
-  return launch_after_predecessor(matmul_kernel<kCols>, dim3(grid), dim3(C::kThreads), C::kSmem, stream, p, s, fault,
-                                  amap, wmap);
+  const long long most = p.cu_rows == nullptr
+                             ? (long long)((p.rows + kCols - 1) / kCols) * s.col_tiles
+                             : ((long long)p.rows / kCols + (p.groups < p.rows ? p.groups : p.rows)) * s.col_tiles;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(s.split > 0 ? unsigned(most << s.split) : unsigned(most < sms ? most : sms));
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1u << s.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = s.split > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<kCols>, p, s, fault, amap, wmap);
 }
 
 }  // namespace
@@ -488,12 +431,29 @@ cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t 
   MmShape s;
   s.kb = (p.k + kMmK - 1) / kMmK;
   s.col_tiles = (p.n + kMmRows - 1) / kMmRows;
+  s.split = 0;
   const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
-  if (rows <= 16) return launch_cols<16>(p, s, sms, fault, stream);
-  if (rows <= 32) return launch_cols<32>(p, s, sms, fault, stream);
-  if (rows <= 64) return launch_cols<64>(p, s, sms, fault, stream);
-  if (rows <= 128) return launch_cols<128>(p, s, sms, fault, stream);
-  return launch_cols<256>(p, s, sms, fault, stream);
+  if (MM_PAIR) return launch_matmul_pair(p, sms, fault, stream);
+  int cols = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+#ifdef MM_COLS
+  cols = MM_COLS;
+#endif
+  // the tiles of one group are known here: where they leave SMs without work, the
+  // blocks of K are split, down to two blocks a CTA
+  if (p.cu_rows == nullptr) {
+    const long long tiles = (long long)((p.rows + cols - 1) / cols) * s.col_tiles;
+    while (s.split < 3 && (tiles << (s.split + 1)) <= sms && s.kb >= 4 << s.split) ++s.split;
+#ifdef MM_SPLIT
+    s.split = MM_SPLIT;
+#endif
+  }
+  switch (cols) {
+    case 16: return launch_cols<16>(p, s, sms, fault, stream);
+    case 32: return launch_cols<32>(p, s, sms, fault, stream);
+    case 64: return launch_cols<64>(p, s, sms, fault, stream);
+    case 128: return launch_cols<128>(p, s, sms, fault, stream);
+    default: return launch_cols<256>(p, s, sms, fault, stream);
+  }
 }
 
 }  // namespace qsfm
