@@ -21,8 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libqsfm.so")
 SOURCES = ["qsfm_api.cu", "qsfm_attention.cu", "qsfm_attention4.cu", "qsfm_aux.cu", "qsfm_noalloc.cu",
-           "qsfm_indexer.cu", "qsfm_rows.cu", "qsfm_tables.cu", "qsfm_quantize.cu", "qsfm_matmul.cu",
-           "qsfm_matmul_pair.cu"]
+           "qsfm_indexer.cu", "qsfm_rows.cu", "qsfm_tables.cu", "qsfm_quantize.cu", "qsfm_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "-I", INCLUDE, "-I", CSRC,
          "--expt-relaxed-constexpr"]

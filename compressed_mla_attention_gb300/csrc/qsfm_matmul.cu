@@ -5,114 +5,345 @@
 //
 // The scales differ from block to block of K, so a block's products (tcgen05.mma
 // kind::f8f6f4, fp32 accumulators in tensor memory) are read out, multiplied by their
-// two scales and added to sums in registers. This file's kernel is that of few rows (of a
-// group, on average; qsfm_matmul_pair.cu has the other). The matrix is the MMA's M side
-// (128 of its rows, one scale), the rows of a are its N side (kCols of them at most):
-// single tokens waste none of the matrix's stream, and the N of an instruction is what
-// the tile has. Tensor-memory lanes are the tile's matrix rows, a thread's sums those of
-// one matrix row with rows of a.
+// two scales and added to sums in registers. Rows of a are the tensor-memory lanes: a
+// thread's 128 sums are those of one row with 128 matrix rows, which have one scale, so a
+// block's factor is one number a thread.
 //
-// Roles: a warp that loads (TMA, 128-byte swizzle), one that issues MMAs, one that
-// copies the scales of the tile's rows (cp.async), 4 or 8 that add up and store. A CTA
-// walks tiles in turn; the rows of a group fastest, then the matrix's. Where the tiles
-// leave SMs without work, a tile's blocks of K are split over a cluster, whose CTAs
-// exchange their sums through distributed shared memory.
-#include <atomic>
+// A tile is 128 rows of a by 256 matrix rows, or, where a group has more than 128 rows on
+// average, 256 by 256 of a pair of CTAs (cta_group::2): each loads its own 128 rows of a
+// and half of the matrix's, 32 KB a block of K instead of 48. With few rows the matrix's
+// bytes are what a product has to read, and a CTA has 128 KB of them on their way; rows of
+// a that are not there are not loaded, and warps without rows do not add.
+//
+// Per CTA: a warp that loads (TMA, 128-byte swizzle), two that issue MMAs (of a pair's
+// first CTA alone), one that copies scales, eight that add up and store. A block's MMAs
+// take 512 cycles; meanwhile the eight warps read the previous one's products out of
+// tensor memory and add them up. What it took (cycles a block of a pair, K = 8192):
+//  * a release of an accumulator at the cluster's scope waits for all the thread's memory
+//    operations: 2800 -> 1250 without;
+//  * single FMAs instead of pairs (fma.rn.f32x2: 64 a thread took longer than 128): 960;
+//  * scales through shared memory, eight blocks at a time, instead of 4-byte loads: 770.
+// At 770 the GPU is at its power limit (1660 MHz of 2070 in a loop): 8192 x 8192 x 8192 in
+// 385 us (2.86 PFLOP/s), 420 in a loop; a library's product of the same codes without
+// scales 330 in a loop. Tried: tiles of 192 matrix rows (one round of loads from tensor
+// memory, an earlier release) 460; two MMAs of 128 matrix rows each 500, before the last
+// step.
+//
+// A CTA (or pair) walks tiles in turn, eight row tiles of a group before the next of the
+// matrix's. Where the tiles of one group leave SMs without work, a tile's blocks of K are
+// split over a cluster, whose CTAs exchange their sums through distributed shared memory
+// and add them in the order of the CTAs.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
 
-#include "qsfm_matmul_common.cuh"
-#ifndef MM_PAIR
-#define MM_PAIR (rows > 128)
-#endif
+#include <atomic>
+#include <mutex>
+
+#include "qsfm_device.cuh"
+#include "qsfm_internal.h"
 
 namespace qsfm {
 namespace {
 
-constexpr int kMmRows = 128;        // matrix rows of a tile
-constexpr int kMmScaleSlots = 8;
-constexpr int kMmMaxStages = 12;
+constexpr int kMmK = 128;         // bytes of K per stage: one block of scales
+constexpr int kChunk = 16;        // columns that a part of a split tile joins at a time
+constexpr int kBlockTiles = 8;    // row tiles that are walked before the next of the matrix's
+constexpr int kMaxGroups = 1024;
+constexpr long long kMaxTiles = (1ll << 30) + 1;  // counted at most
+constexpr int kAddWarps = 8;
+constexpr int kMmThreads = 32 * (kAddWarps + 4);
+constexpr int kAddRegs = 224, kOtherRegs = 56, kLaunchRegs = 168;
+static_assert(256 * kAddRegs + 128 * kOtherRegs <= kMmThreads * kLaunchRegs, "registers");
+constexpr int kSlots = 3, kSlotBlocks = 8;  // scales of 8 blocks of K at a time
+constexpr uint32_t kSlotBlock = 512 + 16;   // 128 rows' scales, one of the matrix's for each half
+constexpr uint32_t kOutWarp = 2048;         // of each adding warp: 32 rows x 64 bytes on their way out
+constexpr uint64_t kMmTimeoutNs = 1000000000ull;
+// Cycles that a block of K of a tile takes, and a tile and the join of a split one besides
+constexpr double kPairCycles = 740, kWideCycles = 800, kSmallCycles = 480, kTileCycles = 4000, kJoinCycles = 2500;
 
-template <int kCols>
-struct MmConfig {
-  static constexpr int kLogCols = kCols == 16 ? 4 : kCols == 32 ? 5 : kCols == 64 ? 6 : kCols == 128 ? 7 : 8;
-  static constexpr int kEpiWarps = kCols >= 64 ? 8 : 4;
-  static constexpr int kWarpCols = kCols >= 64 ? kCols / 2 : kCols;  // columns of an adding warp
-  static constexpr int kThreads = 32 * (kEpiWarps + 4);
-  // 128 sums a thread and 64 products on their way: registers that the other warps give
-  static constexpr bool kShareRegs = kCols == 256;
-  static constexpr int kAddRegs = 216, kOtherRegs = 72, kLaunchRegs = 168;
-  static_assert(256 * kAddRegs + 128 * kOtherRegs <= 384 * kLaunchRegs, "registers");
-  static constexpr int kBoxRows = kCols < 32 ? kCols : 32;  // rows of a per copy
-  static constexpr uint32_t kStage = kMmRows * kMmK + kCols * kMmK;
-  static constexpr uint32_t kScaleSlot = kCols * 4;
-  // after the stages: scale slots, group prefix, barriers
-  static constexpr uint32_t kTail = kMmScaleSlots * kScaleSlot + (kMmMaxGroups + 4) * 4 + 512;
-  static constexpr int kFit = int((kMmSmemMax - 1024 - kTail) / kStage);
-  static constexpr int kStages = kFit < kMmMaxStages ? kFit : kMmMaxStages;
-  static constexpr uint32_t kScaleAt = kStages * kStage;
-  static constexpr uint32_t kPrefixAt = kScaleAt + kMmScaleSlots * kScaleSlot;
-  static constexpr uint32_t kBarAt = (kPrefixAt + (kMmMaxGroups + 4) * 4 + 7) & ~7u;
-  static constexpr uint32_t kSmem = kBarAt + 512 + 1024;
-  static constexpr uint32_t kTmemCols = 2 * kCols < 32 ? 32 : 2 * kCols;
-  static_assert(kSmem <= kMmSmemMax && kCols * kMmRows * 4 <= kScaleAt, "shared memory");
+// Tiles of 128 kCtas_ rows of a by kCols_ matrix rows.
+template <int kCtas_, int kCols_>
+struct Mm {
+  static constexpr int kCtas = kCtas_, kCols = kCols_, kRows = 128 * kCtas;
+  static constexpr int kSums = kCols / 2;  // of an adding thread
+  static constexpr int kRound = 64;        // products of a thread on their way from tensor memory
+  static constexpr uint32_t kTmem = 2 * kCols;                             // two accumulators
+  static constexpr uint32_t kABytes = 128 * kMmK, kWRows = kCols / kCtas;  // a CTA's
+  static constexpr uint32_t kStage = kABytes + kWRows * kMmK;
+  static constexpr int kStages = kStage > 32768 ? 4 : 6;
+  static_assert(kStages % 2 == 0, "an issuing warp's stages are every other one");
+  static constexpr uint32_t kOutAt = kStages * kStage, kScaleAt = kOutAt + kAddWarps * kOutWarp;
+  static constexpr uint32_t kPrefixAt = kScaleAt + kSlots * kSlotBlocks * kSlotBlock;
+  static constexpr uint32_t kBarAt = (kPrefixAt + (kMaxGroups + 4) * 4 + 7) & ~7u;
+  static constexpr uint32_t kSmem = kBarAt + 256 + 1024;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-// barriers
-constexpr int kMbFull = 0, kMbEmpty = kMmMaxStages, kMbSFull = 2 * kMmMaxStages, kMbSEmpty = kMbSFull + kMmScaleSlots,
-              kMbTFull = kMbSEmpty + kMmScaleSlots, kMbTEmpty = kMbTFull + 2, kMbDrain = kMbTEmpty + 2,
-              kMbCount = kMbDrain + 1;
-static_assert(kMbCount * 8 + 8 <= 512, "barriers");
+// barriers; of a pair, those marked * are used in the first CTA alone
+constexpr int kMaxStages = 6;
+constexpr int kBFull = 0 /* * both CTAs' copies */, kBEmpty = kMaxStages, kBTFull = 2 * kMaxStages,
+              kBTEmpty = kBTFull + 2 /* * both CTAs' adding warps */, kBDrain = kBTEmpty + 2 /* * of each issuing warp */,
+              kBSFull = kBDrain + 2, kBSEmpty = kBSFull + kSlots, kBCount = kBSEmpty + kSlots;
+static_assert(kBCount * 8 + 8 <= 256, "barriers");
 
 struct MmShape {
-  int kb;         // blocks of K
-  int col_tiles;  // tiles of the matrix's rows
-  int split;      // log2 of the CTAs of a cluster, which share a tile's blocks of K
+  int kb;          // blocks of K
+  int col_tiles;   // tiles of the matrix's rows
+  int col_blocks;  // scales along the matrix's rows
+  int parts;       // of a tile's blocks of K, one a CTA or pair of a cluster
 };
 
+struct MmSmem {
+  uint32_t base;
+  uint8_t* ptr;
+  uint32_t bars;  // offset of two words (tensor memory's address, abort flag) and the barriers
+  __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(ptr + bars + 8) + i; }
+  __device__ uint32_t* tmem_slot() const { return reinterpret_cast<uint32_t*>(ptr + bars); }
+  __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(ptr + bars + 4); }
+};
+
+__device__ __forceinline__ bool mm_wait(const MmSmem& sm, int bar, uint32_t parity, int* fault) {
+  if (mbar_wait_bounded(sm.bar(bar), parity, sm.abort_flag(), kMmTimeoutNs)) return true;
+  if (!*sm.abort_flag()) {
+    *sm.abort_flag() = 1;
+    atomicOr(fault, QSFM_FAULT_TIMEOUT);
+  }
+  return false;
+}
+
+// Every lane waits (on an open barrier one test), the warp goes on together.
+__device__ __forceinline__ bool mm_warp_wait(const MmSmem& sm, int bar, uint32_t parity, int* fault) {
+  const bool ok = mm_wait(sm, bar, parity, fault);
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// Two barriers, tested together: a test takes 100 cycles, most of them in flight.
+__device__ __forceinline__ bool mm_warp_wait2(const MmSmem& sm, int bar0, uint32_t parity0, int bar1, uint32_t parity1,
+                                              int* fault) {
+  const bool a = mbar_test(smem_u32(sm.bar(bar0)), parity0), b = mbar_test(smem_u32(sm.bar(bar1)), parity1);
+  if (__all_sync(0xffffffffu, a && b)) return true;
+  return mm_warp_wait(sm, bar0, parity0, fault) && mm_warp_wait(sm, bar1, parity1, fault);
+}
+
+// D (+)= A B^T of 32 e4m3 of K, operands K-major with the 128-byte swizzle (8-row groups
+// of 1 KB). The whole warp runs the loop around it and one elected lane issues, so the
+// descriptors stay in uniform registers.
+constexpr uint32_t kMmDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);  // group stride, version, swizzle
+template <uint32_t kOff, int kCtas = 1>
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kCtas == 1) {
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 a, b;\n add.u32 x, %1, %6;\n add.u32 y, %2, %6;\n"
+        " mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
+        " setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kMmDescHigh), "n"(kOff)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, e;\n .reg .b32 x, y;\n .reg .b64 a, b;\n add.u32 x, %1, %6;\n add.u32 y, %2, %6;\n"
+        " mov.b64 a, {x, %5};\n mov.b64 b, {y, %5};\n"
+        " setp.ne.b32 p, %4, 0;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kMmDescHigh), "n"(kOff)
+        : "memory");
+  }
+}
+__device__ __forceinline__ uint32_t mm_desc(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | ((16u >> 4) << 16); }
+
+// 4 bytes to shared memory without a register.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// One of the barrier's arrivals, once the thread's copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Address in CTA `rank` of the cluster of this CTA's shared address.
+__device__ __forceinline__ uint32_t in_cta(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+
+// Registers of a warpgroup: the shares of a block add up to what it was launched with.
+template <int kRegs>
+__device__ __forceinline__ void mm_more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void mm_fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// One tile: rows row0 .. row0 + rows - 1 of a, matrix rows n0 .. of group g.
+struct MmTile {
+  int g, n0, row0, rows;
+};
+
+// Rows of group g, cut to what there is.
+__device__ __forceinline__ void group_rows(const qsfm_matmul_params& p, int g, int& lo, int& hi, bool& bad) {
+  if (p.cu_rows == nullptr) {
+    lo = 0;
+    hi = p.rows;
+    bad = false;
+    return;
+  }
+  const int a = __ldg(p.cu_rows + g), b = __ldg(p.cu_rows + g + 1);
+  bad = a < 0 || b < a || b > p.rows;
+  lo = min(max(a, 0), p.rows);
+  hi = max(lo, min(b, p.rows));
+}
+
+// prefix[g]: tiles (of `rows` rows and one of col_tiles parts of the matrix) before group
+// g's. One warp.
+__device__ __forceinline__ void count_tiles(const qsfm_matmul_params& p, int rows, int col_tiles, int* prefix, int* fault) {
+  const int lane = threadIdx.x & 31;
+  long long run = 0;  // overlapping groups of a bad cu_rows may count more than there can be
+  const auto cut = [](long long v) { return int(v < kMaxTiles ? v : kMaxTiles); };
+  for (int g0 = 0; g0 < p.groups; g0 += 32) {
+    long long n = 0;
+    if (g0 + lane < p.groups) {
+      int lo, hi;
+      bool bad;
+      group_rows(p, g0 + lane, lo, hi, bad);
+      if (bad && blockIdx.x == 0) atomicOr(fault, QSFM_FAULT_GROUP_ROWS);
+      n = (long long)((hi - lo + rows - 1) / rows) * col_tiles;
+    }
+    long long sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (g0 + lane < p.groups) prefix[g0 + lane] = cut(run + sum - n);
+    run += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) prefix[p.groups] = cut(run);
+}
+
+// The first bytes of a copy's destination are this CTA's; it completes on `bar`, of a pair
+// in the first CTA.
+template <int kCtas>
+__device__ __forceinline__ void mm_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void mm_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+// Arrives on `bar` (of both CTAs of a pair, `mask`) once the MMAs issued so far have completed.
+template <int kCtas>
+__device__ __forceinline__ void mm_commit(uint64_t* bar, uint32_t mask) {
+  if constexpr (kCtas == 2)
+    asm volatile(
+        "{\n .reg .pred e;\n .reg .b16 both;\n cvt.u16.u32 both, %1;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], both;\n}"
+        ::"r"(smem_u32(bar)), "r"(mask)
+        : "memory");
+  else
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+// (What it orders is tensor memory's reads, by tcgen05.fence; a release at the cluster's
+// scope would wait for every load and store of the thread before it.)
+__device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-// The CTA's walk over the tiles: prefix[g] tiles lie before group g's.
-template <int kCols>
+// The walk over the tiles of a CTA or pair.
+template <class C>
 struct MmWalk {
   const int* prefix;
   int g, at, step, total;
   __device__ __forceinline__ bool next(const qsfm_matmul_params& p, const MmShape& s, MmTile& t) {
+    constexpr int kRows = C::kRows;
     if (at >= total) return false;
     while (at >= prefix[g + 1]) ++g;
     int lo, hi;
     bool bad;
     group_rows(p, g, lo, hi, bad);
-    const int local = at - prefix[g], row_tiles = (hi - lo + kCols - 1) / kCols;
-    const int n = local / row_tiles, m = local - n * row_tiles;
+    const int row_tiles = (hi - lo + kRows - 1) / kRows;
+    const int local = at - prefix[g], block = local / (kBlockTiles * s.col_tiles);
+    const int rest = local - block * (kBlockTiles * s.col_tiles), high = min(kBlockTiles, row_tiles - block * kBlockTiles);
+    const int n = rest / high, m = block * kBlockTiles + rest - n * high;
     t.g = g;
-    t.n0 = n * kMmRows;
-    t.row0 = lo + m * kCols;
-    t.cols = min(kCols, hi - t.row0);
+    t.n0 = n * C::kCols;
+    t.row0 = lo + m * kRows;
+    t.rows = min(kRows, hi - t.row0);
     at += step;
     return true;
   }
 };
 
+// What a warp knows of its place: `cta` in the pair, the blocks b0 .. b1 - 1 of K, the
+// pair's first CTA in the cluster.
+struct MmPlace {
+  uint32_t cta, first;
+  int b0, b1;
+};
+
 // ------------------------------------------------------------- loads
-template <int kCols>
-__device__ void mm_load(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<kCols> walk, int b0,
-                        int b1, const CUtensorMap* amap, const CUtensorMap* wmap, int* fault) {
-  using C = MmConfig<kCols>;
+template <class C>
+__device__ void mm_load(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
+                        const CUtensorMap* amap, const CUtensorMap* wmap, int* fault) {
   if ((threadIdx.x & 31) != 0) return;
   uint32_t st = 0, par = 1;
   MmTile t;
   while (walk.next(p, s, t)) {
-    const int boxes = (t.cols + C::kBoxRows - 1) / C::kBoxRows;
-    const uint32_t bytes = uint32_t(kMmRows + boxes * C::kBoxRows) * kMmK;
-    for (int b = b0; b < b1; ++b) {
-      if (!mm_wait(sm, kMbEmpty + st, par, fault)) return;
-      const uint32_t at = sm.base + st * C::kStage;
-      mbar_arrive_expect_tx(sm.bar(kMbFull + st), bytes);
-      mm_load_3d(at, wmap, b * kMmK, t.n0, t.g, sm.bar(kMbFull + st));
-      for (int i = 0; i < boxes; ++i)
-        tma_load_2d(at + kMmRows * kMmK + i * C::kBoxRows * kMmK, amap, b * kMmK, t.row0 + i * C::kBoxRows,
-                    sm.bar(kMbFull + st));
+    // of a tile of few rows 32 at a time; a pair's are loaded whole
+    const int boxes = C::kCtas == 2 ? 4 : (t.rows + 31) / 32;
+    const uint32_t bytes = C::kCtas * (uint32_t(boxes) * 32 * kMmK + C::kWRows * kMmK);
+    for (int b = at.b0; b < at.b1; ++b) {
+      if (!mm_wait(sm, kBEmpty + st, par, fault)) return;
+      const uint32_t to = sm.base + st * C::kStage;
+      const uint32_t bar = C::kCtas == 2 ? in_cta(smem_u32(sm.bar(kBFull + st)), at.first) : smem_u32(sm.bar(kBFull + st));
+      if (at.cta == 0) mbar_arrive_expect_tx(sm.bar(kBFull + st), bytes);
+      mm_load_3d<C::kCtas>(to + C::kABytes, wmap, b * kMmK, t.n0 + int(C::kWRows * at.cta), t.g, bar);
+      if constexpr (C::kCtas == 2) {
+        mm_load_2d<C::kCtas>(to, amap, b * kMmK, t.row0 + 128 * int(at.cta), bar);
+      } else {
+        for (int i = 0; i < boxes; ++i) mm_load_2d<C::kCtas>(to + i * 32 * kMmK, amap, b * kMmK, t.row0 + 32 * i, bar);
+      }
       if (++st == C::kStages) {
         st = 0;
         par ^= 1;
@@ -122,57 +353,69 @@ __device__ void mm_load(const qsfm_matmul_params& p, const MmShape& s, const MmS
 }
 
 // ------------------------------------------------------------- MMA issue
-template <int kCols>
-__device__ void mm_issue(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<kCols> walk, int b0,
-                         int b1, uint32_t tmem, int* fault) {
-  using C = MmConfig<kCols>;
-  uint32_t st = 0, par = 0, buf = 0, tpar = 1;
+// Two warps issue in turn, `odd` the second: waiting for a stage and an accumulator and
+// handing four MMAs and two commits over takes one warp 550 cycles and more, longer than
+// the MMAs themselves.
+template <class C>
+__device__ void mm_issue(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
+                         uint32_t odd, uint32_t tmem, int* fault) {
+  // formats 0 (e4m3) for both operands, as in the bf16 descriptor's f16 form
+  constexpr uint32_t idesc = make_idesc_bf16(C::kRows, C::kCols, 0, 0, true);
+  const uint32_t d = tmem + odd * C::kCols, mask = 3u << at.first;
+  uint32_t st = odd, par = 0, tpar = 1, first = odd;  // first: whether the tile's first block is the other warp's
   MmTile t;
   while (walk.next(p, s, t)) {
-    // formats 0 (e4m3) for both operands, as in the bf16 descriptor's f16 form
-    const uint32_t idesc = make_idesc_bf16(kMmRows, (t.cols + 15) & ~15, 0, 0, true);
-    for (int b = b0; b < b1; ++b) {
-      if (!mm_warp_wait(sm, kMbTEmpty + buf, tpar, fault)) return;
-      if (!mm_warp_wait(sm, kMbFull + st, par, fault)) return;
+    for (int b = at.b0 + int(first); b < at.b1; b += 2) {
+      if (!mm_warp_wait2(sm, kBFull + st, par, kBTEmpty + odd, tpar, fault)) return;
       tc_fence_after();
-      const uint32_t w = mm_desc(sm.base + st * C::kStage), a = w + ((kMmRows * kMmK) >> 4);
-      const uint32_t d = tmem + buf * kCols;
-      mma_e4m3<0>(d, w, a, idesc, 0);
-      mma_e4m3<2>(d, w, a, idesc, 1);
-      mma_e4m3<4>(d, w, a, idesc, 1);
-      mma_e4m3<6>(d, w, a, idesc, 1);
-      mm_commit(sm.bar(kMbEmpty + st));
-      mm_commit(sm.bar(kMbTFull + buf));
-      if (++st == C::kStages) {
-        st = 0;
+      const uint32_t a = mm_desc(sm.base + st * C::kStage), w = a + (C::kABytes >> 4);
+      mma_e4m3<0, C::kCtas>(d, a, w, idesc, 0);
+      mma_e4m3<2, C::kCtas>(d, a, w, idesc, 1);
+      mma_e4m3<4, C::kCtas>(d, a, w, idesc, 1);
+      mma_e4m3<6, C::kCtas>(d, a, w, idesc, 1);
+      mm_commit<C::kCtas>(sm.bar(kBTFull + odd), mask);
+      mm_commit<C::kCtas>(sm.bar(kBEmpty + st), mask);
+      st += 2;
+      if (st >= C::kStages) {
+        st = odd;
         par ^= 1;
       }
-      buf ^= 1;
-      tpar ^= buf == 0;
+      tpar ^= 1;
     }
+    first ^= uint32_t(at.b1 - at.b0) & 1;
   }
 }
 
 // ------------------------------------------------------------- scales
-template <int kCols>
-__device__ void mm_scales(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<kCols> walk, int b0,
-                          int b1, int* fault) {
-  using C = MmConfig<kCols>;
+// Eight blocks at a time, on their way to shared memory with the loads: from global
+// memory, a thread's own 4 bytes a block cost the adding warps a third of their time.
+template <class C>
+__device__ void mm_scales(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
+                          int* fault) {
   const int lane = threadIdx.x & 31;
   uint32_t slot = 0, par = 1;
   MmTile t;
   while (walk.next(p, s, t)) {
-    for (int b = b0; b < b1; ++b) {
-      if (!mm_warp_wait(sm, kMbSEmpty + slot, par, fault)) return;
-      const uint32_t at = sm.base + C::kScaleAt + slot * C::kScaleSlot;
+    // rows behind the tile's take its last one's scales, and are not stored
+    const int live = (min(t.rows - 128 * int(at.cta), 128) + 31) / 32;
+    const float* as[4];
 #pragma unroll
-      for (int c = lane; c < kCols; c += 32) {
-        const bool in = c < t.cols;
-        cp_async4(at + 4 * c, p.a_scale + size_t(t.row0 + (in ? c : 0)) * p.a_scale_row_stride +
-                                  size_t(b) * p.a_scale_col_stride, in ? 4 : 0);
+    for (int i = 0; i < 4; ++i)
+      as[i] = p.a_scale + size_t(t.row0 + min(128 * int(at.cta) + 32 * i + lane, t.rows - 1)) * p.a_scale_row_stride;
+    // lane 0 and 1: of the two halves
+    const int block = min((t.n0 + C::kSums * (lane & 1)) / 128, s.col_blocks - 1);
+    const float* ws = p.w_scale + (size_t(t.g) * s.col_blocks + block) * s.kb;
+    for (int b0 = at.b0; b0 < at.b1; b0 += kSlotBlocks) {
+      if (!mm_warp_wait(sm, kBSEmpty + slot, par, fault)) break;
+      uint32_t to = sm.base + C::kScaleAt + slot * kSlotBlocks * kSlotBlock;
+      for (int b = b0; b < min(b0 + kSlotBlocks, at.b1); ++b, to += kSlotBlock) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < live) cp_async4(to + 4 * (32 * i + lane), as[i] + size_t(b) * p.a_scale_col_stride);
+        if (lane < 2) cp_async4(to + 512 + 4 * lane, ws + b);
       }
-      cp_async_arrive(sm.bar(kMbSFull + slot));
-      if (++slot == kMmScaleSlots) {
+      cp_async_arrive(sm.bar(kBSFull + slot));
+      if (++slot == kSlots) {
         slot = 0;
         par ^= 1;
       }
@@ -182,129 +425,196 @@ __device__ void mm_scales(const qsfm_matmul_params& p, const MmShape& s, const M
 }
 
 // ------------------------------------------------------------- sums and output
-// Adds up the blocks b0 .. b1 - 1 of a tile in registers; false after a timeout. A round
-// takes up to 64 columns out of tensor memory at once (a load and its wait take 200 cycles
-// and more, whatever its size).
-template <int kCols>
-__device__ __forceinline__ bool mm_add(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, const MmTile& t,
-                                       int b0, int b1, uint32_t tmem, uint32_t& buf, uint32_t& tpar, uint32_t& slot,
-                                       uint32_t& spar, float (&acc)[MmConfig<kCols>::kWarpCols], int* fault) {
-  using C = MmConfig<kCols>;
-  constexpr int kN = C::kWarpCols, kRound = kN < 64 ? kN : 64, kPart = kN < 32 ? kN : 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, c0 = (warp >> 2) * kN;
+// kPart columns of the warp's 32 rows (a lane has a row) to `out`, rows `stride` elements
+// apart, of which the first `rows` and `cols` are there: through shared memory (`stage`, a
+// row's 16-byte pieces in turn by row), so that a warp stores whole sectors; single
+// elements where the output is not aligned or ends.
+template <typename T, int kPart>
+__device__ __forceinline__ void store_part(T* out, size_t stride, const float* v, int rows, int cols, bool aligned,
+                                           uint8_t* stage) {
+  constexpr int kEach = 16 / sizeof(T), kPieces = kPart / kEach, kTurn = 8 / kPieces;
+  const int lane = threadIdx.x & 31;
+  const auto at = [&](int r, int piece) { return stage + 16 * kPieces * r + 16 * (piece ^ ((r / kTurn) & (kPieces - 1))); };
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kN; ++i) acc[i] = 0.f;
-  const int live = t.cols - c0;  // columns of this warp
-  const float* wsp = p.w_scale + (size_t(t.g) * s.col_tiles + t.n0 / kMmRows) * s.kb;
-  // two blocks ahead, into the register that the block of the same parity is done with
-  // (a copy from register to register would wait for the load)
-  float wsr[2] = {b0 < b1 ? __ldg(wsp + b0) : 0.f, b0 + 1 < b1 ? __ldg(wsp + b0 + 1) : 0.f};
-  for (int bb = b0; bb < b1; bb += 2) {
+  for (int i = 0; i < kPieces; ++i) {
+    uint32_t w[4];
 #pragma unroll
-   for (int par2 = 0; par2 < 2; ++par2) {
-    const int b = bb + par2;
-    if (b >= b1) break;
-    const float ws = wsr[par2];
-    if (b + 2 < b1) wsr[par2] = __ldg(wsp + b + 2);
-    if (!mm_warp_wait(sm, kMbSFull + slot, spar, fault)) return false;
-    if (!mm_warp_wait(sm, kMbTFull + buf, tpar, fault)) return false;
-    tc_fence_after();
-    const float4* sc = reinterpret_cast<const float4*>(sm.ptr + C::kScaleAt + slot * C::kScaleSlot) + c0 / 4;
-    const uint32_t at = tmem + buf * kCols + c0 + (uint32_t(32 * quarter) << 16);
-#pragma unroll
-    for (int c = 0; c < kN; c += kRound) {
-      float v[kRound];
-#pragma unroll
-      for (int h = 0; h < kRound; h += kPart)
-        if (c + h < live) {
-          if constexpr (kPart == 32) tmem_ld32(at + c + h, v + h);
-          else tmem_ld16(at + c + h, v + h);
-        }
-      tmem_ld_wait();
-      if (c + kRound >= kN) {  // the accumulator is free as soon as the last round has it
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(sm.bar(kMbTEmpty + buf));
+    for (int j = 0; j < 4; ++j) {
+      const int c = kEach * i + kEach / 4 * j;
+      if constexpr (sizeof(T) == 4) {
+        w[j] = __float_as_uint(v[c]);
+      } else if constexpr (__is_same(T, __half)) {
+        w[j] = pack_f16(v[c], v[c + 1]);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
       }
+    }
+    *reinterpret_cast<uint4*>(at(lane, i)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+  if (aligned && kPart <= cols) {
 #pragma unroll
-      for (int h = 0; h < kRound; h += kPart)
-        if (c + h < live) {
+    for (int i = 0; i < kPieces; ++i) {
+      const int r = 32 / kPieces * i + lane / kPieces, piece = lane % kPieces;
+      const uint4 x = *reinterpret_cast<const uint4*>(at(r, piece));
+      if (r < rows) *reinterpret_cast<uint4*>(out + r * stride + piece * kEach) = x;
+    }
+  } else {
+    for (int i = lane; i < rows * kPart; i += 32) {
+      const int r = i / kPart, c = i % kPart;
+      if (c < cols) out[r * stride + c] = *reinterpret_cast<const T*>(at(r, c / kEach) + c % kEach * sizeof(T));
+    }
+  }
+}
+
+// kN columns of the warp's rows, from element `at` of the output on.
+template <int kN>
+__device__ __forceinline__ void store_sums(const qsfm_matmul_params& p, size_t at, const float (&v)[kN], int rows, int cols,
+                                           uint8_t* stage) {
+  const int size = p.out_type == QSFM_F32 ? 4 : 2;
+  const bool aligned = (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 && (p.out_row_stride * size) % 16 == 0;
+  constexpr int kHalf = kN < 32 ? kN : 32;  // 64 bytes of a row at a time
 #pragma unroll
-          for (int i = h; i < h + kPart; i += 4) {
-            const float4 f = sc[(c + i) / 4];
-            mm_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f.x * ws, f.y * ws);
-            mm_fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f.z * ws, f.w * ws);
+  for (int c = 0; c < kN; c += kHalf) {
+    if (c >= cols) break;
+    if (p.out_type == QSFM_BF16)
+      store_part<__nv_bfloat16, kHalf>(static_cast<__nv_bfloat16*>(p.out) + at + c, p.out_row_stride, v + c, rows, cols - c,
+                                       aligned, stage);
+    else if (p.out_type == QSFM_F16)
+      store_part<__half, kHalf>(static_cast<__half*>(p.out) + at + c, p.out_row_stride, v + c, rows, cols - c, aligned,
+                                stage);
+    else
+#pragma unroll
+      for (int h = 0; h < kHalf; h += 16)
+        if (c + h < cols)
+          store_part<float, 16>(static_cast<float*>(p.out) + at + c + h, p.out_row_stride, v + c + h, rows, cols - c - h,
+                                aligned, stage);
+  }
+}
+
+// Adds up a tile's blocks; false after a timeout. Warps without rows (kLive false) keep
+// step with the others.
+template <class C, bool kLive>
+__device__ __forceinline__ bool mm_add(const MmShape& s, const MmSmem& sm, MmPlace at, uint32_t tmem, uint32_t tempty,
+                                       uint32_t& buf, uint32_t& tpar, uint32_t& slot, uint32_t& spar,
+                                       float (&acc)[C::kSums], int* fault) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, half = warp >> 2;
+  if constexpr (kLive) {
+#pragma unroll
+    for (int i = 0; i < C::kSums; ++i) acc[i] = 0.f;
+  }
+  for (int b0 = at.b0; b0 < at.b1; b0 += kSlotBlocks) {
+    if (!mm_warp_wait(sm, kBSFull + slot, spar, fault)) return false;
+    const float* scales = reinterpret_cast<const float*>(sm.ptr + C::kScaleAt + slot * kSlotBlocks * kSlotBlock);
+    for (int b = b0; b < min(b0 + kSlotBlocks, at.b1); ++b, scales += kSlotBlock / 4) {
+      const float f = kLive ? scales[32 * (warp & 3) + lane] * scales[128 + half] : 0.f;
+      if (!mm_warp_wait(sm, kBTFull + buf, tpar, fault)) return false;
+      tc_fence_after();
+      const uint32_t from = tmem + buf * C::kCols + C::kSums * half + (uint32_t(32 * (warp & 3)) << 16);
+#pragma unroll
+      for (int c = 0; c < C::kSums; c += C::kRound) {
+        float v[C::kRound];
+        if constexpr (kLive) {
+#pragma unroll
+          for (int j = 0; j < C::kRound; j += 32) tmem_ld32(from + c + j, v + j);
+          tmem_ld_wait();
+        }
+        if (c + C::kRound >= C::kSums) {  // the accumulator is free as soon as the last round has it
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (C::kCtas == 2) arrive_in_cluster(tempty + 8 * buf);
+            else mbar_arrive(sm.bar(kBTEmpty + buf));
           }
         }
+        if constexpr (kLive) {
+#pragma unroll
+          for (int j = 0; j < C::kRound; ++j) acc[c + j] = fmaf(v[j], f, acc[c + j]);
+        }
+      }
+      buf ^= 1;
+      tpar ^= buf == 0;
     }
     __syncwarp();
-    if (lane == 0) mbar_arrive(sm.bar(kMbSEmpty + slot));
-    buf ^= 1;
-    tpar ^= buf == 0;
-    if (++slot == kMmScaleSlots) {
+    if (lane == 0) mbar_arrive(sm.bar(kBSEmpty + slot));
+    if (++slot == kSlots) {
       slot = 0;
       spar ^= 1;
     }
-   }
   }
   return true;
 }
 
-template <int kCols>
-__device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<kCols> walk, int b0,
-                       int b1, uint32_t tmem, int* fault) {
-  using C = MmConfig<kCols>;
-  constexpr int kN = C::kWarpCols;
+template <class C>
+__device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
+                       uint32_t tmem, int* fault) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = 32 * (warp & 3) + lane, c0 = (warp >> 2) * kN;
+  const int row0 = 128 * int(at.cta) + 32 * (warp & 3), half = warp >> 2;
+  const uint32_t tempty = in_cta(smem_u32(sm.bar(kBTEmpty)), at.first);
+  uint8_t* stage = sm.ptr + C::kOutAt + kOutWarp * warp;
   uint32_t buf = 0, tpar = 0, slot = 0, spar = 0;
   MmTile t;
-  float acc[kN];
-  if (s.split == 0) {
+  float acc[C::kSums];
+  if (s.parts == 1) {
     while (walk.next(p, s, t)) {
-      if (!mm_add<kCols>(p, s, sm, t, b0, b1, tmem, buf, tpar, slot, spar, acc, fault)) return;
-      if (t.n0 + row < p.n) {
-#pragma unroll
-        for (int c = 0; c < kN; ++c)
-          if (c0 + c < t.cols) mm_store(p, size_t(t.row0 + c0 + c) * p.out_row_stride + t.n0 + row, acc[c]);
+      const int rows = min(32, t.rows - row0), n0 = t.n0 + C::kSums * half, cols = p.n - n0;
+      if (rows <= 0) {
+        if (!mm_add<C, false>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault)) return;
+        continue;
       }
+      if (!mm_add<C, true>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault)) return;
+      if (cols > 0) store_sums(p, size_t(t.row0 + row0) * p.out_row_stride + n0, acc, rows, cols, stage);
     }
     return;
   }
-  // The cluster's one tile: CTA r adds up the columns r w .. r w + w - 1 of all, w = kCols /
-  // CTAs, in the order of the CTAs. Their sums take the place of the operands, which every
-  // CTA of the cluster is through with at the first barrier.
+  // The cluster's one tile: its part q adds up the chunks n q / parts .. of the tile's n
+  // chunks of 16 columns, in the order of the parts. The sums take the place of the
+  // operands, which every CTA of the cluster is through with at the first barrier: of part
+  // q's chunk c from part r at [r][c - first of q][16][128 rows].
+  constexpr int kChunks = C::kCols / kChunk;
   bool ok = walk.next(p, s, t);
-  if (ok) ok = mm_add<kCols>(p, s, sm, t, b0, b1, tmem, buf, tpar, slot, spar, acc, fault);
-  const uint32_t rank = cluster_rank();
-  const int shift = C::kLogCols - s.split, w = 1 << shift;
+  const int rows = ok ? min(32, t.rows - row0) : 0;
+  if (ok)
+    ok = rows > 0 ? mm_add<C, true>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault)
+                  : mm_add<C, false>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault);
+  const int part = int(at.first) / C::kCtas, most = (kChunks + s.parts - 1) / s.parts;
   cluster_sync();
-  if (ok) {
+  if (ok && lane < rows) {
 #pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      const int col = c0 + c;
-      if (col < t.cols)
-        st_cluster(in_cta(sm.base + 4 * (((rank << shift) + (col & (w - 1))) * kMmRows + row), uint32_t(col >> shift)), acc[c]);
+    for (int c = 0; c < C::kSums; c += kChunk) {
+      const int chunk = (C::kSums * half + c) / kChunk;
+      const int owner = ((chunk + 1) * s.parts - 1) / kChunks;  // the last q with n q / parts <= chunk
+      const uint32_t to = in_cta(sm.base + 4 * (((part * most + chunk - kChunks * owner / s.parts) * kChunk) * 128 + (row0 & 127) + lane),
+                                 uint32_t(owner * C::kCtas) + at.cta);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) st_cluster(to + 512 * i, acc[c + i]);
     }
   }
   cluster_sync();
-  if (!ok || t.n0 + row >= p.n) return;
-  const float* sums = reinterpret_cast<const float*>(sm.ptr) + row;
-  for (int c = warp >> 2; c < w; c += C::kEpiWarps / 4) {
-    const int col = int(rank << shift) + c;
-    if (col >= t.cols) break;
-    float v = sums[c * kMmRows];
-    for (int r = 1; r < 1 << s.split; ++r) v += sums[((r << shift) + c) * kMmRows];
-    mm_store(p, size_t(t.row0 + col) * p.out_row_stride + t.n0 + row, v);
+  if (!ok || rows <= 0) return;
+  const float* sums = reinterpret_cast<const float*>(sm.ptr) + (row0 & 127) + lane;
+  const int c0 = kChunks * part / s.parts, c1 = kChunks * (part + 1) / s.parts;
+  for (int c = c0 + half; c < c1; c += 2) {
+    const int n0 = t.n0 + kChunk * c;
+    if (n0 >= p.n) break;
+    float v[kChunk];
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = sums[((c - c0) * kChunk + i) * 128];
+    for (int q = 1; q < s.parts; ++q) {
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) v[i] += sums[((q * most + c - c0) * kChunk + i) * 128];
+    }
+    store_sums(p, size_t(t.row0 + row0) * p.out_row_stride + n0, v, rows, p.n - n0, stage);
   }
 }
 
-template <int kCols>
-__global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
+// ------------------------------------------------------------- the kernel
+template <class C>
+__global__ void __launch_bounds__(kMmThreads, 1)
     matmul_kernel(const qsfm_matmul_params p, const MmShape s, int* fault, const __grid_constant__ CUtensorMap amap,
                   const __grid_constant__ CUtensorMap wmap) {
-  using C = MmConfig<kCols>;
   extern __shared__ uint8_t mm_smem[];
   const uint32_t raw = smem_u32(mm_smem);
   MmSmem sm;
@@ -312,113 +622,236 @@ __global__ void __launch_bounds__(MmConfig<kCols>::kThreads, 1)
   sm.ptr = mm_smem + (sm.base - raw);
   sm.bars = C::kBarAt;
   const int tid = threadIdx.x, warp = tid >> 5;
+  const bool cluster = C::kCtas == 2 || s.parts > 1;
+  const uint32_t rank = cluster ? cluster_rank() : 0;
   int* prefix = reinterpret_cast<int*>(sm.ptr + C::kPrefixAt);
   if (tid == 0) {
     for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(sm.bar(kMbFull + i), 1);
-      mbar_init(sm.bar(kMbEmpty + i), 1);
-    }
-    for (int i = 0; i < kMmScaleSlots; ++i) {
-      mbar_init(sm.bar(kMbSFull + i), 32);
-      mbar_init(sm.bar(kMbSEmpty + i), C::kEpiWarps);
+      mbar_init(sm.bar(kBFull + i), 1);
+      mbar_init(sm.bar(kBEmpty + i), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(sm.bar(kMbTFull + i), 1);
-      mbar_init(sm.bar(kMbTEmpty + i), C::kEpiWarps);
+      mbar_init(sm.bar(kBTFull + i), 1);
+      mbar_init(sm.bar(kBTEmpty + i), C::kCtas * kAddWarps);
+      mbar_init(sm.bar(kBDrain + i), 1);
     }
-    mbar_init(sm.bar(kMbDrain), 1);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(sm.bar(kBSFull + i), 32);
+      mbar_init(sm.bar(kBSEmpty + i), kAddWarps);
+    }
     *sm.abort_flag() = 0;
     fence_mbar_init();
   }
-  if (warp == C::kEpiWarps + 1) tmem_alloc(sm.tmem_slot(), C::kTmemCols);
+  if (warp == kAddWarps + 1) {  // of both CTAs
+    if constexpr (C::kCtas == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(sm.tmem_slot())),
+                   "r"(C::kTmem)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      tmem_alloc(sm.tmem_slot(), C::kTmem);
+    }
+  }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (warp == 0) count_tiles(p, kCols, s.col_tiles, prefix, fault);
+  if (warp == 0) count_tiles(p, C::kRows, s.col_tiles, prefix, fault);
   tc_fence_before();
   __syncthreads();
+  if (cluster) cluster_sync();  // barriers and tensor memory of all CTAs are there
   tc_fence_after();
   const uint32_t tmem = *sm.tmem_slot();
-  MmWalk<kCols> walk;
+  MmPlace at;
+  at.cta = rank & (C::kCtas - 1);
+  at.first = rank - at.cta;
+  const int part = int(at.first) / C::kCtas;
+  at.b0 = int(int64_t(s.kb) * part / s.parts);
+  at.b1 = int(int64_t(s.kb) * (part + 1) / s.parts);
+  MmWalk<C> walk;
   walk.prefix = prefix;
   walk.g = 0;
-  walk.at = int(blockIdx.x >> s.split);
-  walk.step = int(gridDim.x >> s.split);
+  walk.at = int(blockIdx.x / unsigned(C::kCtas * s.parts));
+  walk.step = int(gridDim.x / unsigned(C::kCtas * s.parts));
   walk.total = prefix[p.groups];
-  const int part = int(blockIdx.x) & ((1 << s.split) - 1);
-  const int b0 = int(int64_t(s.kb) * part >> s.split), b1 = int(int64_t(s.kb) * (part + 1) >> s.split);
-  if constexpr (C::kShareRegs) {
-    if (warp < C::kEpiWarps) mm_more_registers<C::kAddRegs>();
-    else mm_fewer_registers<C::kOtherRegs>();
-  }
-  if (warp < C::kEpiWarps) {
-    mm_sum<kCols>(p, s, sm, walk, b0, b1, tmem, fault);
-  } else if (warp == C::kEpiWarps) {
-    mm_load<kCols>(p, s, sm, walk, b0, b1, &amap, &wmap, fault);
-  } else if (warp == C::kEpiWarps + 1) {
-    mm_issue<kCols>(p, s, sm, walk, b0, b1, tmem, fault);
-    // every MMA issued has completed before tensor memory is freed
-    mm_commit(sm.bar(kMbDrain));
-    volatile int never = 0;
-    if (!mbar_wait_poll(smem_u32(sm.bar(kMbDrain)), 0, &never, kMmTimeoutNs)) atomicOr(fault, QSFM_FAULT_TIMEOUT);
-  } else if (warp == C::kEpiWarps + 2) {
-    mm_scales<kCols>(p, s, sm, walk, b0, b1, fault);
-  }
-  __syncwarp();
-  if (s.split > 0 && warp >= C::kEpiWarps) {  // (the adding warps' are in mm_sum)
-    cluster_sync();
-    cluster_sync();
+  if (warp < kAddWarps) {
+    mm_more_registers<kAddRegs>();
+    mm_sum<C>(p, s, sm, walk, at, tmem, fault);
+  } else {
+    mm_fewer_registers<kOtherRegs>();
+    if (warp == kAddWarps) {
+      mm_load<C>(p, s, sm, walk, at, &amap, &wmap, fault);
+    } else if (warp == kAddWarps + 3) {
+      mm_scales<C>(p, s, sm, walk, at, fault);
+    } else if (at.cta == 0) {
+      const int odd = warp - kAddWarps - 1;
+      mm_issue<C>(p, s, sm, walk, at, uint32_t(odd), tmem, fault);
+      // every MMA issued has completed before tensor memory is freed
+      mm_commit<C::kCtas>(sm.bar(kBDrain + odd), 1u << at.first);
+      volatile int never = 0;
+      if (!mbar_wait_poll(smem_u32(sm.bar(kBDrain + odd)), 0, &never, kMmTimeoutNs)) atomicOr(fault, QSFM_FAULT_TIMEOUT);
+    }
+    __syncwarp();
+    if (s.parts > 1) {  // (the adding warps' are in mm_sum)
+      cluster_sync();
+      cluster_sync();
+    }
   }
   // after an abort copies may still be on their way into this CTA's shared memory:
   // a millisecond is far more than they take
-  if (warp == C::kEpiWarps && *sm.abort_flag())
+  if (warp == kAddWarps && *sm.abort_flag())
     for (int i = 0; i < 1000; ++i) __nanosleep(1000);
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kEpiWarps + 1) {
+  if (C::kCtas == 2) cluster_sync();  // no arrival for the other CTA is on its way, its accumulators are read
+  if (warp == kAddWarps + 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, C::kTmemCols);
+    if constexpr (C::kCtas == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::kTmem) : "memory");
+    else
+      tmem_dealloc(tmem, C::kTmem);
   }
 }
 
 // ------------------------------------------------------------- host side
-template <int kCols>
-cudaError_t launch_cols(const qsfm_matmul_params& p, const MmShape& s, int sms, int* fault, cudaStream_t stream) {
-  using C = MmConfig<kCols>;
-  cudaError_t e = cudaFuncSetAttribute(matmul_kernel<kCols>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult qres;
+    void* fn = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &qres) ==
+            cudaSuccess &&
+        qres == cudaDriverEntryPointSuccess)
+      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  return encode;
+}
+
+// Bytes [planes, rows, k] in boxes of box_rows x 128, what lies outside read as zero.
+// (A stride of a dimension of length 1 is not used: the encoder still wants it to be a
+// multiple of 16 that is not below the extent within.)
+cudaError_t make_map(const void* base, int k, int rows, int planes, long long row_stride, long long plane_stride,
+                     int box_rows, bool is3d, CUtensorMap* map) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  if (rows <= 1) row_stride = (k + 15) & ~15;
+  if (planes <= 1) plane_stride = row_stride * rows;
+  const cuuint64_t dims[3] = {cuuint64_t(k), cuuint64_t(rows), cuuint64_t(planes)};
+  const cuuint64_t strides[2] = {cuuint64_t(row_stride), cuuint64_t(plane_stride)};
+  const cuuint32_t box[3] = {kMmK, cuuint32_t(box_rows), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, is3d ? 3 : 2, const_cast<void*>(base), dims, strides,
+                            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+constexpr int kMaxDevices = 64;
+
+// Prepares a device for a kernel, once: its shared memory, and that it has the registers
+// that the split counts on (with fewer the adding warps would wait forever).
+template <class C>
+cudaError_t prepare(int dev) {
+  static std::atomic<bool> done[kMaxDevices];
+  if (dev < kMaxDevices && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, matmul_kernel<C>);
   if (e != cudaSuccess) return e;
-  if constexpr (C::kShareRegs) {
-    // with fewer registers than the split counts on, the adding warps would wait forever
-    static std::atomic<bool> enough{false};
-    if (!enough.load(std::memory_order_relaxed)) {
-      cudaFuncAttributes attr;
-      if ((e = cudaFuncGetAttributes(&attr, matmul_kernel<kCols>)) != cudaSuccess) return e;
-      if (attr.numRegs < C::kLaunchRegs) return cudaErrorInvalidConfiguration;
-      enough.store(true, std::memory_order_relaxed);
+  if (attr.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(matmul_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::kSmem));
+  if (e == cudaSuccess && dev < kMaxDevices) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
+// Clusters of `size` CTAs that run at a time, 0 if none: fewer than SMs / size, since each
+// lies in one part of the GPU (36 of four, 23 of six, 15 of eight on 152 SMs). Looked up
+// once for a device.
+template <class C>
+int active_clusters(int dev, int sms, int size) {
+  if (size == 1) return sms;
+  static std::atomic<int> known[kMaxDevices][9];
+  int n = dev < kMaxDevices ? known[dev][size].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(size * sms));
+    cfg.blockDim = dim3(kMmThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(size);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, matmul_kernel<C>, &cfg) != cudaSuccess || n < 1) n = -1;
+    if (dev < kMaxDevices) known[dev][size].store(n, std::memory_order_relaxed);
+  }
+  return n > 0 ? n : 0;
+}
+
+struct MmPlan {
+  long long tiles;  // at most
+  int parts;
+  double cost;      // cycles, estimated
+};
+
+// The number of parts that a tile's blocks of K are split into, with the estimated time.
+// The tiles of one group are known here; of several a few may be added, and they are not
+// split.
+template <class C>
+MmPlan plan(const qsfm_matmul_params& p, int dev, int sms, double block_cycles) {
+  const int kb = (p.k + kMmK - 1) / kMmK;
+  const long long col_tiles = (p.n + C::kCols - 1) / C::kCols;
+  MmPlan best = {0, 1, 0};
+  if (p.cu_rows != nullptr) {
+    // every group but one may add a tile that is not full
+    best.tiles = ((long long)p.rows / C::kRows + (p.groups < p.rows ? p.groups : p.rows)) * col_tiles;
+    return best;
+  }
+  best.tiles = (long long)((p.rows + C::kRows - 1) / C::kRows) * col_tiles;
+  for (int parts = 1; parts * C::kCtas <= 8 && (parts == 1 || 2 * parts <= kb); ++parts) {
+    const long long room = active_clusters<C>(dev, sms, parts * C::kCtas);
+    if (room == 0 || (parts > 1 && best.tiles > room)) continue;  // split tiles all run at once
+    const double rounds = double((best.tiles + room - 1) / room);
+    const double cost = rounds * ((kb + parts - 1) / parts * block_cycles + kTileCycles) + (parts > 1 ? kJoinCycles : 0);
+    if (parts == 1 || cost < best.cost) {
+      best.parts = parts;
+      best.cost = cost;
     }
   }
+#ifdef MM_PARTS
+  best.parts = MM_PARTS;
+#endif
+  return best;
+}
+
+template <class C>
+cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int dev, int sms, int* fault, cudaStream_t stream) {
+  cudaError_t e;
+  MmShape s;
+  s.kb = (p.k + kMmK - 1) / kMmK;
+  s.col_blocks = (p.n + 127) / 128;
+  s.col_tiles = (p.n + C::kCols - 1) / C::kCols;
+  s.parts = plan.parts;
   CUtensorMap amap, wmap;
-  if ((e = make_map(p.a, p.k, p.rows, 1, p.a_row_stride, 0, C::kBoxRows, false, &amap)) != cudaSuccess) return e;
-  if ((e = make_map(p.w, p.k, p.n, p.groups, p.w_row_stride, p.w_group_stride, kMmRows, true, &wmap)) != cudaSuccess)
+  if ((e = make_map(p.a, p.k, p.rows, 1, p.a_row_stride, 0, C::kCtas == 2 ? 128 : 32, false, &amap)) != cudaSuccess)
     return e;
-  // at most this many tiles: every group but one may add a tile that is not full
-  const long long most = p.cu_rows == nullptr
-                             ? (long long)((p.rows + kCols - 1) / kCols) * s.col_tiles
-                             : ((long long)p.rows / kCols + (p.groups < p.rows ? p.groups : p.rows)) * s.col_tiles;
+  if ((e = make_map(p.w, p.k, p.n, p.groups, p.w_row_stride, p.w_group_stride, int(C::kWRows), true, &wmap)) != cudaSuccess)
+    return e;
+  const long long room = sms / C::kCtas;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(s.split > 0 ? unsigned(most << s.split) : unsigned(most < sms ? most : sms));
-  cfg.blockDim = dim3(C::kThreads);
+  cfg.gridDim = dim3(unsigned(C::kCtas * (s.parts > 1 ? plan.tiles * s.parts : plan.tiles < room ? plan.tiles : room)));
+  cfg.blockDim = dim3(kMmThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1u << s.split;
+  attr[1].val.clusterDim.x = unsigned(C::kCtas * s.parts);
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = s.split > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<kCols>, p, s, fault, amap, wmap);
+  cfg.numAttrs = C::kCtas * s.parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<C>, p, s, fault, amap, wmap);
 }
 
 }  // namespace
@@ -428,32 +861,26 @@ cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  MmShape s;
-  s.kb = (p.k + kMmK - 1) / kMmK;
-  s.col_tiles = (p.n + kMmRows - 1) / kMmRows;
-  s.split = 0;
-  const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
-  if (MM_PAIR) return launch_matmul_pair(p, sms, fault, stream);
-  int cols = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
-#ifdef MM_COLS
-  cols = MM_COLS;
+  using Pair = Mm<2, 256>;
+  using Wide = Mm<1, 256>;
+  using Small = Mm<1, 128>;
+  if ((e = prepare<Pair>(dev)) != cudaSuccess || (e = prepare<Wide>(dev)) != cudaSuccess ||
+      (e = prepare<Small>(dev)) != cudaSuccess)
+    return e;
+  const MmPlan pair = plan<Pair>(p, dev, sms, kPairCycles), wide = plan<Wide>(p, dev, sms, kWideCycles),
+               small = plan<Small>(p, dev, sms, kSmallCycles);
+#ifdef MM_KERNEL
+  if (MM_KERNEL == 2) return launch_ctas<Pair>(p, pair, dev, sms, fault, stream);
+  if (MM_KERNEL == 1) return launch_ctas<Wide>(p, wide, dev, sms, fault, stream);
+  return launch_ctas<Small>(p, small, dev, sms, fault, stream);
 #endif
-  // the tiles of one group are known here: where they leave SMs without work, the
-  // blocks of K are split, down to two blocks a CTA
-  if (p.cu_rows == nullptr) {
-    const long long tiles = (long long)((p.rows + cols - 1) / cols) * s.col_tiles;
-    while (s.split < 3 && (tiles << (s.split + 1)) <= sms && s.kb >= 4 << s.split) ++s.split;
-#ifdef MM_SPLIT
-    s.split = MM_SPLIT;
-#endif
+  if (p.cu_rows != nullptr) {
+    const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
+    return rows > 128 ? launch_ctas<Pair>(p, pair, dev, sms, fault, stream) : launch_ctas<Wide>(p, wide, dev, sms, fault, stream);
   }
-  switch (cols) {
-    case 16: return launch_cols<16>(p, s, sms, fault, stream);
-    case 32: return launch_cols<32>(p, s, sms, fault, stream);
-    case 64: return launch_cols<64>(p, s, sms, fault, stream);
-    case 128: return launch_cols<128>(p, s, sms, fault, stream);
-    default: return launch_cols<256>(p, s, sms, fault, stream);
-  }
+  if (pair.cost <= wide.cost && pair.cost <= small.cost) return launch_ctas<Pair>(p, pair, dev, sms, fault, stream);
+  return wide.cost <= small.cost ? launch_ctas<Wide>(p, wide, dev, sms, fault, stream)
+                                 : launch_ctas<Small>(p, small, dev, sms, fault, stream);
 }
 
 }  // namespace qsfm
