@@ -22,7 +22,7 @@
 //  * a release of an accumulator at the cluster's scope waits for all the thread's memory
 //    operations: 2800 -> 1250 without;
 //  * single FMAs instead of pairs (fma.rn.f32x2: 64 a thread took longer than 128): 960;
-//  * scales through shared memory, eight blocks at a time, instead of 4-byte loads: 770.
+//  * scales through shared memory, some blocks at a time, instead of 4-byte loads: 770.
 // At 770 the GPU is at its power limit (1660 MHz of 2070 in a loop): 8192 x 8192 x 8192 in
 // 385 us (2.86 PFLOP/s), 420 in a loop; a library's product of the same codes without
 // scales 330 in a loop. Tried: tiles of 192 matrix rows (one round of loads from tensor
@@ -40,6 +40,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "qsfm_device.cuh"
@@ -50,6 +51,7 @@ namespace {
 
 constexpr int kMmK = 128;         // bytes of K per stage: one block of scales
 constexpr int kChunk = 16;        // columns that a part of a split tile joins at a time
+constexpr int kChunkBytes = kChunk * 128 * 4;
 constexpr int kBlockTiles = 8;    // row tiles that are walked before the next of the matrix's
 constexpr int kMaxGroups = 1024;
 constexpr long long kMaxTiles = (1ll << 30) + 1;  // counted at most
@@ -57,12 +59,11 @@ constexpr int kAddWarps = 8;
 constexpr int kMmThreads = 32 * (kAddWarps + 4);
 constexpr int kAddRegs = 224, kOtherRegs = 56, kLaunchRegs = 168;
 static_assert(256 * kAddRegs + 128 * kOtherRegs <= kMmThreads * kLaunchRegs, "registers");
-constexpr int kSlots = 3, kSlotBlocks = 8;  // scales of 8 blocks of K at a time
+constexpr int kSlots = 4, kSlotBlocks = 4;  // scales of 4 blocks of K at a time
 constexpr uint32_t kSlotBlock = 512 + 16;   // 128 rows' scales, one of the matrix's for each half
-constexpr uint32_t kOutWarp = 2048;         // of each adding warp: 32 rows x 64 bytes on their way out
+constexpr uint32_t kOutPart = 2048;         // of an adding warp: 32 rows x 64 bytes on their way out
+constexpr uint32_t kOutBox = 4096;          // 32 rows x 128 bytes, a copy's
 constexpr uint64_t kMmTimeoutNs = 1000000000ull;
-// Cycles that a block of K of a tile takes, and a tile and the join of a split one besides
-constexpr double kPairCycles = 740, kWideCycles = 800, kSmallCycles = 480, kTileCycles = 4000, kJoinCycles = 2500;
 
 // Tiles of 128 kCtas_ rows of a by kCols_ matrix rows.
 template <int kCtas_, int kCols_>
@@ -73,9 +74,14 @@ struct Mm {
   static constexpr uint32_t kTmem = 2 * kCols;                             // two accumulators
   static constexpr uint32_t kABytes = 128 * kMmK, kWRows = kCols / kCtas;  // a CTA's
   static constexpr uint32_t kStage = kABytes + kWRows * kMmK;
-  static constexpr int kStages = kStage > 32768 ? 4 : 6;
+  static constexpr int kStages = 4;
+  // two boxes of output an adding warp, where there is room
+  static constexpr bool kBoxes = kStages * kStage + kAddWarps * 2 * kOutBox <= 200 * 1024;
+  static constexpr uint32_t kOutWarp = kBoxes ? 2 * kOutBox : kOutPart;
   static_assert(kStages % 2 == 0, "an issuing warp's stages are every other one");
   static constexpr uint32_t kOutAt = kStages * kStage, kScaleAt = kOutAt + kAddWarps * kOutWarp;
+  // where a split tile's joined sums are on their way out, behind the parts' sums
+  static constexpr uint32_t kJoinedAt = kScaleAt - kAddWarps * kOutPart;
   static constexpr uint32_t kPrefixAt = kScaleAt + kSlots * kSlotBlocks * kSlotBlock;
   static constexpr uint32_t kBarAt = (kPrefixAt + (kMaxGroups + 4) * 4 + 7) & ~7u;
   static constexpr uint32_t kSmem = kBarAt + 256 + 1024;
@@ -83,17 +89,24 @@ struct Mm {
 };
 
 // barriers; of a pair, those marked * are used in the first CTA alone
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 4;
 constexpr int kBFull = 0 /* * both CTAs' copies */, kBEmpty = kMaxStages, kBTFull = 2 * kMaxStages,
               kBTEmpty = kBTFull + 2 /* * both CTAs' adding warps */, kBDrain = kBTEmpty + 2 /* * of each issuing warp */,
               kBSFull = kBDrain + 2, kBSEmpty = kBSFull + kSlots, kBCount = kBSEmpty + kSlots;
-static_assert(kBCount * 8 + 8 <= 256, "barriers");
+static_assert(kBCount * 8 + 8 <= 256 && kBCount <= 32, "barriers");
 
 struct MmShape {
   int kb;          // blocks of K
   int col_tiles;   // tiles of the matrix's rows
   int col_blocks;  // scales along the matrix's rows
   int parts;       // of a tile's blocks of K, one a CTA or pair of a cluster
+  int tiles;       // of one group of rows (of several they are counted in the kernel)
+  int log_box;     // of the rows of a of a copy
+  int out_boxes;   // the output can be written by copies
+  // of a split tile (no division by the number of parts in the kernel: 100 cycles and more)
+  int most;                // chunks of a part at most
+  uint8_t first[9];        // the first chunk that part q joins
+  uint8_t owner[16];       // the part that joins a chunk
 };
 
 struct MmSmem {
@@ -168,6 +181,16 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
+__device__ __forceinline__ uint32_t cluster_id() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t clusters() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
+  return r;
+}
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -195,12 +218,6 @@ struct MmTile {
 
 // Rows of group g, cut to what there is.
 __device__ __forceinline__ void group_rows(const qsfm_matmul_params& p, int g, int& lo, int& hi, bool& bad) {
-  if (p.cu_rows == nullptr) {
-    lo = 0;
-    hi = p.rows;
-    bad = false;
-    return;
-  }
   const int a = __ldg(p.cu_rows + g), b = __ldg(p.cu_rows + g + 1);
   bad = a < 0 || b < a || b > p.rows;
   lo = min(max(a, 0), p.rows);
@@ -234,37 +251,49 @@ __device__ __forceinline__ void count_tiles(const qsfm_matmul_params& p, int row
   if (lane == 0) prefix[p.groups] = cut(run);
 }
 
-// The first bytes of a copy's destination are this CTA's; it completes on `bar`, of a pair
-// in the first CTA.
+// Copies of a block of K into this CTA's shared memory, by one elected lane of a converged
+// warp (so that what they take stays in uniform registers; a lane of its own takes 150
+// cycles a copy): matrix rows, rows of a (2-D, from row y on). They complete on `bar`, of a
+// pair in the first CTA.
 template <int kCtas>
-__device__ __forceinline__ void mm_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void mm_load_w(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
   if constexpr (kCtas == 2)
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 template <int kCtas>
-__device__ __forceinline__ void mm_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+__device__ __forceinline__ void mm_load_a(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
   if constexpr (kCtas == 2)
     asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void mm_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+      " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}" ::"r"(bar), "r"(bytes)
+      : "memory");
 }
 // Arrives on `bar` (of both CTAs of a pair, `mask`) once the MMAs issued so far have completed.
 template <int kCtas>
@@ -286,8 +315,12 @@ __device__ __forceinline__ void mm_commit(uint64_t* bar, uint32_t mask) {
 __device__ __forceinline__ void arrive_in_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
 // The walk over the tiles of a CTA or pair.
@@ -298,14 +331,17 @@ struct MmWalk {
   __device__ __forceinline__ bool next(const qsfm_matmul_params& p, const MmShape& s, MmTile& t) {
     constexpr int kRows = C::kRows;
     if (at >= total) return false;
-    while (at >= prefix[g + 1]) ++g;
-    int lo, hi;
-    bool bad;
-    group_rows(p, g, lo, hi, bad);
+    int lo = 0, hi = p.rows, local = at;
+    if (p.cu_rows != nullptr) {
+      while (at >= prefix[g + 1]) ++g;
+      bool bad;
+      group_rows(p, g, lo, hi, bad);
+      local -= prefix[g];
+    }
     const int row_tiles = (hi - lo + kRows - 1) / kRows;
-    const int local = at - prefix[g], block = local / (kBlockTiles * s.col_tiles);
+    const int block = row_tiles <= kBlockTiles ? 0 : local / (kBlockTiles * s.col_tiles);
     const int rest = local - block * (kBlockTiles * s.col_tiles), high = min(kBlockTiles, row_tiles - block * kBlockTiles);
-    const int n = rest / high, m = block * kBlockTiles + rest - n * high;
+    const int n = high == 1 ? rest : rest / high, m = block * kBlockTiles + rest - n * high;
     t.g = g;
     t.n0 = n * C::kCols;
     t.row0 = lo + m * kRows;
@@ -326,24 +362,20 @@ struct MmPlace {
 template <class C>
 __device__ void mm_load(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
                         const CUtensorMap* amap, const CUtensorMap* wmap, int* fault) {
-  if ((threadIdx.x & 31) != 0) return;
   uint32_t st = 0, par = 1;
   MmTile t;
   while (walk.next(p, s, t)) {
-    // of a tile of few rows 32 at a time; a pair's are loaded whole
-    const int boxes = C::kCtas == 2 ? 4 : (t.rows + 31) / 32;
-    const uint32_t bytes = C::kCtas * (uint32_t(boxes) * 32 * kMmK + C::kWRows * kMmK);
+    // rows of a tile that are not there are not loaded, but for a pair's
+    const int boxes = C::kCtas == 2 ? 1 : (t.rows + (1 << s.log_box) - 1) >> s.log_box;
+    const uint32_t bytes = C::kCtas * (uint32_t(boxes << s.log_box) + C::kWRows) * kMmK;
     for (int b = at.b0; b < at.b1; ++b) {
-      if (!mm_wait(sm, kBEmpty + st, par, fault)) return;
+      if (!mm_warp_wait(sm, kBEmpty + st, par, fault)) return;
       const uint32_t to = sm.base + st * C::kStage;
-      const uint32_t bar = C::kCtas == 2 ? in_cta(smem_u32(sm.bar(kBFull + st)), at.first) : smem_u32(sm.bar(kBFull + st));
-      if (at.cta == 0) mbar_arrive_expect_tx(sm.bar(kBFull + st), bytes);
-      mm_load_3d<C::kCtas>(to + C::kABytes, wmap, b * kMmK, t.n0 + int(C::kWRows * at.cta), t.g, bar);
-      if constexpr (C::kCtas == 2) {
-        mm_load_2d<C::kCtas>(to, amap, b * kMmK, t.row0 + 128 * int(at.cta), bar);
-      } else {
-        for (int i = 0; i < boxes; ++i) mm_load_2d<C::kCtas>(to + i * 32 * kMmK, amap, b * kMmK, t.row0 + 32 * i, bar);
-      }
+      const uint32_t full = smem_u32(sm.bar(kBFull + st)), bar = C::kCtas == 2 ? in_cta(full, at.first) : full;
+      if (at.cta == 0) mm_expect(full, bytes);
+      mm_load_w<C::kCtas>(to + C::kABytes, wmap, b * kMmK, t.n0 + int(C::kWRows * at.cta), t.g, bar);
+      for (int i = 0; i < boxes; ++i)
+        mm_load_a<C::kCtas>(to + (i * kMmK << s.log_box), amap, b * kMmK, t.row0 + 128 * int(at.cta) + (i << s.log_box), bar);
       if (++st == C::kStages) {
         st = 0;
         par ^= 1;
@@ -387,7 +419,7 @@ __device__ void mm_issue(const qsfm_matmul_params& p, const MmShape& s, const Mm
 }
 
 // ------------------------------------------------------------- scales
-// Eight blocks at a time, on their way to shared memory with the loads: from global
+// Four blocks at a time, on their way to shared memory with the loads: from global
 // memory, a thread's own 4 bytes a block cost the adding warps a third of their time.
 template <class C>
 __device__ void mm_scales(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
@@ -401,18 +433,22 @@ __device__ void mm_scales(const qsfm_matmul_params& p, const MmShape& s, const M
     const float* as[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      as[i] = p.a_scale + size_t(t.row0 + min(128 * int(at.cta) + 32 * i + lane, t.rows - 1)) * p.a_scale_row_stride;
+      as[i] = p.a_scale + size_t(t.row0 + min(128 * int(at.cta) + 32 * i + lane, t.rows - 1)) * p.a_scale_row_stride +
+              size_t(at.b0) * p.a_scale_col_stride;
     // lane 0 and 1: of the two halves
     const int block = min((t.n0 + C::kSums * (lane & 1)) / 128, s.col_blocks - 1);
-    const float* ws = p.w_scale + (size_t(t.g) * s.col_blocks + block) * s.kb;
+    const float* ws = p.w_scale + (size_t(t.g) * s.col_blocks + block) * s.kb + at.b0;
     for (int b0 = at.b0; b0 < at.b1; b0 += kSlotBlocks) {
       if (!mm_warp_wait(sm, kBSEmpty + slot, par, fault)) break;
       uint32_t to = sm.base + C::kScaleAt + slot * kSlotBlocks * kSlotBlock;
       for (int b = b0; b < min(b0 + kSlotBlocks, at.b1); ++b, to += kSlotBlock) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (i < live) cp_async4(to + 4 * (32 * i + lane), as[i] + size_t(b) * p.a_scale_col_stride);
-        if (lane < 2) cp_async4(to + 512 + 4 * lane, ws + b);
+        for (int i = 0; i < 4; ++i) {
+          if (i < live) cp_async4(to + 4 * (32 * i + lane), as[i]);
+          as[i] += p.a_scale_col_stride;
+        }
+        if (lane < 2) cp_async4(to + 512 + 4 * lane, ws);
+        ++ws;
       }
       cp_async_arrive(sm.bar(kBSFull + slot));
       if (++slot == kSlots) {
@@ -494,6 +530,50 @@ __device__ __forceinline__ void store_sums(const qsfm_matmul_params& p, size_t a
   }
 }
 
+// A warp's 32 whole rows of kN columns to the output by copies, which read shared memory
+// while the next tile is added up: boxes of 32 rows x 128 bytes (128-byte swizzle), two at
+// a time. Columns behind the output's are not written.
+template <typename T, int kN>
+__device__ __forceinline__ void store_boxes(const CUtensorMap* omap, const float (&v)[kN], int row, int n0, int n,
+                                            uint32_t stage) {
+  constexpr int kBox = 128 / sizeof(T), kEach = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int c0 = 0; c0 < kN; c0 += kBox) {
+    if (n0 + c0 >= n) break;
+    const uint32_t box = stage + (c0 / kBox % 2) * kOutBox;
+    if (c0 / kBox % 2 == 0) {  // the boxes written last have been read
+      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + kEach * i + kEach / 4 * j;
+        if constexpr (sizeof(T) == 4) {
+          w[j] = __float_as_uint(v[c]);
+        } else if constexpr (__is_same(T, __half)) {
+          w[j] = pack_f16(v[c], v[c + 1]);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      sts_v4(box + 128 * lane + 16 * (i ^ (lane & 7)), make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0)
+      asm volatile(
+          "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n cp.async.bulk.commit_group;" ::"l"(
+              reinterpret_cast<uint64_t>(omap)),
+          "r"(n0 + c0), "r"(row), "r"(box)
+          : "memory");
+  }
+}
+
 // Adds up a tile's blocks; false after a timeout. Warps without rows (kLive false) keep
 // step with the others.
 template <class C, bool kLive>
@@ -549,11 +629,11 @@ __device__ __forceinline__ bool mm_add(const MmShape& s, const MmSmem& sm, MmPla
 
 template <class C>
 __device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSmem& sm, MmWalk<C> walk, MmPlace at,
-                       uint32_t tmem, int* fault) {
+                       uint32_t tmem, const CUtensorMap* omap, int* fault) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row0 = 128 * int(at.cta) + 32 * (warp & 3), half = warp >> 2;
   const uint32_t tempty = in_cta(smem_u32(sm.bar(kBTEmpty)), at.first);
-  uint8_t* stage = sm.ptr + C::kOutAt + kOutWarp * warp;
+  uint8_t* stage = sm.ptr + (s.parts == 1 ? C::kOutAt + C::kOutWarp * warp : C::kJoinedAt + kOutPart * warp);
   uint32_t buf = 0, tpar = 0, slot = 0, spar = 0;
   MmTile t;
   float acc[C::kSums];
@@ -565,46 +645,59 @@ __device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSm
         continue;
       }
       if (!mm_add<C, true>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault)) return;
-      if (cols > 0) store_sums(p, size_t(t.row0 + row0) * p.out_row_stride + n0, acc, rows, cols, stage);
+      if (cols <= 0) continue;
+      if (C::kBoxes && s.out_boxes && rows == 32) {
+        const uint32_t boxes = sm.base + C::kOutAt + C::kOutWarp * warp;
+        if (p.out_type == QSFM_BF16) store_boxes<__nv_bfloat16>(omap, acc, t.row0 + row0, n0, p.n, boxes);
+        else if (p.out_type == QSFM_F16) store_boxes<__half>(omap, acc, t.row0 + row0, n0, p.n, boxes);
+        else store_boxes<float>(omap, acc, t.row0 + row0, n0, p.n, boxes);
+      } else {
+        if (C::kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        store_sums(p, size_t(t.row0 + row0) * p.out_row_stride + n0, acc, rows, cols, stage);
+      }
     }
+    if (C::kBoxes && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     return;
   }
   // The cluster's one tile: its part q adds up the chunks n q / parts .. of the tile's n
   // chunks of 16 columns, in the order of the parts. The sums take the place of the
   // operands, which every CTA of the cluster is through with at the first barrier: of part
-  // q's chunk c from part r at [r][c - first of q][16][128 rows].
-  constexpr int kChunks = C::kCols / kChunk;
+  // q's chunk c from part r at [r][c - first of q][4][128 rows][4 columns].
   bool ok = walk.next(p, s, t);
   const int rows = ok ? min(32, t.rows - row0) : 0;
   if (ok)
     ok = rows > 0 ? mm_add<C, true>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault)
                   : mm_add<C, false>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault);
-  const int part = int(at.first) / C::kCtas, most = (kChunks + s.parts - 1) / s.parts;
+  const int part = int(at.first) / C::kCtas;
   cluster_sync();
   if (ok && lane < rows) {
 #pragma unroll
     for (int c = 0; c < C::kSums; c += kChunk) {
       const int chunk = (C::kSums * half + c) / kChunk;
-      const int owner = ((chunk + 1) * s.parts - 1) / kChunks;  // the last q with n q / parts <= chunk
-      const uint32_t to = in_cta(sm.base + 4 * (((part * most + chunk - kChunks * owner / s.parts) * kChunk) * 128 + (row0 & 127) + lane),
-                                 uint32_t(owner * C::kCtas) + at.cta);
+      const int owner = s.owner[chunk], place = part * s.most + chunk - s.first[owner];
+      const uint32_t to = in_cta(sm.base + place * kChunkBytes + 16 * ((row0 & 127) + lane), uint32_t(owner * C::kCtas) + at.cta);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) st_cluster(to + 512 * i, acc[c + i]);
+      for (int i = 0; i < kChunk; i += 4) st_cluster(to + 512 * i, acc[c + i], acc[c + i + 1], acc[c + i + 2], acc[c + i + 3]);
     }
   }
   cluster_sync();
   if (!ok || rows <= 0) return;
-  const float* sums = reinterpret_cast<const float*>(sm.ptr) + (row0 & 127) + lane;
-  const int c0 = kChunks * part / s.parts, c1 = kChunks * (part + 1) / s.parts;
+  const uint8_t* sums = sm.ptr + 16 * ((row0 & 127) + lane);
+  const int c0 = s.first[part], c1 = s.first[part + 1];
   for (int c = c0 + half; c < c1; c += 2) {
     const int n0 = t.n0 + kChunk * c;
     if (n0 >= p.n) break;
     float v[kChunk];
+    for (int q = 0; q < s.parts; ++q) {
+      const uint8_t* from = sums + (q * s.most + c - c0) * kChunkBytes;
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) v[i] = sums[((c - c0) * kChunk + i) * 128];
-    for (int q = 1; q < s.parts; ++q) {
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) v[i] += sums[((q * most + c - c0) * kChunk + i) * 128];
+      for (int i = 0; i < kChunk; i += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(from + 512 * i);
+        v[i] = q == 0 ? x.x : v[i] + x.x;
+        v[i + 1] = q == 0 ? x.y : v[i + 1] + x.y;
+        v[i + 2] = q == 0 ? x.z : v[i + 2] + x.z;
+        v[i + 3] = q == 0 ? x.w : v[i + 3] + x.w;
+      }
     }
     store_sums(p, size_t(t.row0 + row0) * p.out_row_stride + n0, v, rows, p.n - n0, stage);
   }
@@ -613,8 +706,9 @@ __device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSm
 // ------------------------------------------------------------- the kernel
 template <class C>
 __global__ void __launch_bounds__(kMmThreads, 1)
-    matmul_kernel(const qsfm_matmul_params p, const MmShape s, int* fault, const __grid_constant__ CUtensorMap amap,
-                  const __grid_constant__ CUtensorMap wmap) {
+    matmul_kernel(const __grid_constant__ qsfm_matmul_params p, const __grid_constant__ MmShape s, int* fault,
+                  const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap wmap,
+                  const __grid_constant__ CUtensorMap omap) {
   extern __shared__ uint8_t mm_smem[];
   const uint32_t raw = smem_u32(mm_smem);
   MmSmem sm;
@@ -625,22 +719,18 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   const bool cluster = C::kCtas == 2 || s.parts > 1;
   const uint32_t rank = cluster ? cluster_rank() : 0;
   int* prefix = reinterpret_cast<int*>(sm.ptr + C::kPrefixAt);
-  if (tid == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
-      mbar_init(sm.bar(kBFull + i), 1);
-      mbar_init(sm.bar(kBEmpty + i), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(sm.bar(kBTFull + i), 1);
-      mbar_init(sm.bar(kBTEmpty + i), C::kCtas * kAddWarps);
-      mbar_init(sm.bar(kBDrain + i), 1);
-    }
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(sm.bar(kBSFull + i), 32);
-      mbar_init(sm.bar(kBSEmpty + i), kAddWarps);
-    }
-    *sm.abort_flag() = 0;
+  if (tid < kBCount) {  // a barrier each
+    const int i = tid;
+    mbar_init(sm.bar(i), i >= kBTEmpty && i < kBDrain     ? C::kCtas * kAddWarps
+                         : i >= kBSFull && i < kBSEmpty ? 32
+                         : i >= kBSEmpty                ? kAddWarps
+                                                        : 1);
+    if (tid == 0) *sm.abort_flag() = 0;
     fence_mbar_init();
+  }
+  if (warp == kAddWarps && (tid & 31) == 0) {
+    prefetch_map(&amap);
+    prefetch_map(&wmap);
   }
   if (warp == kAddWarps + 1) {  // of both CTAs
     if constexpr (C::kCtas == 2) {
@@ -654,7 +744,7 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (warp == 0) count_tiles(p, C::kRows, s.col_tiles, prefix, fault);
+  if (warp == 0 && p.cu_rows != nullptr) count_tiles(p, C::kRows, s.col_tiles, prefix, fault);
   tc_fence_before();
   __syncthreads();
   if (cluster) cluster_sync();  // barriers and tensor memory of all CTAs are there
@@ -664,17 +754,17 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   at.cta = rank & (C::kCtas - 1);
   at.first = rank - at.cta;
   const int part = int(at.first) / C::kCtas;
-  at.b0 = int(int64_t(s.kb) * part / s.parts);
-  at.b1 = int(int64_t(s.kb) * (part + 1) / s.parts);
+  at.b0 = s.parts == 1 ? 0 : int(uint32_t(s.kb * part) / uint32_t(s.parts));
+  at.b1 = s.parts == 1 ? s.kb : int(uint32_t(s.kb * (part + 1)) / uint32_t(s.parts));
   MmWalk<C> walk;
   walk.prefix = prefix;
   walk.g = 0;
-  walk.at = int(blockIdx.x / unsigned(C::kCtas * s.parts));
-  walk.step = int(gridDim.x / unsigned(C::kCtas * s.parts));
-  walk.total = prefix[p.groups];
+  walk.at = int(cluster_id());
+  walk.step = int(clusters());
+  walk.total = p.cu_rows != nullptr ? prefix[p.groups] : s.tiles;
   if (warp < kAddWarps) {
     mm_more_registers<kAddRegs>();
-    mm_sum<C>(p, s, sm, walk, at, tmem, fault);
+    mm_sum<C>(p, s, sm, walk, at, tmem, &omap, fault);
   } else {
     mm_fewer_registers<kOtherRegs>();
     if (warp == kAddWarps) {
@@ -746,6 +836,21 @@ cudaError_t make_map(const void* base, int k, int rows, int planes, long long ro
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The output in boxes of 32 rows x 128 bytes.
+cudaError_t make_out_map(const qsfm_matmul_params& p, int size, CUtensorMap* map) {
+  const auto encode = tensor_map_encoder();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const long long stride = p.rows == 1 ? (p.n * (long long)size + 15) & ~15ll : p.out_row_stride * size;
+  const cuuint64_t dims[2] = {cuuint64_t(p.n), cuuint64_t(p.rows)}, strides[1] = {cuuint64_t(stride)};
+  const cuuint32_t box[2] = {cuuint32_t(128 / size), 32}, estr[2] = {1, 1};
+  const CUtensorMapDataType type = p.out_type == QSFM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : p.out_type == QSFM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUresult r = encode(map, type, 2, p.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 constexpr int kMaxDevices = 64;
 
 // Prepares a device for a kernel, once: its shared memory, and that it has the registers
@@ -788,34 +893,53 @@ int active_clusters(int dev, int sms, int size) {
   return n > 0 ? n : 0;
 }
 
+// How long a product takes with tiles of C, in microseconds, as fitted to 16 shapes of 1 to
+// 4096 rows, 1000 to 32768 matrix rows and K of 1024 to 32768 with every number of parts
+// (the shortest of them within 10% of the estimate's choice): a launch, per round of tiles
+// the blocks of K and what a tile takes besides, or the matrices' bytes at the rate that
+// they arrive at, and the join of a split tile, which grows with its rows.
+struct MmTimes {
+  double block, tile, join, join_rows;
+};
+constexpr MmTimes kPairTimes = {0.41, 1.9, 2.0, 3.5}, kWideTimes = {0.43, 2.2, 2.0, 3.5}, kSmallTimes = {0.36, 1.0, 1.5, 2.0};
+constexpr double kLaunchTime = 2.5, kBytesPerUs = 6.2e6;
+
 struct MmPlan {
   long long tiles;  // at most
-  int parts;
-  double cost;      // cycles, estimated
+  int parts;        // of a tile's blocks of K
+  double time;
 };
 
-// The number of parts that a tile's blocks of K are split into, with the estimated time.
-// The tiles of one group are known here; of several a few may be added, and they are not
-// split.
+// The tiles of one group are known here, and where they leave SMs without work they are
+// split; of several groups the tiles are a guess, and not split.
 template <class C>
-MmPlan plan(const qsfm_matmul_params& p, int dev, int sms, double block_cycles) {
+MmPlan plan(const qsfm_matmul_params& p, int dev, int sms, const MmTimes& times) {
   const int kb = (p.k + kMmK - 1) / kMmK;
   const long long col_tiles = (p.n + C::kCols - 1) / C::kCols;
   MmPlan best = {0, 1, 0};
-  if (p.cu_rows != nullptr) {
+  double tiles, rows, groups = 1;
+  if (p.cu_rows == nullptr) {
+    best.tiles = (long long)((p.rows + C::kRows - 1) / C::kRows) * col_tiles;
+    rows = p.rows;
+    tiles = double(best.tiles);
+  } else {
     // every group but one may add a tile that is not full
-    best.tiles = ((long long)p.rows / C::kRows + (p.groups < p.rows ? p.groups : p.rows)) * col_tiles;
-    return best;
+    groups = p.groups < p.rows ? p.groups : p.rows;
+    best.tiles = ((long long)p.rows / C::kRows + (long long)groups) * col_tiles;
+    rows = p.rows / groups;
+    tiles = groups * (rows <= C::kRows / 2 ? 1 : rows / C::kRows + 0.5) * col_tiles;
   }
-  best.tiles = (long long)((p.rows + C::kRows - 1) / C::kRows) * col_tiles;
+  const double bytes = (groups * p.n + p.rows) * p.k / kBytesPerUs;
   for (int parts = 1; parts * C::kCtas <= 8 && (parts == 1 || 2 * parts <= kb); ++parts) {
     const long long room = active_clusters<C>(dev, sms, parts * C::kCtas);
-    if (room == 0 || (parts > 1 && best.tiles > room)) continue;  // split tiles all run at once
-    const double rounds = double((best.tiles + room - 1) / room);
-    const double cost = rounds * ((kb + parts - 1) / parts * block_cycles + kTileCycles) + (parts > 1 ? kJoinCycles : 0);
-    if (parts == 1 || cost < best.cost) {
+    if (parts > 1 && (p.cu_rows != nullptr || best.tiles > room)) continue;  // split tiles all run at once
+    const double rounds = std::ceil(tiles / double(room > 0 ? room : 1));
+    const double work = rounds * ((kb + parts - 1) / parts * times.block + times.tile);
+    const double time = kLaunchTime + (work > bytes ? work : bytes) +
+                        (parts > 1 ? times.join + times.join_rows * (rows < 128 ? rows : 128) / 128 : 0);
+    if (parts == 1 || time < best.time) {
       best.parts = parts;
-      best.cost = cost;
+      best.time = time;
     }
   }
 #ifdef MM_PARTS
@@ -825,18 +949,32 @@ MmPlan plan(const qsfm_matmul_params& p, int dev, int sms, double block_cycles) 
 }
 
 template <class C>
-cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int dev, int sms, int* fault, cudaStream_t stream) {
+cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int rows, int sms, int* fault,
+                        cudaStream_t stream) {
   cudaError_t e;
   MmShape s;
   s.kb = (p.k + kMmK - 1) / kMmK;
   s.col_blocks = (p.n + 127) / 128;
   s.col_tiles = (p.n + C::kCols - 1) / C::kCols;
   s.parts = plan.parts;
+  s.tiles = int(plan.tiles);
+  // as many rows of a as a tile has (a copy takes its time to issue), few where it has few
+  s.log_box = C::kCtas == 2 || rows > 64 ? 7 : rows > 32 ? 6 : 5;
+  constexpr int kChunks = C::kCols / kChunk;
+  s.most = (kChunks + s.parts - 1) / s.parts;
+  for (int q = 0; q <= s.parts; ++q) s.first[q] = uint8_t(kChunks * q / s.parts);
+  for (int q = 0; q < s.parts; ++q)
+    for (int c = s.first[q]; c < s.first[q + 1]; ++c) s.owner[c] = uint8_t(q);
   CUtensorMap amap, wmap;
-  if ((e = make_map(p.a, p.k, p.rows, 1, p.a_row_stride, 0, C::kCtas == 2 ? 128 : 32, false, &amap)) != cudaSuccess)
+  if ((e = make_map(p.a, p.k, p.rows, 1, p.a_row_stride, 0, 1 << s.log_box, false, &amap)) != cudaSuccess)
     return e;
   if ((e = make_map(p.w, p.k, p.n, p.groups, p.w_row_stride, p.w_group_stride, int(C::kWRows), true, &wmap)) != cudaSuccess)
     return e;
+  CUtensorMap omap = amap;  // (not used)
+  const int size = p.out_type == QSFM_F32 ? 4 : 2;
+  s.out_boxes = C::kBoxes && s.parts == 1 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 &&
+                (p.rows == 1 || (p.out_row_stride * size) % 16 == 0);
+  if (s.out_boxes && (e = make_out_map(p, size, &omap)) != cudaSuccess) return e;
   const long long room = sms / C::kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(C::kCtas * (s.parts > 1 ? plan.tiles * s.parts : plan.tiles < room ? plan.tiles : room)));
@@ -851,7 +989,7 @@ cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int dev
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = C::kCtas * s.parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, matmul_kernel<C>, p, s, fault, amap, wmap);
+  return cudaLaunchKernelEx(&cfg, matmul_kernel<C>, p, s, fault, amap, wmap, omap);
 }
 
 }  // namespace
@@ -861,26 +999,25 @@ cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t 
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+  const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
   using Pair = Mm<2, 256>;
   using Wide = Mm<1, 256>;
   using Small = Mm<1, 128>;
   if ((e = prepare<Pair>(dev)) != cudaSuccess || (e = prepare<Wide>(dev)) != cudaSuccess ||
       (e = prepare<Small>(dev)) != cudaSuccess)
     return e;
-  const MmPlan pair = plan<Pair>(p, dev, sms, kPairCycles), wide = plan<Wide>(p, dev, sms, kWideCycles),
-               small = plan<Small>(p, dev, sms, kSmallCycles);
+  const MmPlan pair = plan<Pair>(p, dev, sms, kPairTimes), wide = plan<Wide>(p, dev, sms, kWideTimes),
+               small = plan<Small>(p, dev, sms, kSmallTimes);
 #ifdef MM_KERNEL
-  if (MM_KERNEL == 2) return launch_ctas<Pair>(p, pair, dev, sms, fault, stream);
-  if (MM_KERNEL == 1) return launch_ctas<Wide>(p, wide, dev, sms, fault, stream);
-  return launch_ctas<Small>(p, small, dev, sms, fault, stream);
+  if (MM_KERNEL == 2) return launch_ctas<Pair>(p, pair, rows, sms, fault, stream);
+  if (MM_KERNEL == 1) return launch_ctas<Wide>(p, wide, rows, sms, fault, stream);
+  return launch_ctas<Small>(p, small, rows, sms, fault, stream);
 #endif
-  if (p.cu_rows != nullptr) {
-    const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
-    return rows > 128 ? launch_ctas<Pair>(p, pair, dev, sms, fault, stream) : launch_ctas<Wide>(p, wide, dev, sms, fault, stream);
-  }
-  if (pair.cost <= wide.cost && pair.cost <= small.cost) return launch_ctas<Pair>(p, pair, dev, sms, fault, stream);
-  return wide.cost <= small.cost ? launch_ctas<Wide>(p, wide, dev, sms, fault, stream)
-                                 : launch_ctas<Small>(p, small, dev, sms, fault, stream);
+  // (the pair first where it is as good: it reads a third less)
+  if (pair.time <= 1.03 * wide.time && pair.time <= 1.03 * small.time)
+    return launch_ctas<Pair>(p, pair, rows, sms, fault, stream);
+  return wide.time <= small.time ? launch_ctas<Wide>(p, wide, rows, sms, fault, stream)
+                                 : launch_ctas<Small>(p, small, rows, sms, fault, stream);
 }
 
 }  // namespace qsfm
