@@ -687,6 +687,16 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _current_stream(index: int) -> int:
+    """The handle of a device's current stream: as torch's generated code asks
+    for it where there is that call (the public one makes a Stream object, 2 us
+    a call)."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class _Launch:
     """A parameter block with its device: calls run on that device, and the
     tensors it points to live as long as it does."""
@@ -699,8 +709,9 @@ class _Launch:
         import torch
 
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        at = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+            at = _current_stream(self.device.index)
+        else:
+            at = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
         if self.device.index == torch.cuda.current_device():
             _check(fn, getattr(lib(), fn)(self.ref, at))
         else:
