@@ -68,8 +68,10 @@ struct QuantizeShape {
   uint32_t total;    // rows * groups
   int k;             // elements of a row
   uint32_t units;    // fours of groups that a warp takes at a time
-  FastDiv groups_of; // by the groups of a row (kTurns: of a head row)
-  FastDiv heads_of;  // kTurns: by the heads; else by the groups of a head row
+  FastDiv groups_of; // by the groups of a row (kHeads: by those of a head row that a launch takes)
+  FastDiv heads_of;  // kHeads: by the heads; else by the groups of a head row
+  uint32_t of_head;  // kHeads: groups of a head row; those from first on, without the one at skip
+  uint32_t first, skip;
 };
 
 // 8 consecutive elements as they are read, and in fp32.
@@ -278,7 +280,7 @@ struct Item {
 
   // Drops the row where its position says so (after all loads are on their way).
   __device__ __forceinline__ void check(const qsfm_quantize_params& p, int* fault) {
-    if (pos < 0 || (kTurns && row >= 0 && pos >= p.max_positions)) {
+    if (pos < 0 || (p.rope_dim > 0 && row >= 0 && pos >= p.max_positions)) {
       if (pos >= 0 && (threadIdx.x & (kQLanes - 1)) == 0) atomicOr(fault, QSFM_FAULT_POSITION);
       row = -1;
       live[0] = live[1] = false;
@@ -549,9 +551,9 @@ __device__ __forceinline__ void finish(const qsfm_quantize_params& p, const Quan
 }
 
 // kItems times four groups per warp: neighbours in a row or, where a part of each head is
-// turned, the same group of four heads in a row, so that what is turned is in warps of
-// its own.
-template <typename T, int kMode, int kItems>
+// turned (kHeads), the same group of four heads in a row, so that what is turned is in
+// warps of its own.
+template <typename T, int kMode, int kItems, bool kHeads>
 __global__ void __launch_bounds__(32 * kQWarps, blocks_per_sm(kMode))
     quantize_kernel(const __grid_constant__ qsfm_quantize_params p, const __grid_constant__ QuantizeShape s, int* fault) {
   grid_dependency_wait();
@@ -563,10 +565,12 @@ __global__ void __launch_bounds__(32 * kQWarps, blocks_per_sm(kMode))
   size_t scale_at[kItems];
 #pragma unroll
   for (int u = 0; u < kItems; ++u) {
-    if constexpr (Item<T, kMode>::kTurns) {
-      const uint32_t four = s.groups_of.div(first + u), g = first + u - four * s.groups_of.d;
-      const uint32_t head = 4 * four + quarter, row = s.heads_of.div(head), h = head - row * uint32_t(p.heads);
-      scale_at[u] = size_t(head) * s.groups_of.d + g;
+    if constexpr (kHeads) {
+      const uint32_t four = s.groups_of.div(first + u), head = 4 * four + quarter, row = s.heads_of.div(head);
+      const uint32_t h = head - row * uint32_t(p.heads);
+      uint32_t g = first + u - four * s.groups_of.d + s.first;
+      if (g >= s.skip) ++g;
+      scale_at[u] = size_t(head) * s.of_head + g;
       item[u].load(p, s, first + u < s.units ? row : 0xffffffffu, h, int(g) * kQGroup, int(h) * p.dim + int(g) * kQGroup, fault);
     } else {
       const uint32_t f = 4 * (first + u) + quarter, row = s.groups_of.div(f), g = f - row * s.groups_of.d;
@@ -585,29 +589,54 @@ __global__ void __launch_bounds__(32 * kQWarps, blocks_per_sm(kMode))
   }
 }
 
+template <typename T, int kMode, int kItems, bool kHeads>
+cudaError_t launch_units(const qsfm_quantize_params& p, const QuantizeShape& s, int* fault, cudaStream_t stream) {
+  const uint32_t warps = (s.units + kItems - 1) / kItems;
+  return launch_after_predecessor(quantize_kernel<T, kMode, kItems, kHeads>, dim3((warps + kQWarps - 1) / kQWarps),
+                                  dim3(32 * kQWarps), 0, stream, p, s, fault);
+}
+
+// Units of four groups up to which a warp takes one, so that they spread over the SMs;
+// with more it has 64 bytes of the inputs a lane on their way.
+constexpr uint32_t kFewUnits = 152 * 32;
+
 template <typename T, int kMode>
 cudaError_t launch_mode(const qsfm_quantize_params& p, int* fault, cudaStream_t stream) {
+  constexpr int kItems = sizeof(T) == 4 || kMode == kGated ? 1 : 2;
   QuantizeShape s;
   s.k = p.heads * p.dim;
-  const uint32_t groups = uint32_t((s.k + kQGroup - 1) / kQGroup), of_head = uint32_t((p.dim + kQGroup - 1) / kQGroup);
-  if (Item<T, kMode>::kTurns) {
-    s.groups_of.set(of_head);
+  const uint32_t groups = uint32_t((s.k + kQGroup - 1) / kQGroup);
+  s.of_head = uint32_t((p.dim + kQGroup - 1) / kQGroup);
+  s.first = 0;
+  s.skip = 0xffffffffu;
+  if constexpr (Item<T, kMode>::kTurns) {
+    const uint32_t fours = uint32_t((uint64_t(p.rows) * uint32_t(p.heads) + 3) / 4);
     s.heads_of.set(uint32_t(p.heads));
-    s.units = uint32_t((uint64_t(p.rows) * uint32_t(p.heads) + 3) / 4) * of_head;
+    s.groups_of.set(s.of_head);
+    s.units = fours * s.of_head;
+    if (s.units <= kFewUnits) return launch_units<T, kMode, 1, true>(p, s, fault, stream);
+    // of many, the groups that nothing is turned of in a launch of the kernel for them,
+    // which has twice the warps on an SM (4099 tokens of 64 heads: 91 us in one launch)
+    const uint32_t turned = uint32_t(p.rope_offset) / kQGroup;
+    if (s.of_head > 1) {
+      QuantizeShape rest = s;
+      rest.groups_of.set(s.of_head - 1);
+      rest.units = fours * (s.of_head - 1);
+      rest.skip = turned;
+      const cudaError_t e = launch_units<T, kPlain, kItems, true>(p, rest, fault, stream);
+      if (e != cudaSuccess) return e;
+    }
+    s.groups_of.set(1);
+    s.units = fours;
+    s.first = turned;
+    return launch_units<T, kMode, kItems, true>(p, s, fault, stream);
   } else {
     s.groups_of.set(groups);
-    s.heads_of.set(of_head);
+    s.heads_of.set(s.of_head);
     s.units = (uint32_t(p.rows) * groups + 3) / 4;
+    if (kItems == 1 || s.units <= kFewUnits) return launch_units<T, kMode, 1, false>(p, s, fault, stream);
+    return launch_units<T, kMode, kItems, false>(p, s, fault, stream);
   }
-  // few groups: four a warp, so that they spread over the SMs; many: 64 bytes of the
-  // inputs a lane, for the bytes in flight
-  constexpr int kItems = sizeof(T) == 4 || kMode == kGated ? 1 : 2;
-  if (kItems == 1 || s.units <= 152 * 32)
-    return launch_after_predecessor(quantize_kernel<T, kMode, 1>, dim3((s.units + kQWarps - 1) / kQWarps),
-                                    dim3(32 * kQWarps), 0, stream, p, s, fault);
-  const uint32_t warps = (s.units + kItems - 1) / kItems;
-  return launch_after_predecessor(quantize_kernel<T, kMode, kItems>, dim3((warps + kQWarps - 1) / kQWarps),
-                                  dim3(32 * kQWarps), 0, stream, p, s, fault);
 }
 
 template <typename T>

@@ -677,8 +677,8 @@ typedef struct qsfm_quantize_params {
 /* Defaults: one head, pointers NULL. */
 void qsfm_quantize_params_init(qsfm_quantize_params* p);
 
-/* One launch on `stream` (none for T = 0, whose pointers are not looked at); no
- * workspace, nothing read back. Errors: QSFM_ERR_INVALID_ARG,
+/* One launch on `stream`, two for many heads that are turned (none for T = 0, whose
+ * pointers are not looked at); no workspace, nothing read back. Errors: QSFM_ERR_INVALID_ARG,
  * QSFM_ERR_UNSUPPORTED (K not a multiple of 16, heads of a dim that is not one of
  * 128, rope_dim not built, T ceil(K / 128) of 2^31 - 2^16 or more, a stride of 2^31 or more). */
 qsfm_status qsfm_quantize_rows(const qsfm_quantize_params* p, void* stream);
