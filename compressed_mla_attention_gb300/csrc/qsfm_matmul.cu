@@ -942,9 +942,6 @@ MmPlan plan(const qsfm_matmul_params& p, int dev, int sms, const MmTimes& times)
       best.time = time;
     }
   }
-#ifdef MM_PARTS
-  best.parts = MM_PARTS;
-#endif
   return best;
 }
 
@@ -1008,11 +1005,6 @@ cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t 
     return e;
   const MmPlan pair = plan<Pair>(p, dev, sms, kPairTimes), wide = plan<Wide>(p, dev, sms, kWideTimes),
                small = plan<Small>(p, dev, sms, kSmallTimes);
-#ifdef MM_KERNEL
-  if (MM_KERNEL == 2) return launch_ctas<Pair>(p, pair, rows, sms, fault, stream);
-  if (MM_KERNEL == 1) return launch_ctas<Wide>(p, wide, rows, sms, fault, stream);
-  return launch_ctas<Small>(p, small, rows, sms, fault, stream);
-#endif
   // (the pair first where it is as good: it reads a third less)
   if (pair.time <= 1.03 * wide.time && pair.time <= 1.03 * small.time)
     return launch_ctas<Pair>(p, pair, rows, sms, fault, stream);

@@ -292,6 +292,30 @@ def test_products_match_the_oracle(cuda_device, shape):
         assert np.all(np.abs(f64(out) - ref) <= tolerance(ref, mag, sa.shape[1], dtype))
 
 
+#: few rows over a long K (split over many parts, odd numbers of them among them), pairs of
+#: row tiles, many row tiles; columns that end inside a tile
+LARGE = [(1, 4096, 32768), (48, 2048, 16384), (16, 8192, 1024), (130, 4096, 8192), (256, 4096, 16384), (200, 2000, 4112),
+         (300, 640, 16400), (640, 2000, 4112), (2100, 1800, 1040), (5000, 520, 272), (1500, 1500, 4096), (9000, 264, 144)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES, ids=str)
+@pytest.mark.parametrize("shape", LARGE, ids=str)
+def test_large_products_of_whole_numbers_are_exact(cuda_device, shape, dtype):
+    """Against torch's product in 64 bits, which is exact for these. The sums of the
+    terms' magnitudes stay below 2^24 of the smallest unit, 2^-4, so that fp32 sums
+    are exact in any order."""
+    m, n, k = shape
+    a, sa, w, sw = whole_numbers(m, n, k, 1, torch.Generator().manual_seed(m + n + k), cuda_device)
+    wide = torch.full((m, n + 8), 9.0, dtype=dtype, device=cuda_device)  # rows with a gap behind them
+    Q.scaled_matmul(a, sa, w[0], sw[0], out=wide[:, :n])
+    clean()
+    left = a.double() * sa.double().repeat_interleave(128, 1)[:, :k]
+    right = w[0].double() * sw[0].double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    assert float((left.abs() @ right.abs().t()).max()) * 16 < 2 ** 24
+    assert torch.equal(wide[:, :n], (left @ right.t()).float().to(dtype))
+    assert torch.all(wide[:, n:] == 9)
+
+
 def test_products_repeat_bit_for_bit(cuda_device):
     for m, n, k in ((3, 512, 4096), (200, 384, 8192), (600, 512, 1024)):
         a, sa, w, sw = real_numbers(m, n, k, 1, torch.Generator().manual_seed(m), cuda_device)
@@ -368,6 +392,8 @@ GROUPS = {
     "around the tiles": ([0, 15, 31, 48, 111, 175, 240, 367, 495, 624, 879, 1135, 1392], 136, 144, 1400),
     "many": (list(np.cumsum([0] + [(7 * i) % 5 for i in range(300)])), 64, 128, 600),
     "the most": (list(np.minimum(np.arange(1025) // 3, 200)), 32, 16, 200),
+    "pairs": ([0, 256, 511, 1100, 1101, 1900], 392, 656, 1930),
+    "pairs of many": ([3] + [3 + 300 * (i + 1) - 7 * i for i in range(12)], 128, 400, 3700),
 }
 
 
