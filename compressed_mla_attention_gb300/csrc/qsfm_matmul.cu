@@ -44,6 +44,7 @@
 #include <mutex>
 
 #include "qsfm_device.cuh"
+#include "qsfm_divide.cuh"
 #include "qsfm_internal.h"
 
 namespace qsfm {
@@ -101,6 +102,8 @@ struct MmShape {
   int col_blocks;  // scales along the matrix's rows
   int parts;       // of a tile's blocks of K, one a CTA or pair of a cluster
   int tiles;       // of one group of rows (of several they are counted in the kernel)
+  FastDiv block_div;            // by the tiles of kBlockTiles row tiles
+  FastDiv high_div[kBlockTiles + 1];  // by the row tiles of a block
   int log_box;     // of the rows of a of a copy
   int out_boxes;   // the output can be written by copies
   // of a split tile (no division by the number of parts in the kernel: 100 cycles and more)
@@ -339,9 +342,9 @@ struct MmWalk {
       local -= prefix[g];
     }
     const int row_tiles = (hi - lo + kRows - 1) / kRows;
-    const int block = row_tiles <= kBlockTiles ? 0 : local / (kBlockTiles * s.col_tiles);
+    const int block = int(s.block_div.div(uint32_t(local)));
     const int rest = local - block * (kBlockTiles * s.col_tiles), high = min(kBlockTiles, row_tiles - block * kBlockTiles);
-    const int n = high == 1 ? rest : rest / high, m = block * kBlockTiles + rest - n * high;
+    const int n = int(s.high_div[high].div(uint32_t(rest))), m = block * kBlockTiles + rest - n * high;
     t.g = g;
     t.n0 = n * C::kCols;
     t.row0 = lo + m * kRows;
@@ -539,38 +542,42 @@ __device__ __forceinline__ void store_boxes(const CUtensorMap* omap, const float
   constexpr int kBox = 128 / sizeof(T), kEach = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int c0 = 0; c0 < kN; c0 += kBox) {
+  for (int c0 = 0; c0 < kN; c0 += 2 * kBox) {
     if (n0 + c0 >= n) break;
-    const uint32_t box = stage + (c0 / kBox % 2) * kOutBox;
-    if (c0 / kBox % 2 == 0) {  // the boxes written last have been read
-      if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-      __syncwarp();
-    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last boxes have been read
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint32_t w[4];
+    for (int h = 0; h < 2 * kBox && c0 + h < kN; h += kBox) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = c0 + kEach * i + kEach / 4 * j;
-        if constexpr (sizeof(T) == 4) {
-          w[j] = __float_as_uint(v[c]);
-        } else if constexpr (__is_same(T, __half)) {
-          w[j] = pack_f16(v[c], v[c + 1]);
-        } else {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(v[c], v[c + 1]);
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 8; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = c0 + h + kEach * i + kEach / 4 * j;
+          if constexpr (sizeof(T) == 4) {
+            w[j] = __float_as_uint(v[c]);
+          } else if constexpr (__is_same(T, __half)) {
+            w[j] = pack_f16(v[c], v[c + 1]);
+          } else {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(v[c], v[c + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&x);
+          }
         }
+        sts_v4(stage + (h / kBox) * kOutBox + 128 * lane + 16 * (i ^ (lane & 7)), make_uint4(w[0], w[1], w[2], w[3]));
       }
-      sts_v4(box + 128 * lane + 16 * (i ^ (lane & 7)), make_uint4(w[0], w[1], w[2], w[3]));
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0)
-      asm volatile(
-          "cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];\n cp.async.bulk.commit_group;" ::"l"(
-              reinterpret_cast<uint64_t>(omap)),
-          "r"(n0 + c0), "r"(row), "r"(box)
-          : "memory");
+    if (lane == 0) {
+#pragma unroll
+      for (int h = 0; h < 2 * kBox && c0 + h < kN; h += kBox)
+        if (n0 + c0 + h < n)
+          asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                           reinterpret_cast<uint64_t>(omap)),
+                       "r"(n0 + c0 + h), "r"(row), "r"(stage + (h / kBox) * kOutBox)
+                       : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
   }
 }
 
@@ -955,6 +962,8 @@ cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int row
   s.col_tiles = (p.n + C::kCols - 1) / C::kCols;
   s.parts = plan.parts;
   s.tiles = int(plan.tiles);
+  s.block_div.set(uint32_t(kBlockTiles * s.col_tiles));
+  for (int i = 1; i <= kBlockTiles; ++i) s.high_div[i].set(uint32_t(i));
   // as many rows of a as a tile has (a copy takes its time to issue), few where it has few
   s.log_box = C::kCtas == 2 || rows > 64 ? 7 : rows > 32 ? 6 : 5;
   constexpr int kChunks = C::kCols / kChunk;

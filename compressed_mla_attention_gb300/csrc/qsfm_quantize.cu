@@ -32,6 +32,7 @@
 #include <type_traits>
 
 #include "qsfm_device.cuh"
+#include "qsfm_divide.cuh"
 #include "qsfm_internal.h"
 
 namespace qsfm {
@@ -49,19 +50,6 @@ enum QuantizeMode { kPlain = 0, kAdjacent = 1, kHalves = 2, kGated = 3 };  // th
 // Blocks on an SM, from what was measured: 16384 bf16 rows of 8192 in 58 us with 6, 62 with
 // 4; gated 32 (5), 33 (4); turned 91 (4), 96 (5, an item a warp), 106 (3).
 constexpr int blocks_per_sm(int mode) { return mode == kPlain ? 6 : mode == kGated ? 5 : 4; }
-
-// Division of 31-bit numbers by an invariant d: q = (n * m) >> (32 + s) with
-// m = ceil(2^(32 + s) / d), s = ceil(log2 d) - 1 (exact for n < 2^31).
-struct FastDiv {
-  uint32_t d, m, s;
-  __host__ void set(uint32_t div) {
-    d = div;
-    s = 0;
-    while ((2u << s) < div) ++s;
-    m = div <= 1 ? 0 : uint32_t(((1ull << (32 + s)) + div - 1) / div);
-  }
-  __device__ __forceinline__ uint32_t div(uint32_t n) const { return d <= 1 ? n : __umulhi(n, m) >> s; }
-};
 
 struct QuantizeShape {
   uint32_t groups;   // scales of a row
