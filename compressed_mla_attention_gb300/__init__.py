@@ -921,8 +921,9 @@ def _head_rows(name: str, t, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected " + (str(tuple(shape)) if shape else "[T, K] or [T, N, D]"))
     if int(t.shape[-1]) > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
-    heads = int(t.shape[1]) if t.dim() == 3 else 1
-    return int(t.shape[0]), heads, int(t.shape[-1]), t.stride(0), t.stride(1) if heads > 1 else 0
+    rows, heads = int(t.shape[0]), int(t.shape[1]) if t.dim() == 3 else 1
+    # the stride of an axis of one entry is not stepped along, and may be anything
+    return rows, heads, int(t.shape[-1]), t.stride(0) if rows > 1 else 0, t.stride(1) if heads > 1 else 0
 
 
 def make_quantize_params(

@@ -221,6 +221,42 @@ def test_strided_rows_and_empty_ones(cuda_device):
     assert codes.shape == (0, 640)
 
 
+def test_one_row_of_any_stride(cuda_device):
+    x = torch.randn(3, 261, generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).to(cuda_device)
+    x = x[:1, :256]  # 522 bytes to the next row, which there is not
+    codes, scale = Q.quantize_rows(x, gate=x)
+    again, _ = Q.quantize_rows(x.clone(), gate=x.clone())
+    assert torch.equal(codes, again)
+    out = Q.scaled_matmul(codes, scale, codes, scale)
+    clean()
+    assert out.shape == (1, 1)
+
+
+def test_rows_past_2_to_the_31_elements(cuda_device):
+    """Offsets that do not fit 31 bits: input, codes and a product's output."""
+    dev, n = cuda_device, 66000
+    if torch.cuda.mem_get_info(dev)[0] < 30 << 30:
+        pytest.skip("not enough memory")
+    x = torch.empty(n, 32768, dtype=torch.bfloat16, device=dev)
+    x[:-3] = 1.0
+    x[-3:] = torch.randn(3, 32768, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).to(dev)
+    codes, scale = Q.quantize_rows(x)
+    last, last_scale = Q.quantize_rows(x[-3:].clone())
+    assert torch.equal(codes[-3:], last) and torch.equal(scale[-3:], last_scale)
+    turned = dict(cos_sin=table_of(100, 64, dev), rope_offset=64, inverse=True)
+    at = torch.arange(n, dtype=torch.int32, device=dev) % 100
+    Q.quantize_rows(x.view(n, 64, 512), positions=at, codes=codes, scale=scale, **turned)
+    last, last_scale = Q.quantize_rows(x[-3:].clone().view(3, 64, 512), positions=at[-3:].clone(), **turned)
+    assert torch.equal(codes[-3:], last.view(3, -1)) and torch.equal(scale[-3:], last_scale)
+    del x
+    a, sa = codes[:, :128], scale[:, :1]  # strided rows
+    w, sw = last.view(-1, 128)[:256].repeat(128, 1), torch.ones(256, 1, device=dev)
+    out = Q.scaled_matmul(a, sa, w, sw)
+    small = Q.scaled_matmul(a[-3:].clone(), sa[-3:].clone(), w, sw)
+    clean()
+    assert out.numel() > 2 ** 31 and torch.equal(out[-3:], small)
+
+
 def test_index_into_no_rows(cuda_device):
     c, s = Q.quantize_rows(torch.empty(0, 256, device=cuda_device), row_index=i32([0, -1], cuda_device))
     torch.cuda.synchronize()
