@@ -824,6 +824,22 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return encode;
 }
 
+// A tensor map by `call`. The encoder is a driver call and wants a context, which a host
+// thread has from its first runtime call that needs one: the product may be that thread's
+// first (what it asks of the device before is answered without), so it is bound here.
+template <class Call>
+cudaError_t encode_map(const Call& call) {
+  CUresult r = call();
+  if (r == CUDA_ERROR_INVALID_CONTEXT || r == CUDA_ERROR_NOT_INITIALIZED) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaSetDevice(dev);
+    if (e != cudaSuccess) return e;
+    r = call();
+  }
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Bytes [planes, rows, k] in boxes of box_rows x 128, what lies outside read as zero.
 // (A stride of a dimension of length 1 is not used: the encoder still wants it to be a
 // multiple of 16 that is not below the extent within.)
@@ -837,10 +853,11 @@ cudaError_t make_map(const void* base, int k, int rows, int planes, long long ro
   const cuuint64_t strides[2] = {cuuint64_t(row_stride), cuuint64_t(plane_stride)};
   const cuuint32_t box[3] = {kMmK, cuuint32_t(box_rows), 1};
   const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, is3d ? 3 : 2, const_cast<void*>(base), dims, strides,
-                            box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode_map([&] {
+    return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, is3d ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 // The output in boxes of 32 rows x 128 bytes.
@@ -853,9 +870,10 @@ cudaError_t make_out_map(const qsfm_matmul_params& p, int size, CUtensorMap* map
   const CUtensorMapDataType type = p.out_type == QSFM_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : p.out_type == QSFM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                             : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUresult r = encode(map, type, 2, p.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  return encode_map([&] {
+    return encode(map, type, 2, p.out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 constexpr int kMaxDevices = 64;

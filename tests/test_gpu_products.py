@@ -2,6 +2,8 @@
 products, products by group of rows) with the fp64 oracle, each alone and in
 the order a step runs them around the indexer and the attention."""
 
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -490,6 +492,44 @@ def test_bad_group_rows_are_cut_and_reported(cuda_device):
 
 
 # ------------------------------------------------------------------ streams, graphs, steps
+def test_products_as_the_first_call_of_a_thread(cuda_device):
+    """Host threads that have not used CUDA before, each on a stream of its own, at
+    once; the first call of the process is the main thread's."""
+    dev = cuda_device
+    gen = torch.Generator().manual_seed(3)
+    x = torch.randn(300, 1024, generator=gen).to(dev)
+    w = torch.randint(0, 120, (512, 1024), generator=gen, dtype=torch.uint8).to(dev)
+    sw = torch.rand(4, 8, generator=gen).to(dev)
+    codes, scale = Q.quantize_rows(x)
+    want = [Q.scaled_matmul(codes[:m], scale[:m], w, sw) for m in (1, 300)]
+    torch.cuda.synchronize(dev)
+    outs = [[torch.zeros_like(v) for v in want] for _ in range(4)]
+    streams = [torch.cuda.Stream(dev) for _ in outs]
+    errors = []
+
+    def run(out, stream):
+        try:
+            params = [
+                Q.make_matmul_params(a=codes[: v.shape[0]], a_scale=scale[: v.shape[0]], w=w, w_scale=sw, out=v)
+                for v in out
+            ]
+            for _ in range(20):
+                for p in params:
+                    Q.matmul(p, stream=stream)
+        except Exception as e:  # (an exception of a thread would be lost)
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=a) for a in zip(outs, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize(dev)
+    assert not errors, errors
+    assert all(torch.equal(g, v) for out in outs for g, v in zip(out, want))
+    assert Q.device_status() == 0
+
+
 def test_other_streams_and_captured_calls(cuda_device):
     """Calls on streams of their own, two at once; a captured step replayed on
     other inputs in the same buffers, between eager calls."""
