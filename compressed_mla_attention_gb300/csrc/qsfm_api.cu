@@ -462,7 +462,7 @@ qsfm_status check_quantize(const qsfm_quantize_params* pp) {
   return overlap(outs[0].at, outs[0].n, outs[1].at, outs[1].n) ? QSFM_ERR_INVALID_ARG : QSFM_OK;
 }
 
-constexpr long long kMaxStride = 1ll << 37;  // elements; times a number of rows it stays within 64 bits
+constexpr long long kMaxStride = 1ll << 36;  // elements; times a number of rows of 4 bytes it stays within 64 bits
 constexpr int kMaxMatmulGroups = 1024;
 constexpr int kMaxMatmulSize = 1 << 24;
 constexpr long long kMaxMatmulTiles = 1 << 30;  // of 128 x 16 outputs, the smallest

@@ -9,30 +9,36 @@
 // thread's 128 sums are those of one row with 128 matrix rows, which have one scale, so a
 // block's factor is one number a thread.
 //
-// A tile is 128 rows of a by 256 matrix rows, or, where a group has more than 128 rows on
-// average, 256 by 256 of a pair of CTAs (cta_group::2): each loads its own 128 rows of a
-// and half of the matrix's, 32 KB a block of K instead of 48. With few rows the matrix's
-// bytes are what a product has to read, and a CTA has 128 KB of them on their way; rows of
-// a that are not there are not loaded, and warps without rows do not add.
+// Three kernels, by the estimate of their time at MmTimes: tiles of 256 rows of a by 256
+// matrix rows of a pair of CTAs (cta_group::2), each of which loads its own 128 rows of a
+// and half of the matrix's, 32 KB a block of K instead of 48; 128 by 256 of a CTA, whose
+// clusters take more parts; and 128 by 128, of which there are more and whose sums are
+// fewer to join. (2048 x 4096 x 4096: 34.2, 36.0, 51.5 us; 256 x 4096 x 32768 in parts:
+// 48.6, 41.7, 54.2; 128 x 4096 x 4096 in parts: 15.1, 13.0, 10.4.) With few rows the
+// matrix's bytes are what a product has to read, four stages of 16 or 32 KB a CTA on their
+// way; rows of a that are not there are not loaded, and warps without rows do not add.
 //
-// Per CTA: a warp that loads (TMA, 128-byte swizzle), two that issue MMAs (of a pair's
-// first CTA alone), one that copies scales, eight that add up and store. A block's MMAs
-// take 512 cycles; meanwhile the eight warps read the previous one's products out of
+// Per CTA: a warp that loads (TMA, 128-byte swizzle), two that issue MMAs in turn (of a
+// pair's first CTA alone), one that copies scales, eight that add up and store. A block's
+// MMAs take 512 cycles; meanwhile the eight warps read the previous one's products out of
 // tensor memory and add them up. What it took (cycles a block of a pair, K = 8192):
 //  * a release of an accumulator at the cluster's scope waits for all the thread's memory
 //    operations: 2800 -> 1250 without;
 //  * single FMAs instead of pairs (fma.rn.f32x2: 64 a thread took longer than 128): 960;
-//  * scales through shared memory, some blocks at a time, instead of 4-byte loads: 770.
-// At 770 the GPU is at its power limit (1660 MHz of 2070 in a loop): 8192 x 8192 x 8192 in
-// 385 us (2.86 PFLOP/s), 420 in a loop; a library's product of the same codes without
-// scales 330 in a loop. Tried: tiles of 192 matrix rows (one round of loads from tensor
-// memory, an earlier release) 460; two MMAs of 128 matrix rows each 500, before the last
-// step.
+//  * scales through shared memory, some blocks at a time, instead of 4-byte loads: 770;
+//  * a second warp that issues: 715.
+// What is left is the way of an accumulator: commit, products read, release, next MMAs,
+// some 1300 cycles over the two that tensor memory has room for. 8192 x 8192 x 8192 takes
+// 380 us (2.9 PFLOP/s); in a loop the GPU is at its power limit and takes 420, a library's
+// product of the same codes without scales 330. Slower or no faster: tiles of 192 matrix
+// rows, two MMAs of 128 matrix rows each, 32 products of a thread at a time, six stages,
+// a test of the next accumulator ahead of time, waits by one lane of a warp.
 //
 // A CTA (or pair) walks tiles in turn, eight row tiles of a group before the next of the
 // matrix's. Where the tiles of one group leave SMs without work, a tile's blocks of K are
 // split over a cluster, whose CTAs exchange their sums through distributed shared memory
-// and add them in the order of the CTAs.
+// and add them in the order of the CTAs (1 x 4096 x 4096: 8.0 us in four parts, 13.8 in
+// one).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

@@ -21,10 +21,16 @@
 //    2^-24, and its last four bits are cut: what lies on a border is then on it, what
 //    does not stays on its side.
 //  * Elsewhere (y computed, or fp32) an element is next to a border by chance. The
-//    quotient, within a few units (error()), is converted twice, times 1 - error and
+//    quotient, within a few units (`error` in finish()), is converted twice, times 1 - error and
 //    1 + error: where both give the same code, that is the code. Otherwise the sign of
 //    448 |y| - m A decides, m the border (0: the even code), with y and A as sums of two
 //    fp32 values and the products' roundings carried: about 46 bits.
+//
+// Measured (a call among others in a graph): 16384 bf16 rows of 8192 in 58 us, 7.0 TB/s,
+// the rate of a copy; 4099 tokens of 64 heads of 512, 64 elements of each turned, 88 us,
+// 4.7 TB/s (the launch of the turned groups takes 26 instructions an element, two thirds of
+// the issue slots of its 36 us; the other moves 5.4 TB/s); gated 32 us, 5.2 TB/s, 0.6 of
+// the issue slots; one row 1.2 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -148,6 +148,7 @@ MATMUL = [
     ("negative stride of a_scale", dict(a_scale_row_stride=-1), INVALID),
     ("rows of out that overlap", dict(out_row_stride=199), INVALID),
     ("a stride of 2^37", dict(w_group_stride=1 << 37), UNSUPPORTED),
+    ("a scale stride of 2^36", dict(a_scale_row_stride=1 << 36), UNSUPPORTED),
     ("out over a", dict(out=A + 1024), INVALID),
     ("out over the matrices", dict(out=W + 2 * 1040 * 200), INVALID),
     ("out over a_scale", dict(out=AS + 64), INVALID),
