@@ -221,9 +221,11 @@ __device__ __forceinline__ uint32_t nearer(uint32_t code, Wide y, float num, Wid
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(two) : "h"(uint16_t(lower | ((lower + 1) << 8))));
   const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&two));
   const float m = 0.5f * (f.x + f.y);
-  const float yh = fabsf(y.hi), yl = y.hi < 0.f ? -y.lo : y.lo;
-  const float v = num * yh, w = m * den.hi;
-  const float over = (v - w) + ((__fmaf_rn(num, yh, -v) - __fmaf_rn(m, den.hi, -w)) + (num * yl - m * den.lo));
+  // (large numbers are made smaller, by a power of two: 448 y is at most fp32's largest)
+  const float k = den.hi > 0x1p100f ? 0x1p-32f : 1.f;
+  const float yh = fabsf(y.hi) * k, yl = (y.hi < 0.f ? -y.lo : y.lo) * k, dh = den.hi * k, dl = den.lo * k;
+  const float v = num * yh, w = m * dh;
+  const float over = (v - w) + ((__fmaf_rn(num, yh, -v) - __fmaf_rn(m, dh, -w)) + (num * yl - m * dl));
   return sign | (over > 0.f ? lower + 1 : over < 0.f ? lower : lower + (lower & 1));
 }
 

@@ -1,0 +1,70 @@
+"""8-bit products where their arithmetic could leave the formula."""
+
+import numpy as np
+import pytest
+import torch
+
+import compressed_mla_attention_gb300 as Q
+from oracle import product_oracle as P
+from oracle import qsfm_oracle as O
+from tests.test_gpu_products import SCALE_REL, built, check_quantised, clean, f64, values  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+LARGEST = float(np.finfo(np.float32).max)
+BORDERS = (O.E4M3FN_TABLE[1:127] + O.E4M3FN_TABLE[:126]) / 2
+
+
+def next_to(y):
+    """y in fp32 with the numbers before and behind."""
+    y = np.asarray(y, dtype=np.float32)
+    return np.concatenate((np.nextafter(y, np.float32(0)), y, np.nextafter(y, np.float32(np.inf))))
+
+
+def groups_of(top, y):
+    """Groups of 128 whose first element is `top`, the others y in turn, signs mixed."""
+    y = np.concatenate((y, np.zeros(-len(y) % 127, dtype=np.float32))).reshape(-1, 127)
+    y = y * np.where(np.arange(127) % 3 == 0, -1, 1).astype(np.float32)
+    return np.concatenate((np.full((len(y), 1), top, dtype=np.float32), y), 1)
+
+
+def check_computed(codes, scale, y):
+    """check_quantised() of elements that 64 bits round too: y and A are carried to 2^-48
+    of themselves, and what is compared to 2^-47 (three sums of terms below 2^-23, each in
+    fp32), so that within 2^-45 of a border, the fp64 roundings among it, either of its codes may be taken."""
+    want, _ = P.quantize(y, False)
+    a = np.abs(y).reshape(len(y), -1, 128).max(2).repeat(128, 1)
+    near = np.abs(np.abs(y * 448 / a)[..., None] / BORDERS - 1) < 2.0 ** -45
+    got = values(codes)
+    free = near.any(2) & (got != want)
+    lower, upper = O.E4M3FN_TABLE[near.argmax(2)], O.E4M3FN_TABLE[near.argmax(2) + 1]
+    assert np.all((np.abs(got) == lower)[free] | (np.abs(got) == upper)[free])
+    assert np.array_equal(np.signbit(got)[free], np.signbit(y)[free])
+    assert np.array_equal(got[~free], want[~free])
+    assert np.all(np.abs(f64(scale) / (a[:, ::128] / 448) - 1) <= SCALE_REL["gated"])
+
+
+def still(n, dim, dev):
+    """A table whose angles are all 0."""
+    return torch.cat((torch.ones(n, dim // 2), torch.zeros(n, dim // 2)), 1).to(dev)
+
+
+# ------------------------------------------------------------------ quantised rows
+@pytest.mark.parametrize("top", [LARGEST, 1.75 * 2.0 ** 126, 1.3 * 2.0 ** 120, 1.9 * 2.0 ** 119, 2.0 ** 101, 2.0 ** 100], ids=str)
+def test_borders_near_the_largest_numbers(cuda_device, top):
+    top = float(np.float32(top))
+    x = torch.from_numpy(groups_of(top, next_to(BORDERS * (top / 448)))).to(cuda_device)
+    codes, scale = Q.quantize_rows(x)
+    clean()
+    check_quantised(codes, scale, f64(x), False, "plain")
+    zero = torch.zeros(len(x), dtype=torch.int32, device=cuda_device)
+    for inter in (True, False):
+        codes, scale = Q.quantize_rows(x, positions=zero, cos_sin=still(1, 64, cuda_device), rope_offset=64, interleaved=inter)
+        clean()
+        check_quantised(codes, scale, f64(x), False, "rotate")
+    small = x / 16
+    for spread in (0.0, 0.25):  # of equal gates the borders of x are y's
+        gate = 8 + spread * torch.rand(x.shape, generator=torch.Generator().manual_seed(1)).to(cuda_device)
+        codes, scale = Q.quantize_rows(small, gate=gate)
+        clean()
+        check_computed(codes, scale, f64(small) * P.silu(f64(gate)))
