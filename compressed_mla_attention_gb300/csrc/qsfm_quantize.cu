@@ -158,10 +158,11 @@ __device__ __forceinline__ float over448(float a) {
   return __fmaf_rn(__fmaf_rn(-448.f, q, a), kInv, q);
 }
 
-// The smallest e with a <= 448 2^e = 1.75 2^(8 + e), within -100 .. 100.
-__device__ __forceinline__ int pow2_exponent(float a) {
-  const uint32_t u = __float_as_uint(a);
-  return min(max(int(u >> 23) - 127 - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0), -100), 100);
+// The smallest e with a + more <= 448 2^e = 1.75 2^(8 + e), within -100 .. 100 (|more| at
+// most half a unit of a).
+__device__ __forceinline__ int pow2_exponent(float a, float more = 0.f) {
+  const uint32_t u = __float_as_uint(a), part = u & 0x7FFFFFu;
+  return min(max(int(u >> 23) - 127 - 8 + (part > 0x600000u || (part == 0x600000u && more > 0.f) ? 1 : 0), -100), 100);
 }
 __device__ __forceinline__ float power2(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }
 
@@ -469,10 +470,7 @@ __device__ __forceinline__ void finish(const qsfm_quantize_params& p, const Quan
       const bool near = !bad && abs(int(__float_as_uint(m) & 0x7FFFFFu) - 0x600000) < 128;
       if (__any_sync(kAllLanes, near)) {
         const float2 top = wide_top<T, kMode>(p, item.row, item.k0, near ? near_top(y, m) & own : 0);
-        if (near) {
-          e = pow2_exponent(top.x);
-          if ((__float_as_uint(top.x) & 0x7FFFFFu) == 0x600000u && top.y > 0.f) e = min(max(e + 1, -100), 100);
-        }
+        if (near) e = pow2_exponent(top.x, top.y);
       }
     }
     scale = power2(e);

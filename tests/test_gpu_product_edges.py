@@ -7,7 +7,7 @@ import torch
 import compressed_mla_attention_gb300 as Q
 from oracle import product_oracle as P
 from oracle import qsfm_oracle as O
-from tests.test_gpu_products import SCALE_REL, built, check_quantised, clean, f64, values  # noqa: F401
+from tests.test_gpu_products import SCALE_REL, built, check_quantised, clean, f64, i32, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +68,22 @@ def test_borders_near_the_largest_numbers(cuda_device, top):
         codes, scale = Q.quantize_rows(small, gate=gate)
         clean()
         check_computed(codes, scale, f64(small) * P.silu(f64(gate)))
+
+
+@pytest.mark.parametrize("inter", [True, False])
+def test_power_of_two_scales_of_tiny_turned_rows(cuda_device, inter):
+    """The largest element is a little above 1.75 2^j, its fp32 value is not: the
+    exponent is one more, and is clipped after that."""
+    at = list(range(-126, -85, 3)) + [-94, -93, -92, -91, 3, 106, 107]
+    x = torch.zeros(len(at), 128)
+    other = 1 if inter else 32
+    for i, j in enumerate(at):
+        x[i, 64], x[i, 64 + other] = 1.75 * 2.0 ** j, -1.75 * 2.0 ** j
+    table = torch.cat((torch.ones(1, 32), torch.full((1, 32), 2.0 ** -26)), 1)
+    codes, scale = Q.quantize_rows(x.to(cuda_device), positions=i32([0] * len(at), cuda_device), cos_sin=table.to(cuda_device),
+                                   rope_offset=64, interleaved=inter, pow2_scale=True)
+    clean()
+    cos, sin = f64(table[:, :32]).repeat(len(at), 0), f64(table[:, 32:]).repeat(len(at), 0)
+    y = P.turn(f64(x)[:, None], cos, sin, 64, inter, False)[:, 0]
+    assert np.all(y.max(1) > 1.75 * 2.0 ** np.array(at, dtype=float)) and np.all(y.astype(np.float32).max(1) == x.numpy().max(1))
+    check_quantised(codes, scale, y, True, "rotate")
