@@ -49,7 +49,8 @@ constexpr int kQLanes = 8;          // lanes of a group
 constexpr int kQElems = 16;         // elements of a lane
 constexpr int kQWarps = 8;
 constexpr uint32_t kAllLanes = 0xffffffffu;
-constexpr float kQMin = 1e-12f;     // A of an all-zero group
+constexpr float kQMin = 1e-12f;     // A of an all-zero group,
+constexpr float kQMinRest = float(1e-12 - double(kQMin));  // and what fp32 leaves over of it
 
 enum QuantizeMode { kPlain = 0, kAdjacent = 1, kHalves = 2, kGated = 3 };  // the middle two turn pairs
 
@@ -531,12 +532,13 @@ __device__ __forceinline__ void finish(const qsfm_quantize_params& p, const Quan
   if (kMode != kPlain || sizeof(T) == 4) {
     which &= own;
     if (__any_sync(kAllLanes, which != 0)) {
-      Wide den = {a, 0.f};
+      Wide den = {a, a == kQMin ? kQMinRest : 0.f};
       if (p.pow2_scale) {
-        den.hi = scale;
+        den = {scale, 0.f};
       } else if (kMode != kPlain) {
         const float2 top = wide_top<T, kMode>(p, item.row, item.k0, bad ? 0 : near_top(y, m) & own);
-        if (top.x >= kQMin) den = {top.x, top.y};
+        const bool least = top.x < kQMin || (top.x == kQMin && top.y <= kQMinRest);
+        den = least ? Wide{kQMin, kQMinRest} : Wide{top.x, top.y};
       }
       if (which != 0) fix_borders<T, kMode>(p, item.row, item.k0, which, p.pow2_scale ? 1.f : 448.f, den);
       __syncwarp();

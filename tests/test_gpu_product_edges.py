@@ -87,3 +87,18 @@ def test_power_of_two_scales_of_tiny_turned_rows(cuda_device, inter):
     y = P.turn(f64(x)[:, None], cos, sin, 64, inter, False)[:, 0]
     assert np.all(y.max(1) > 1.75 * 2.0 ** np.array(at, dtype=float)) and np.all(y.astype(np.float32).max(1) == x.numpy().max(1))
     check_quantised(codes, scale, y, True, "rotate")
+
+
+def test_groups_below_the_least_maximum(cuda_device):
+    """Where all elements are below 1e-12, that is A: the number itself, not the fp32
+    number next to it (one element in fp32 lies between the borders of the two)."""
+    for top in (0.0, 9e-13, 2e-17, float(np.float32(1e-12)), float(np.nextafter(np.float32(1e-12), np.float32(1)))):
+        y = next_to(BORDERS * (1e-12 / 448))
+        x = torch.from_numpy(groups_of(top, y[y <= max(top, 9e-13)])).to(cuda_device)
+        codes, scale = Q.quantize_rows(x)
+        clean()
+        check_quantised(codes, scale, f64(x), False, "plain")
+        zero = torch.zeros(len(x), dtype=torch.int32, device=cuda_device)
+        codes, scale = Q.quantize_rows(x, positions=zero, cos_sin=still(1, 128, cuda_device))
+        clean()
+        check_quantised(codes, scale, f64(x), False, "rotate")
