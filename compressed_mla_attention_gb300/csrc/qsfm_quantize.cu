@@ -358,6 +358,12 @@ struct Item {
   }
 };
 
+// Whether y, as far as its fp32 value may be off, can be the group's largest, which is m in
+// fp32: 256 units of difference are more than the errors of both (118 units of 2^-24 at most).
+__device__ __forceinline__ bool may_be_top(float y, float m) {
+  return (__float_as_uint(y) & 0x7FFFFFFFu) + 256u >= __float_as_uint(m);
+}
+
 // The largest |y| of the lane's runs and of the group, NaN when one is.
 __device__ __forceinline__ float group_max(const float (&y)[kQElems], float (&run)[2]) {
 #pragma unroll
@@ -405,7 +411,7 @@ __device__ __forceinline__ uint32_t near_top(const float (&y)[kQElems], float m)
   uint32_t which = 0;
 #pragma unroll
   for (int i = 0; i < kQElems; ++i)
-    which |= (__float_as_uint(y[i]) & 0x7FFFFFFFu) + 256u >= __float_as_uint(m) ? 1u << i : 0u;
+    which |= may_be_top(y[i], m) ? 1u << i : 0u;
   return which;
 }
 
@@ -488,8 +494,9 @@ __device__ __forceinline__ void finish(const qsfm_quantize_params& p, const Quan
     uint32_t chance = 0xFFFFu;
     if constexpr (kTurns) {
       if (sizeof(T) == 2 || p.pow2_scale) {
-        // A is computed where a lane of the group holds it among its turned elements
-        const bool holds = (item.in(p, 0) && run[0] == m) || (item.in(p, 1) && run[1] == m);
+        // A is computed where a lane of the group may hold it among its turned elements
+        // (one whose fp32 value is below m may itself be above)
+        const bool holds = (item.in(p, 0) && may_be_top(run[0], m)) || (item.in(p, 1) && may_be_top(run[1], m));
         const bool of_group = !p.pow2_scale && (__ballot_sync(kAllLanes, holds) >> (threadIdx.x & 24u) & 0xFFu) != 0;
         chance = of_group ? 0xFFFFu : (item.in(p, 0) ? 0xFFu : 0u) | (item.in(p, 1) ? 0xFF00u : 0u);
       }

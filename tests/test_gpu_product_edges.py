@@ -102,3 +102,37 @@ def test_groups_below_the_least_maximum(cuda_device):
         codes, scale = Q.quantize_rows(x, positions=zero, cos_sin=still(1, 128, cuda_device))
         clean()
         check_quantised(codes, scale, f64(x), False, "rotate")
+
+
+#: cosine, sine, and a pair (a, b) of bf16 whose a cos - b sin lies within 2^-25 above 1,
+#: and in fp32, within its roundings, below
+ABOVE_ONE = [("0x1.6346e4p-3", "-0x1.f83cb8p-1", -0.00130462646484375, 1.015625),
+             ("-0x1.433022p-2", "-0x1.e5d4a2p-1", 0.002471923828125, 1.0546875),
+             ("-0x1.1cb348p-2", "0x1.ebd03cp-1", 0.0201416015625, -1.046875),
+             ("-0x1.c867eap-2", "0x1.ca54c4p-1", 0.00018310546875, -1.1171875),
+             ("-0x1.536868p-1", "0x1.7f55f6p-1", 0.000331878662109375, -1.3359375)]
+
+
+@pytest.mark.parametrize("inter", [True, False])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+def test_turned_element_just_above_the_largest_other(cuda_device, dtype, inter):
+    """An element that is not turned is 1; a turned one is larger by less than what its
+    fp32 value may be off: elements on a border of A = 1 lie below the border of A."""
+    x = torch.zeros(len(ABOVE_ONE), 128)
+    table = torch.zeros(len(ABOVE_ONE), 64)
+    # 448 y = m, the border of two codes: m a multiple of 7
+    ties = [(m / 448) * 2.0 ** -e for m in (21.0, 28 / 2.0 ** 12) for e in range(0, 9)]
+    for i, (c, s, a, b) in enumerate(ABOVE_ONE):
+        x[i, 0] = 1.0
+        x[i, 1:1 + len(ties)] = torch.tensor(ties)
+        x[i, 64], x[i, 65 if inter else 96] = a, b
+        table[i, 0], table[i, 32] = float.fromhex(c), float.fromhex(s)
+    assert torch.equal(x.to(torch.bfloat16).float(), x)
+    x = x.to(dtype)
+    codes, scale = Q.quantize_rows(x.to(cuda_device), positions=i32(range(len(x)), cuda_device),
+                                   cos_sin=table.to(cuda_device), rope_offset=64, interleaved=inter)
+    clean()
+    y = P.turn(f64(x)[:, None], *np.split(f64(table), 2, axis=1), 64, inter, False)[:, 0]
+    if dtype != torch.float16:  # fp16 holds a less exactly
+        assert np.all(y[:, 64] > 1) and np.all(y[:, 64] < 1 + 2.0 ** -25) and np.all(np.abs(y).max(1) == y[:, 64])
+    check_quantised(codes, scale, y, False, "rotate")
