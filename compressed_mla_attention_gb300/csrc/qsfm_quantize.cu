@@ -208,11 +208,13 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return o;
 }
 // x silu(g) of two elements. Units of 2^-24: the exponent 1.25 |g| (its product, log2 e),
-// ex2 4, 1 + e 1, the reciprocal 2, two products: 1.25 |g| + 9.
+// ex2 4, 1 + e 1, the reciprocal 2, two products: 1.25 |g| + 9. (x by the reciprocal first:
+// half a gate below the normal numbers would lose bits that a large x makes count. Where x by
+// the reciprocal is below them, either the reciprocal is 1 or y is too small for any code.)
 __device__ __forceinline__ float2 gated(float2 x, float2 g) {
   const float2 t = mul2(g.x, g.y, -1.4426950408889634f);
   const float2 e = plus1(make_float2(ex2_approx(t.x), ex2_approx(t.y)));
-  return mul2(x, mul2(g, make_float2(rcp_approx(e.x), rcp_approx(e.y))));
+  return mul2(mul2(x, make_float2(rcp_approx(e.x), rcp_approx(e.y))), g);
 }
 
 // Which code is that of y, `code` or the next one away from zero: that of the nearer

@@ -136,3 +136,21 @@ def test_turned_element_just_above_the_largest_other(cuda_device, dtype, inter):
     if dtype != torch.float16:  # fp16 holds a less exactly
         assert np.all(y[:, 64] > 1) and np.all(y[:, 64] < 1 + 2.0 ** -25) and np.all(np.abs(y).max(1) == y[:, 64])
     check_quantised(codes, scale, y, False, "rotate")
+
+
+def test_numbers_below_the_normal_ones_in_gated_rows(cuda_device):
+    """silu of a small gate is half of it, and of a large one the gate: what is left of a
+    gate or an element of few bits counts in full."""
+    g = torch.Generator().manual_seed(5)
+    large = 1e30 * torch.randn(40, 256, generator=g)
+    small = torch.randint(1, 2000, (40, 256), generator=g) * 2.0 ** -149
+    small[::2] *= -1
+    small[1] = 2.0 ** -149
+    small[2] = 1e-30
+    for dtype in (torch.float32, torch.bfloat16):
+        for x, gate in ((large, small), (small, 20 + large.abs())):
+            x, gate = x.to(dtype), gate.to(dtype)
+            for pow2 in (False, True):
+                codes, scale = Q.quantize_rows(x.to(cuda_device), gate=gate.to(cuda_device), pow2_scale=pow2)
+                clean()
+                check_quantised(codes, scale, f64(x) * P.silu(f64(gate)), pow2, "gated")
