@@ -1053,8 +1053,10 @@ def scaled_matmul(a, a_scale, w, w_scale, *, out=None, out_dtype=None, stream=No
     a e4m3 codes [M, K] (uint8 or float8_e4m3fn) with a_scale fp32 [M, ceil(K /
     128)] (any strides), as quantize_rows() makes them; w codes [N, K] with
     w_scale fp32 [ceil(N / 128), ceil(K / 128)], one scale per 128 x 128
-    elements. K a multiple of 16; rows of a and w may be strided by multiples of
-    16 bytes. out [M, N] bf16, fp16 or fp32 (rows may be strided) is allocated
+    elements. The two scales of a block are multiplied in fp32: where their
+    product is outside its normal numbers it is inf, or has fewer bits. K a
+    multiple of 16; rows of a and w may be strided by multiples of 16 bytes.
+    out [M, N] bf16, fp16 or fp32 (rows may be strided) is allocated
     when not given, in out_dtype (default bf16). With a stream of its own the
     call expects its inputs to be there for that stream, and to live until it
     has run. Returns out.

@@ -689,10 +689,11 @@ qsfm_status qsfm_quantize_rows(const qsfm_quantize_params* p, void* stream);
  *   out[m][j] = sum over blocks b of 128 of  a_scale[m][b] w_scale[g][j / 128][b]
  *                 * (sum over k in b of a[m][k] w[g][j][k])
  * with e4m3fn a and w; g is 0, or with cu_rows the group of row m, the g with
- * cu_rows[g] <= m < cu_rows[g + 1]. The sum over a block is the tensor cores' (fp32
- * accumulators), blocks are added in fp32, and the result is rounded once to
- * out_type. A call gives the same bits every time; for another number of rows the
- * blocks may be added in another order.
+ * cu_rows[g] <= m < cu_rows[g + 1]. The two scales of a block are multiplied in fp32
+ * (above its largest number their product is inf, below 2^-126 it has fewer bits), the sum
+ * over a block is the tensor cores' (fp32 accumulators), blocks are added in fp32, and the
+ * result is rounded once to out_type. A call gives the same bits every time; for
+ * another number of rows the blocks may be added in another order.
  *   a          e4m3fn bytes [M, K], rows a_row_stride apart
  *   a_scale    fp32 [M, ceil(K / 128)], element strides a_scale_row_stride and
  *              a_scale_col_stride

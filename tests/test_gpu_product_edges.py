@@ -154,3 +154,68 @@ def test_numbers_below_the_normal_ones_in_gated_rows(cuda_device):
                 codes, scale = Q.quantize_rows(x.to(cuda_device), gate=gate.to(cuda_device), pow2_scale=pow2)
                 clean()
                 check_quantised(codes, scale, f64(x) * P.silu(f64(gate)), pow2, "gated")
+
+
+# ------------------------------------------------------------------ products
+#: rows, columns, K
+SHAPES = [(40, 260, 1040), (5, 130, 128), (300, 10130, 144), (700, 10400, 272), (141, 4993, 3712), (41, 6172, 3488)]
+
+
+def codes_of(v, dev):
+    return v.float().to(torch.float8_e4m3fn).to(dev)
+
+
+def scaled_by_fp32(a, sa, w, sw):
+    """The definition in 64 bits, a block's two scales multiplied in fp32, with the sum of
+    the terms' magnitudes."""
+    out, mag = (torch.zeros(a.shape[0], w.shape[0], dtype=torch.float64, device=a.device) for _ in range(2))
+    rows = torch.arange(w.shape[0], device=a.device) // 128
+    for b in range(-(-a.shape[1] // 128)):
+        u, v = a[:, 128 * b:128 * b + 128].double(), w[:, 128 * b:128 * b + 128].double()
+        s = (sa[:, b, None] * sw[rows, b][None]).double()
+        out += s * (u @ v.t())
+        mag += s.abs() * (u.abs() @ v.abs().t())
+    return out, mag
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("ends", ["largest", "least"])
+def test_scales_whose_product_is_at_the_ends_of_fp32(cuda_device, shape, ends):
+    """Products of two scales from 2^125 to 2^127 of small codes, and from 2^-126 to 2^-124 of
+    large ones, each scale far from the other: every result is a number of fp32."""
+    dev, (m, n, k), g = cuda_device, shape, torch.Generator().manual_seed(shape[1])
+    kb, nb = -(-k // 128), -(-n // 128)
+    mant = lambda *s: 1 + torch.rand(*s, generator=g)  # noqa: E731
+    if ends == "largest":  # codes up to 3 x 2^-9: a result is below K 9 2^-18 2^128
+        a, w = (codes_of(torch.randint(-3, 4, s, generator=g) * 2.0 ** -9, dev) for s in ((m, k), (n, k)))
+        sa, sw = mant(m, kb).to(dev) * 2.0 ** 119, mant(nb, kb).to(dev) * 2.0 ** 6
+    else:  # codes of 256 and more: a block's sum is above 2^20, and so exact in fp32 terms
+        a, w = (codes_of(256 + 32 * torch.randint(0, 7, s, generator=g), dev) for s in ((m, k), (n, k)))
+        sa, sw = mant(m, kb).to(dev) * 2.0 ** -100, mant(nb, kb).to(dev) * 2.0 ** -26
+    out = Q.scaled_matmul(a, sa, w, sw, out_dtype=torch.float32)
+    clean()
+    ref, mag = scaled_by_fp32(a, sa, w, sw)
+    # a block's sum is exact (whole numbers of a unit, below 2^24 of them); a rounding each of the
+    # product with the scales' and of the sum, for every block
+    assert torch.isfinite(out).all() and torch.all((out.double() - ref).abs() <= (1 + kb) * 2.0 ** -24 * 1.01 * mag)
+
+
+def test_scales_whose_product_leaves_fp32(cuda_device):
+    """The product of a block's scales is fp32's: inf where it is larger than its largest
+    number, rounded to its steps of 2^-149 where it is small."""
+    dev = cuda_device
+    a = torch.zeros(6, 256, device=dev)
+    a[:, :128] = 1.0
+    a[0, 1:128:2] = -1.0  # a sum of 0
+    a[5, :128] = 448.0
+    w = torch.ones(130, 256, device=dev)
+    a, w = codes_of(a, dev), codes_of(w, dev)
+    sa, sw = torch.ones(6, 2, device=dev), torch.ones(2, 2, device=dev)
+    for first, second in ((2.0 ** 119, 2.0 ** 9), (2.0 ** -100, 2.0 ** -50), (1.3 * 2.0 ** -75, 1.7 * 2.0 ** -72), (-2.0 ** 100, 2.0 ** 100)):
+        sa[:, 0], sw[:, 0] = first, second
+        sa[1, 0] = 2.0 ** -3
+        out = Q.scaled_matmul(a, sa, w, sw, out_dtype=torch.float32)
+        clean()
+        want = (sa[:, :1] * sw[0, 0]).double() * torch.tensor([0, 128, 128, 128, 128, 448 * 128], device=dev)[:, None].double()
+        assert torch.equal(torch.nan_to_num(out, nan=7.0), torch.nan_to_num(want.float(), nan=7.0).expand(6, 130))
+    assert torch.isnan(out[0]).all() and torch.isinf(out[2:]).all() and torch.isfinite(out[1]).all()
