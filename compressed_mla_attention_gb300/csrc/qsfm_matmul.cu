@@ -393,6 +393,15 @@ __device__ void mm_load(const qsfm_matmul_params& p, const MmShape& s, const MmS
       }
     }
   }
+  // the last commits' arrivals come from the pair's first CTA: the second stays until they are there
+  if constexpr (C::kCtas == 2)
+    for (int i = 0; i < C::kStages; ++i) {
+      if (!mm_warp_wait(sm, kBEmpty + st, par, fault)) return;
+      if (++st == C::kStages) {
+        st = 0;
+        par ^= 1;
+      }
+    }
 }
 
 // ------------------------------------------------------------- MMA issue
@@ -807,7 +816,8 @@ __global__ void __launch_bounds__(kMmThreads, 1)
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (C::kCtas == 2) cluster_sync();  // no arrival for the other CTA is on its way, its accumulators are read
+  // the other CTA's accumulators are read, its arrivals are there (the commits': mm_load's last waits)
+  if (C::kCtas == 2) cluster_sync();
   if (warp == kAddWarps + 1) {
     tc_fence_after();
     if constexpr (C::kCtas == 2)
