@@ -187,6 +187,7 @@ EXPORTS = {
     "qsfm_quantize_rows": (_i32, [ctypes.POINTER(QuantizeParams), _ptr]),
     "qsfm_matmul_params_init": (None, [ctypes.POINTER(MatmulParams)]),
     "qsfm_scaled_matmul": (_i32, [ctypes.POINTER(MatmulParams), _ptr]),
+    "qsfm_debug_matmul_plan": (_i32, [ctypes.POINTER(MatmulParams)] + [ctypes.POINTER(_i32)] * 3),
 }
 
 
@@ -1045,6 +1046,17 @@ def make_matmul_params(*, a, a_scale, w, w_scale, out, cu_rows=None) -> _Launch:
 def matmul(launch: _Launch, stream=None) -> None:
     """qsfm_scaled_matmul() with a block of make_matmul_params()."""
     launch.call("qsfm_scaled_matmul", stream)
+
+
+def debug_matmul_plan(launch: _Launch):
+    """qsfm_debug_matmul_plan(): (rows, columns, parts) of the tiles that
+    matmul() computes the product of a block by."""
+    import torch
+
+    out = [_i32() for _ in range(3)]
+    with torch.cuda.device(launch.device):
+        _check("qsfm_debug_matmul_plan", lib().qsfm_debug_matmul_plan(launch.ref, *(ctypes.byref(v) for v in out)))
+    return tuple(v.value for v in out)
 
 
 def scaled_matmul(a, a_scale, w, w_scale, *, out=None, out_dtype=None, stream=None):

@@ -742,6 +742,14 @@ qsfm_status qsfm_scaled_matmul(const qsfm_matmul_params* p, void* stream) {
   return cuda_status(qsfm::launch_matmul(*p, fault, static_cast<cudaStream_t>(stream)));
 }
 
+qsfm_status qsfm_debug_matmul_plan(const qsfm_matmul_params* p, int32_t* tile_rows, int32_t* tile_columns,
+                                   int32_t* parts) {
+  const qsfm_status st = check_matmul(p);
+  if (st != QSFM_OK) return st;
+  if (p->rows == 0 || tile_rows == nullptr || tile_columns == nullptr || parts == nullptr) return QSFM_ERR_INVALID_ARG;
+  return cuda_status(qsfm::matmul_plan(*p, tile_rows, tile_columns, parts));
+}
+
 qsfm_status qsfm_get_device_status(int32_t* fault_word) {
   if (fault_word == nullptr) return QSFM_ERR_INVALID_ARG;
   int v = 0;

@@ -61,6 +61,8 @@ cudaError_t launch_norm_rope(const qsfm_norm_rope_params& p, int* fault, cudaStr
 cudaError_t launch_block_tables(const qsfm_block_table_params& p, int* fault, cudaStream_t s);
 cudaError_t launch_quantize(const qsfm_quantize_params& p, int* fault, cudaStream_t s);
 cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t s);
+// The tiles (rows of a, matrix rows) that launch_matmul() takes, and the parts of their blocks of K.
+cudaError_t matmul_plan(const qsfm_matmul_params& p, int32_t* rows, int32_t* columns, int32_t* parts);
 cudaError_t launch_bounded_wait(uint64_t timeout_ns, unsigned long long* elapsed, int* fault,
                                 cudaStream_t s);
 cudaError_t launch_debug_gather(const qsfm_params& p, const int32_t* tokens, int n,

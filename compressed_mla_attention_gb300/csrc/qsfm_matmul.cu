@@ -1034,27 +1034,55 @@ cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int row
   return cudaLaunchKernelEx(&cfg, matmul_kernel<C>, p, s, fault, amap, wmap, omap);
 }
 
-}  // namespace
+using Pair = Mm<2, 256>;
+using Wide = Mm<1, 256>;
+using Small = Mm<1, 128>;
 
-cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t stream) {
-  int dev = 0, sms = 0;
+// The kernel of a product, prepared on the current device, and its parts.
+struct MmChoice {
+  int ctas, cols;  // of its tiles
+  int sms;
+  MmPlan plan;
+};
+
+cudaError_t choose(const qsfm_matmul_params& p, MmChoice& c) {
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
-  const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
-  using Pair = Mm<2, 256>;
-  using Wide = Mm<1, 256>;
-  using Small = Mm<1, 128>;
+  if ((e = cudaDeviceGetAttribute(&c.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
   if ((e = prepare<Pair>(dev)) != cudaSuccess || (e = prepare<Wide>(dev)) != cudaSuccess ||
       (e = prepare<Small>(dev)) != cudaSuccess)
     return e;
-  const MmPlan pair = plan<Pair>(p, dev, sms, kPairTimes), wide = plan<Wide>(p, dev, sms, kWideTimes),
-               small = plan<Small>(p, dev, sms, kSmallTimes);
+  const MmPlan pair = plan<Pair>(p, dev, c.sms, kPairTimes), wide = plan<Wide>(p, dev, c.sms, kWideTimes),
+               small = plan<Small>(p, dev, c.sms, kSmallTimes);
   // (the pair first where it is as good: it reads a third less)
-  if (pair.time <= 1.03 * wide.time && pair.time <= 1.03 * small.time)
-    return launch_ctas<Pair>(p, pair, rows, sms, fault, stream);
-  return wide.time <= small.time ? launch_ctas<Wide>(p, wide, rows, sms, fault, stream)
-                                 : launch_ctas<Small>(p, small, rows, sms, fault, stream);
+  const bool paired = pair.time <= 1.03 * wide.time && pair.time <= 1.03 * small.time;
+  c.plan = paired ? pair : wide.time <= small.time ? wide : small;
+  c.ctas = paired ? Pair::kCtas : 1;
+  c.cols = paired || wide.time <= small.time ? Wide::kCols : Small::kCols;
+  return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_matmul(const qsfm_matmul_params& p, int* fault, cudaStream_t stream) {
+  MmChoice c;
+  const cudaError_t e = choose(p, c);
+  if (e != cudaSuccess) return e;
+  const int rows = (p.rows + p.groups - 1) / p.groups;  // of a group, on average
+  if (c.ctas == Pair::kCtas) return launch_ctas<Pair>(p, c.plan, rows, c.sms, fault, stream);
+  return c.cols == Wide::kCols ? launch_ctas<Wide>(p, c.plan, rows, c.sms, fault, stream)
+                               : launch_ctas<Small>(p, c.plan, rows, c.sms, fault, stream);
+}
+
+cudaError_t matmul_plan(const qsfm_matmul_params& p, int32_t* rows, int32_t* columns, int32_t* parts) {
+  MmChoice c;
+  const cudaError_t e = choose(p, c);
+  if (e != cudaSuccess) return e;
+  *rows = 128 * c.ctas;
+  *columns = c.cols;
+  *parts = c.plan.parts;
+  return cudaSuccess;
 }
 
 }  // namespace qsfm

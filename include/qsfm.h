@@ -733,6 +733,13 @@ void qsfm_matmul_params_init(qsfm_matmul_params* p);
  * 2^24 or more, more than 2^30 tiles of 16 x 128 outputs, a stride of 2^36 or more). */
 qsfm_status qsfm_scaled_matmul(const qsfm_matmul_params* p, void* stream);
 
+/* How qsfm_scaled_matmul() would compute this product on the current device, for
+ * tests: the rows and columns of out that a tile has, and the parts that a tile's
+ * blocks of K are split into. Launches nothing. QSFM_ERR_INVALID_ARG for M = 0 or a
+ * NULL output. */
+qsfm_status qsfm_debug_matmul_plan(const qsfm_matmul_params* p, int32_t* tile_rows, int32_t* tile_columns,
+                                   int32_t* parts);
+
 /* Synchronously read and clear the device fault word of the current
  * device (QSFM_FAULT_* bits). Returns QSFM_ERR_DEVICE_FAULT when non-zero. */
 qsfm_status qsfm_get_device_status(int32_t* fault_word);

@@ -1,6 +1,8 @@
 """Refusals of the 8-bit products' binding on the CPU, each by its own check: the tensors
 stand for tensors of one CUDA device, so that the unchanged block is accepted."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -141,3 +143,20 @@ def test_block_holds_what_it_was_given(accept):
     assert (p.a_row_stride, p.w_row_stride, p.w_group_stride, p.a_scale_row_stride, p.a_scale_col_stride, p.out_row_stride) == \
         (512, 256, 130 * 256, 1, 9, 200)
     assert p.out == out.data_ptr() and p.cu_rows == g["cu_rows"].data_ptr()
+
+
+def test_plan_query_refuses(lib):  # noqa: F811
+    """As the product itself, before any CUDA call; and without rows or a place for the answer."""
+    from tests.test_products import matmul_valid
+
+    out = [ctypes.c_int32() for _ in range(3)]
+    refs = [ctypes.byref(v) for v in out]
+    assert lib.qsfm_debug_matmul_plan(None, *refs) == 1
+    p = matmul_valid(lib)
+    for i in range(3):
+        assert lib.qsfm_debug_matmul_plan(ctypes.byref(p), *(None if j == i else refs[j] for j in range(3))) == 1
+    p.k = 1032
+    assert lib.qsfm_debug_matmul_plan(ctypes.byref(p), *refs) == 2
+    p = matmul_valid(lib)
+    p.rows = 0
+    assert lib.qsfm_debug_matmul_plan(ctypes.byref(p), *refs) == 1
