@@ -463,9 +463,7 @@ qsfm_status check_quantize(const qsfm_quantize_params* pp) {
 }
 
 constexpr long long kMaxStride = 1ll << 36;  // elements; times a number of rows of 4 bytes it stays within 64 bits
-constexpr int kMaxMatmulGroups = 1024;
 constexpr int kMaxMatmulSize = 1 << 24;
-constexpr long long kMaxMatmulTiles = 1 << 30;  // of 128 x 16 outputs, the smallest
 
 qsfm_status check_matmul(const qsfm_matmul_params* pp) {
   if (pp == nullptr) return QSFM_ERR_INVALID_ARG;
@@ -473,9 +471,9 @@ qsfm_status check_matmul(const qsfm_matmul_params* pp) {
   if (p.rows < 0 || p.n < 1 || p.k < 1 || p.groups < 1) return QSFM_ERR_INVALID_ARG;
   if (p.out_type != QSFM_BF16 && p.out_type != QSFM_F16 && p.out_type != QSFM_F32) return QSFM_ERR_INVALID_ARG;
   if (p.groups > 1 && p.cu_rows == nullptr && p.rows > 0) return QSFM_ERR_INVALID_ARG;
-  if (p.k % 16 != 0 || p.groups > kMaxMatmulGroups) return QSFM_ERR_UNSUPPORTED;
+  if (p.k % 16 != 0 || p.groups > qsfm::kMaxMatmulGroups) return QSFM_ERR_UNSUPPORTED;
   if (p.rows >= kMaxMatmulSize || p.n >= kMaxMatmulSize || p.k >= kMaxMatmulSize) return QSFM_ERR_UNSUPPORTED;
-  if (((p.rows + 15ll) / 16 + p.groups) * ((p.n + 127ll) / 128) > kMaxMatmulTiles) return QSFM_ERR_UNSUPPORTED;
+  if (((p.rows + 127ll) / 128 + p.groups) * ((p.n + 127ll) / 128) > qsfm::kMaxMatmulTiles) return QSFM_ERR_UNSUPPORTED;
   if (p.rows == 0) return QSFM_OK;  // of empty tensors, whose pointers are null, nothing is asked
   if (p.a == nullptr || p.a_scale == nullptr || p.w == nullptr || p.w_scale == nullptr || p.out == nullptr)
     return QSFM_ERR_INVALID_ARG;

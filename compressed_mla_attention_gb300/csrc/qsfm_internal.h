@@ -12,6 +12,9 @@
 
 namespace qsfm {
 
+constexpr int kMaxMatmulGroups = 1024;           // the kernels keep a number of each in shared memory
+constexpr long long kMaxMatmulTiles = 1ll << 30; // of 128 x 128 outputs, the smallest
+
 // Partial-output workspace: per split piece slot, lse [64] fp32 then
 // O [64][512] fp32. Two slots per planned CTA.
 struct Workspace {

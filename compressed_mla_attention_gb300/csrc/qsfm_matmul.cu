@@ -62,8 +62,7 @@ constexpr int kMmK = 128;         // bytes of K per stage: one block of scales
 constexpr int kChunk = 16;        // columns that a part of a split tile joins at a time
 constexpr int kChunkBytes = kChunk * 128 * 4;
 constexpr int kBlockTiles = 8;    // row tiles that are walked before the next of the matrix's
-constexpr int kMaxGroups = 1024;
-constexpr long long kMaxTiles = (1ll << 30) + 1;  // counted at most
+constexpr long long kMaxTiles = kMaxMatmulTiles + 1;  // counted at most
 constexpr int kAddWarps = 8;
 constexpr int kMmThreads = 32 * (kAddWarps + 4);
 constexpr int kAddRegs = 224, kOtherRegs = 56, kLaunchRegs = 168;
@@ -92,7 +91,7 @@ struct Mm {
   // where a split tile's joined sums are on their way out, behind the parts' sums
   static constexpr uint32_t kJoinedAt = kScaleAt - kAddWarps * kOutPart;
   static constexpr uint32_t kPrefixAt = kScaleAt + kSlots * kSlotBlocks * kSlotBlock;
-  static constexpr uint32_t kBarAt = (kPrefixAt + (kMaxGroups + 4) * 4 + 7) & ~7u;
+  static constexpr uint32_t kBarAt = (kPrefixAt + (kMaxMatmulGroups + 4) * 4 + 7) & ~7u;
   static constexpr uint32_t kSmem = kBarAt + 256 + 1024;
   static_assert(kSmem <= 227 * 1024, "shared memory");
 };

@@ -730,7 +730,7 @@ void qsfm_matmul_params_init(qsfm_matmul_params* p);
 /* One launch on `stream` (none for M = 0, whose pointers are not looked at); no
  * workspace, nothing read back. Errors: QSFM_ERR_INVALID_ARG,
  * QSFM_ERR_UNSUPPORTED (K not a multiple of 16, more than 1024 groups, M, N or K of
- * 2^24 or more, more than 2^30 tiles of 16 x 128 outputs, a stride of 2^36 or more). */
+ * 2^24 or more, more than 2^30 tiles of 128 x 128 outputs, a stride of 2^36 or more). */
 qsfm_status qsfm_scaled_matmul(const qsfm_matmul_params* p, void* stream);
 
 /* How qsfm_scaled_matmul() would compute this product on the current device, for

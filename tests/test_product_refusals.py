@@ -160,3 +160,15 @@ def test_plan_query_refuses(lib):  # noqa: F811
     p = matmul_valid(lib)
     p.rows = 0
     assert lib.qsfm_debug_matmul_plan(ctypes.byref(p), *refs) == 1
+
+
+@pytest.mark.parametrize("rows,n,groups,code", [((1 << 24) - 1, 1 << 18, 1, 1), (1 << 20, 1 << 23, 1, 1), (1 << 20, 1 << 23, 1024, 1),
+                                                (1, (1 << 24) - 1, 1024, 1), (1 << 21, 1 << 23, 1, 2), ((1 << 24) - 1, 1 << 20, 1, 2)])
+def test_sizes_are_limited_by_the_smallest_tiles(lib, rows, n, groups, code):  # noqa: F811
+    """2^30 tiles of 128 x 128 outputs, and one for each group beside: more is not
+    supported, less goes on to the next check (here of pointers that are not there)."""
+    from tests.test_products import matmul_valid
+
+    p = matmul_valid(lib)
+    p.rows, p.n, p.groups, p.a = rows, n, groups, None
+    assert lib.qsfm_scaled_matmul(ctypes.byref(p), None) == code
