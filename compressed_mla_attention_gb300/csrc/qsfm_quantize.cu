@@ -1,8 +1,8 @@
 // Rows quantised to e4m3 with one fp32 scale per 128 elements (sm_103a).
 //
-// For each group of 128 elements y of a row, with A = max|y| (at least 1e-12):
-//   scale = A / 448, code = e4m3(448 y / A) to nearest even, or, with scales that
-//   are powers of two, scale = 2^e of the smallest e with A <= 448 2^e.
+// For each group of 128 elements y of a row, with A = max|y|:
+//   scale = A / 448, code = e4m3(448 y / A) to nearest even, A at least 1e-12, or, with
+//   scales that are powers of two, scale = 2^e of the smallest e with A <= 448 2^e.
 // y is the input itself, the input times silu(gate), or the input with a part of
 // each head turned by its position's angles; a row may be taken from anywhere in
 // the input (row_index).
@@ -24,9 +24,10 @@
 //    quotient, within a few units (`error` in finish()), is converted twice, times 1 - error and
 //    1 + error: where both give the same code, that is the code. Otherwise the sign of
 //    448 |y| - m A decides, m the border (0: the even code), with y and A as sums of two
-//    fp32 values and the products' roundings carried: about 46 bits.
+//    fp32 values and the products' roundings carried: about 46 bits (of the terms, where a
+//    turned y is a small difference of large ones).
 //
-// Measured (a call among others in a graph): 16384 bf16 rows of 8192 in 58 us, 7.0 TB/s,
+// Measured (a call among others in a graph): 16384 bf16 rows of 8192 in 62 us, 6.6 TB/s,
 // the rate of a copy; 4099 tokens of 64 heads of 512, 64 elements of each turned, 88 us,
 // 4.7 TB/s (the launch of the turned groups takes 26 instructions an element, two thirds of
 // the issue slots of its 36 us; the other moves 5.4 TB/s); gated 32 us, 5.2 TB/s, 0.6 of
@@ -54,8 +55,9 @@ constexpr float kQMinRest = float(1e-12 - double(kQMin));  // and what fp32 leav
 
 enum QuantizeMode { kPlain = 0, kAdjacent = 1, kHalves = 2, kGated = 3 };  // the middle two turn pairs
 
-// Blocks on an SM, from what was measured: 16384 bf16 rows of 8192 in 58 us with 6, 62 with
-// 4; gated 32 (5), 33 (4); turned 91 (4), 96 (5, an item a warp), 106 (3).
+// Blocks on an SM, from what was measured: 16384 bf16 rows of 8192 in 62 us with 6, 65 with
+// 4; 16001 gated rows of 2048 in 32 us with 5, 33 with 4; 4099 x 64 turned heads of 512 in 88 us
+// with 4, 93 with 5 or 3.
 constexpr int blocks_per_sm(int mode) { return mode == kPlain ? 6 : mode == kGated ? 5 : 4; }
 
 struct QuantizeShape {
@@ -172,8 +174,8 @@ struct Wide {
   float hi, lo;
 };
 
-// a c - b s: the products' difference with what its roundings leave over (each result
-// within 1.5 units), so that y is as good where its terms cancel.
+// a c - b s by Kahan's difference of products: with what its roundings leave over (each
+// result within 1.5 units), so that y is as good where its terms cancel.
 __device__ __forceinline__ float turned(float a, float c, float b, float s) {
   const float w = b * s;
   return __fmaf_rn(a, c, -w) + __fmaf_rn(-b, s, w);
@@ -601,8 +603,8 @@ cudaError_t launch_units(const qsfm_quantize_params& p, const QuantizeShape& s, 
                                   dim3(32 * kQWarps), 0, stream, p, s, fault);
 }
 
-// Units of four groups up to which a warp takes one, so that they spread over the SMs;
-// with more it has 64 bytes of the inputs a lane on their way.
+// Units of four groups up to which a warp takes one, so that they spread over the SMs (of a
+// GB300, 32 warps each); with more it has 64 bytes of the inputs a lane on their way.
 constexpr uint32_t kFewUnits = 152 * 32;
 
 template <typename T, int kMode>

@@ -632,11 +632,14 @@ qsfm_status qsfm_update_block_tables(const qsfm_block_table_params* p, void* str
  *   each head row from rope_offset on turned by the angles of positions[t], as
  *   qsfm_norm_rope_store() turns them, or turned back when inverse is set (the
  *   attention's output, whose values carry the keys' rotation).
- * Every code is that of the formula (a gate below -87 counts as silu = 0). Scales
+ * Every code is that of the formula (a gate below -87 counts as silu = 0). Turned
+ * and gated y are taken to about 46 bits, those of its terms when turned: a quotient
+ * nearer than that to the border of two codes may have either. Scales
  * that are not powers of two are the formula's rounded to fp32, or where A is a
  * computed y within a few units of 2^-24 of it: 4 when turned, 11 + 1.25 |gate|
  * when gated. A group with an element y that is not finite has codes and a
- * scale of NaN.
+ * scale of NaN; so has one with a y, or a term of a turned y, above fp32's largest
+ * number.
  *   x, gate    bf16, fp16 or fp32 (in_type) [source_rows, heads, dim], element
  *              strides *_row_stride and *_head_stride, elements contiguous
  *   row_index  int32 [T] or NULL: row t is made of row row_index[t] of x and gate

@@ -156,6 +156,28 @@ def test_numbers_below_the_normal_ones_in_gated_rows(cuda_device):
                 check_quantised(codes, scale, f64(x) * P.silu(f64(gate)), pow2, "gated")
 
 
+def test_computed_elements_above_the_largest_number(cuda_device):
+    """A turned or gated element that fp32 does not hold, and a term of a turned one, make
+    their group NaN, and no other."""
+    def check(codes, scale):
+        clean()
+        assert torch.isnan(scale).tolist() == [[True, False], [False, False]]
+        assert torch.all(codes[0, :128] == 0x7F) and not torch.any(codes[0, 128:] & 0x7F == 0x7F) and not torch.any(codes[1] & 0x7F == 0x7F)
+
+    for factor in (0.8, 1.2):  # a c - b s above the largest number; both terms above it and 0 left
+        x = torch.randn(2, 256, generator=torch.Generator().manual_seed(2))
+        x[0, 64], x[0, 65] = 3e38, -3e38 if factor < 1 else 3e38
+        table = torch.cat((torch.ones(1, 32), torch.zeros(1, 32)), 1)
+        table[0, 0] = table[0, 32] = factor
+        zero = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+        for pow2 in (False, True):
+            check(*Q.quantize_rows(x.to(cuda_device), positions=zero, cos_sin=table.to(cuda_device), rope_offset=64, pow2_scale=pow2))
+    x, gate = torch.randn(2, 256, generator=torch.Generator().manual_seed(3)), torch.ones(2, 256)
+    x[0, 7], gate[0, 7] = -3e38, 20.0
+    for pow2 in (False, True):
+        check(*Q.quantize_rows(x.to(cuda_device), gate=gate.to(cuda_device), pow2_scale=pow2))
+
+
 # ------------------------------------------------------------------ products
 #: rows, columns, K
 SHAPES = [(40, 260, 1040), (5, 130, 128), (300, 10130, 144), (700, 10400, 272), (141, 4993, 3712), (41, 6172, 3488)]

@@ -2,6 +2,8 @@
 stand for tensors of one CUDA device, so that the unchanged block is accepted."""
 
 import ctypes
+import os
+import re
 
 import pytest
 import torch
@@ -172,3 +174,19 @@ def test_sizes_are_limited_by_the_smallest_tiles(lib, rows, n, groups, code):  #
     p = matmul_valid(lib)
     p.rows, p.n, p.groups, p.a = rows, n, groups, None
     assert lib.qsfm_scaled_matmul(ctypes.byref(p), None) == code
+
+
+def test_weights_quantised_as_the_usage_text_does():
+    """The README's function: codes and scales of its 128 x 128 elements, the last ones fewer."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "README.md")).read()
+    names = {"torch": torch}
+    exec(re.search(r"```python\n(def quantised_matrix.*?)```", text, re.S).group(1), names)
+    w = torch.randn(200, 400, generator=torch.Generator().manual_seed(0))
+    w[129, 300] = 50.0
+    codes, scale = names["quantised_matrix"](w.to(BF16))
+    assert codes.shape == (200, 400) and scale.shape == (2, 4) and codes.is_contiguous() and scale.is_contiguous()
+    wide = scale.repeat_interleave(128, 0)[:200].repeat_interleave(128, 1)[:, :400]
+    assert scale[1, 2] == 50.0 / 448 and codes[129, 300].float() == 448
+    # half a step of 3 bits, relative, or of the least step 2^-9, and the division's rounding
+    assert torch.all((codes.float() * wide - w.to(BF16).float()).abs() <= (2.0 ** -4 * w.abs() + 2.0 ** -10 * wide) * (1 + 2.0 ** -7))
