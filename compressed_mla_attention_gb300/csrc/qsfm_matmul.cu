@@ -48,6 +48,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <mutex>
 
@@ -112,7 +113,7 @@ struct MmShape {
   FastDiv block_div;            // by the tiles of kBlockTiles row tiles
   FastDiv high_div[kBlockTiles + 1];  // by the row tiles of a block
   int log_box;     // of the rows of a of a copy
-  int out_boxes;   // the output can be written by copies
+  int out_cols;    // columns of the output that a warp needs in its part to write them by copies
   // of a split tile (no division by the number of parts in the kernel: 100 cycles and more)
   int most;                // chunks of a part at most
   uint8_t first[9];        // the first chunk that part q joins
@@ -551,7 +552,8 @@ __device__ __forceinline__ void store_sums(const qsfm_matmul_params& p, size_t a
 
 // A warp's 32 whole rows of kN columns to the output by copies, which read shared memory
 // while the next tile is added up: boxes of 32 rows x 128 bytes (128-byte swizzle), two at
-// a time. Columns behind the output's are not written.
+// a time. Columns behind the output's are not written where its rows end at 16 bytes: a copy
+// writes 16 bytes at a time, whatever of them lies within the map.
 template <typename T, int kN>
 __device__ __forceinline__ void store_boxes(const CUtensorMap* omap, const float (&v)[kN], int row, int n0, int n,
                                             uint32_t stage) {
@@ -669,7 +671,7 @@ __device__ void mm_sum(const qsfm_matmul_params& p, const MmShape& s, const MmSm
       }
       if (!mm_add<C, true>(s, sm, at, tmem, tempty, buf, tpar, slot, spar, acc, fault)) return;
       if (cols <= 0) continue;
-      if (C::kBoxes && s.out_boxes && rows == 32) {
+      if (C::kBoxes && cols >= s.out_cols && rows == 32) {
         const uint32_t boxes = sm.base + C::kOutAt + C::kOutWarp * warp;
         if (p.out_type == QSFM_BF16) store_boxes<__nv_bfloat16>(omap, acc, t.row0 + row0, n0, p.n, boxes);
         else if (p.out_type == QSFM_F16) store_boxes<__half>(omap, acc, t.row0 + row0, n0, p.n, boxes);
@@ -1013,9 +1015,10 @@ cudaError_t launch_ctas(const qsfm_matmul_params& p, const MmPlan& plan, int row
     return e;
   CUtensorMap omap = amap;  // (not used)
   const int size = p.out_type == QSFM_F32 ? 4 : 2;
-  s.out_boxes = C::kBoxes && s.parts == 1 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 &&
-                (p.rows == 1 || (p.out_row_stride * size) % 16 == 0);
-  if (s.out_boxes && (e = make_out_map(p, size, &omap)) != cudaSuccess) return e;
+  const bool boxes = C::kBoxes && s.parts == 1 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0 &&
+                     (p.rows == 1 || (p.out_row_stride * size) % 16 == 0);
+  s.out_cols = !boxes ? INT_MAX : (p.n * (long long)size) % 16 == 0 ? 1 : C::kSums;
+  if (boxes && (e = make_out_map(p, size, &omap)) != cudaSuccess) return e;
   const long long room = sms / C::kCtas;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(C::kCtas * (s.parts > 1 ? plan.tiles * s.parts : plan.tiles < room ? plan.tiles : room)));

@@ -164,3 +164,42 @@ def test_split_products_repeat_bit_for_bit(cuda_device, case):
         Q.matmul(Q.make_matmul_params(a=a, a_scale=sa, w=w, w_scale=sw, out=out))
     clean()
     assert all(torch.equal(outs[0], out) for out in outs[1:])
+
+
+#: kernel, parts, rows, columns, K, columns before and behind: rows that begin at 16 bytes and
+#: end between two
+RAGGED = [(PAIR, 1, 700, 10403, 272, 8, 5), (PAIR, 1, 144, 11237, 48, 0, 3), (SMALL, 1, 82, 3, 288, 8, 5), (SMALL, 1, 213, 3251, 240, 4, 1),
+          (SMALL, 1, 300, 1999, 272, 16, 1), (WIDE, 1, 265, 9961, 144, 8, 7), (SMALL, 4, 44, 99, 1344, 8, 5), (PAIR, 4, 132, 3131, 5152, 8, 5)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32], ids=str)
+@pytest.mark.parametrize("case", RAGGED, ids=str)
+def test_columns_beside_the_output_stay(cuda_device, case, dtype):
+    tile, parts, m, n, k, before, behind = case
+    a, sa, w, sw = whole_numbers(m, n, k, 1, torch.Generator().manual_seed(n), cuda_device)
+    whole = torch.full((m, before + n + behind), float("nan"), dtype=dtype, device=cuda_device)
+    assert whole.stride(0) * whole.element_size() % 16 == 0 and n * whole.element_size() % 16 != 0
+    out = whole[:, before:before + n]
+    block = Q.make_matmul_params(a=a, a_scale=sa, w=w[0], w_scale=sw[0], out=out)
+    assert Q.debug_matmul_plan(block) == (*tile, parts)
+    Q.matmul(block)
+    clean()
+    assert torch.equal(out, exact(a, sa, w[0], sw[0]).to(dtype))
+    assert torch.isnan(whole[:, :before]).all() and torch.isnan(whole[:, before + n:]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=str)
+def test_columns_beside_grouped_outputs_stay(cuda_device, dtype):
+    dev = cuda_device
+    cu, m = ragged([1500, 0, 3, 1900, 900, 1, 0, 990], 5, 9)
+    n, k = 1099, 400
+    a, sa, w, sw = whole_numbers(m, n, k, len(cu) - 1, torch.Generator().manual_seed(1), dev)
+    whole = torch.full((m, n + 13), 7.0, dtype=dtype, device=dev)
+    Q.matmul(grouped_block(PAIR, a, sa, w, sw, i32(cu, dev), whole[:, 8:8 + n]))
+    clean()
+    want = torch.full_like(whole, 7.0)
+    for g in range(len(cu) - 1):
+        at = slice(cu[g], cu[g + 1])
+        if at.stop > at.start:
+            want[at, 8:8 + n] = exact(a[at], sa[at], w[g], sw[g]).to(dtype)
+    assert torch.equal(whole, want)
